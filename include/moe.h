@@ -83,7 +83,12 @@ typedef enum {
  * without a format; the one taken here is E4M3FN codes (sign, 4-bit exponent
  * with bias 7, 3-bit mantissa, no infinities, S.1111.111 = NaN) with one fp32
  * scale per output feature: w[k][n] = value(code[k][n]) * scale[n]. */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype_t;
+typedef enum {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_FP8_E4M3 = 2,
+  MOE_F16 = 3 /* the stand-alone operators only (moe_linear, moe_swiglu) */
+} moe_dtype_t;
 
 /* Layer configuration.  Field names follow the model's config fields
  * (llm-atlas "Step-3.5-Flash", "Raw config fields").
@@ -453,6 +458,151 @@ int moe_dense_get_device_error(moe_dense_t* layer, int* device_err);
 
 /* Frees the layer (synchronises the device first).  NULL is ignored. */
 void moe_dense_destroy(moe_dense_t* layer);
+
+/* ------------------------------------------------------ stand-alone products
+ * Matrix products on the caller's own weights, for what stands around the
+ * layer (projections, other FFNs, adapters) and for training its experts:
+ *
+ *   z   = x . W + bias                  (groups = 0: W [K, N], bias [N])
+ *   z   = x . W[g] + bias[g]            (groups = G: W [G, K, N], bias [G, N],
+ *                                        for the rows [offsets[g], offsets[g + 1]))
+ *   out = act(z) + residual             preact = z, if asked for
+ *
+ * and the gradients
+ *
+ *   dz = dout * act'(preact)            (act none: dz = dout)
+ *   dx = dz . W^T,   dW = x^T . dz,   dbias = column sums of dz
+ *
+ * per group; the residual's gradient is dout.  Both work on the tensors as
+ * they are: no weights are packed and no transposed copies made, so changing
+ * weights cost nothing.
+ *
+ * Arithmetic: 16-bit operands, products and sums in fp32 on the tensor cores,
+ * bias, activation and residual in fp32, one rounding to the output type.  dz
+ * is rounded to the operand type where it enters the products (not where
+ * dbias sums it); dbias is summed in fp32.  Every sum has a fixed order: the
+ * same call gives the same bits.
+ *
+ * offsets [G + 1] (device, int32) as moe_routing_t's: non-decreasing, within
+ * [0, rows].  Empty groups are allowed: their dW and dbias are zero.  Rows
+ * before offsets[0] and from offsets[G] on belong to no group: their out,
+ * preact and dx are left as they were.  Offsets that break the rule are
+ * clamped into it on the device (no access leaves the tensors; the result is
+ * then not specified).
+ *
+ * Layouts: row-major with a row stride (in elements, >= the row length) for
+ * x, dout, residual, out, preact, dx and W; W also has a stride between
+ * groups.  bias, dW and dbias are contiguous.  16-byte aligned pointers and
+ * row strides that are multiples of 8 elements are read in place; other x, W
+ * and dout are first copied into the workspace (one more pass over them).
+ * out, preact and dx must not overlap x, W or dout; residual may be out
+ * itself (out += ...).  The workspace must not be shared by calls that may
+ * overlap on the GPU. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,     /* z sigmoid(z) */
+  MOE_ACT_GELU = 3,     /* z Phi(z), Phi the normal distribution function */
+  MOE_ACT_GELU_TANH = 4 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+} moe_activation_t;
+
+/* Supported: 0 <= rows <= 2^24; 1 <= in_features, out_features <= 65536;
+ * 0 <= groups <= 1024; dtype BF16 or F16 (F32 and FP8_E4M3 return
+ * MOE_ERR_UNSUPPORTED); strides below 2^31 elements. */
+typedef struct {
+  int rows;         /* rows of x that exist */
+  int in_features;  /* K */
+  int out_features; /* N */
+  int groups;       /* 0: one product; G: grouped rows with offsets */
+  int dtype;        /* moe_dtype_t of every tensor */
+  int activation;   /* moe_activation_t */
+} moe_linear_config_t;
+
+typedef struct {
+  const void* x;          /* [rows, K] */
+  int64_t ld_x;
+  const int32_t* offsets; /* [G + 1], NULL when groups = 0 */
+  const void* w;          /* [K, N] or [G, K, N] */
+  int64_t ld_w;
+  int64_t group_stride_w; /* elements between groups (groups > 1) */
+  const void* bias;       /* [N] or [G, N], or NULL */
+  const void* residual;   /* [rows, N] or NULL */
+  int64_t ld_residual;
+  void* out;              /* [rows, N] */
+  int64_t ld_out;
+  void* preact;           /* [rows, N] or NULL: z, rounded, for the backward pass */
+  int64_t ld_preact;
+} moe_linear_args_t;
+
+typedef struct {
+  const void* dout;       /* [rows, N] */
+  int64_t ld_dout;
+  const void* x;          /* [rows, K]; may be NULL when dw is */
+  int64_t ld_x;
+  const int32_t* offsets;
+  const void* w;          /* as in the forward; may be NULL when dx is */
+  int64_t ld_w;
+  int64_t group_stride_w;
+  const void* preact;     /* [rows, N]; NULL with MOE_ACT_NONE */
+  int64_t ld_preact;
+  void* dx;               /* [rows, K] or NULL */
+  int64_t ld_dx;
+  void* dw;               /* [K, N] or [G, K, N], contiguous, or NULL */
+  void* dbias;            /* [N] or [G, N], or NULL */
+} moe_linear_grads_t;
+
+/* Host-only check of a configuration; no CUDA call. */
+int moe_linear_config_check(const moe_linear_config_t* cfg);
+
+/* Device workspace bytes (0 for aligned operands in the forward; 256-byte
+ * aligned, caller-allocated).  Host-only; checks the arguments as the call
+ * itself does. */
+int moe_linear_workspace_size(const moe_linear_config_t* cfg, const moe_linear_args_t* args,
+                              size_t* bytes);
+int moe_linear_backward_workspace_size(const moe_linear_config_t* cfg,
+                                       const moe_linear_grads_t* grads, size_t* bytes);
+
+/* The product and its gradients, on the current device.  workspace may be
+ * NULL when 0 bytes are needed.  rows = 0 writes only zeros to dw and dbias. */
+int moe_linear(const moe_linear_config_t* cfg, const moe_linear_args_t* args, void* workspace,
+               size_t ws_bytes, void* stream);
+int moe_linear_backward(const moe_linear_config_t* cfg, const moe_linear_grads_t* grads,
+                        void* workspace, size_t ws_bytes, void* stream);
+
+/* As moe_get_device_error, for the current device's status word of the
+ * stand-alone products (one per device, shared by all their calls). */
+int moe_linear_get_device_error(int* device_err);
+
+/* SwiGLU as an operator of its own, the experts' activation:
+ *
+ *   a = min(gate, L), v = clip(up, -L, L)   (L = limit; 0: no clamp)
+ *   out[r] = scale[r] * silu(a) * v         (scale NULL: 1)
+ *
+ * and its gradients: dgate (0 where gate > L), dup (0 where |up| > L) and
+ * dscale[r], the row's sum of dout * silu(a) * v.  With scale the routed
+ * pairs' gate weights, (scale * h) . W_down is the layer's weighted expert
+ * row, and dscale its gate weight's gradient.
+ * gate, up, dout, out, dgate, dup: [rows, width] in dtype, each with a row
+ * stride; scale, dscale: [rows] fp32.  All arithmetic in fp32, one rounding.
+ * offsets [groups + 1] as for moe_linear, or NULL (groups 0): rows outside
+ * [offsets[0], offsets[groups]) are left as they were.  out may be gate or up
+ * itself, and dgate / dup may be gate / up / dout (the same rows and stride);
+ * other overlaps are not allowed. */
+typedef struct {
+  int rows;    /* 0 <= rows <= 2^24 */
+  int width;   /* 1 <= width <= 65536 */
+  int groups;  /* 0, or the groups of offsets (<= 1024) */
+  int dtype;   /* F32, BF16 or F16 */
+  float limit; /* finite, >= 0 */
+} moe_swiglu_config_t;
+
+int moe_swiglu(const moe_swiglu_config_t* cfg, const void* gate, int64_t ld_gate, const void* up,
+               int64_t ld_up, const float* scale, const int32_t* offsets, void* out,
+               int64_t ld_out, void* stream);
+int moe_swiglu_backward(const moe_swiglu_config_t* cfg, const void* dout, int64_t ld_dout,
+                        const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                        const float* scale, const int32_t* offsets, void* dgate, int64_t ld_dgate,
+                        void* dup, int64_t ld_dup, float* dscale, void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,7 @@ MOE_ERR_NOT_LOADED = 6
 MOE_F32 = 0
 MOE_BF16 = 1
 MOE_FP8_E4M3 = 2
+MOE_F16 = 3
 MOE_PATH_AUTO = 0
 MOE_PATH_MULTI = 1
 MOE_PATH_FUSED = 2
@@ -41,7 +42,9 @@ EXPORTS = (
     "moe_dense_workspace_size", "moe_dense_forward", "moe_dense_get_device_error",
     "moe_dense_destroy", "moe_create_shard", "moe_set_path", "moe_forward_path",
     "moe_check_fused_timeout", "moe_load_shard_weights", "moe_forward_host_async",
-    "moe_forward_host_join",
+    "moe_forward_host_join", "moe_linear_config_check", "moe_linear_workspace_size",
+    "moe_linear_backward_workspace_size", "moe_linear", "moe_linear_backward",
+    "moe_linear_get_device_error", "moe_swiglu", "moe_swiglu_backward",
 )
 MOE_NUM_STAGES = 7
 STAGE_NAMES = ("router", "topk", "sort", "gather", "gate_up", "down", "combine")
@@ -71,6 +74,64 @@ class moe_dense_config_t(ctypes.Structure):
         ("swiglu_limit", ctypes.c_float),
         ("act_dtype", ctypes.c_int),
         ("weight_dtype", ctypes.c_int),
+    ]
+
+
+class moe_linear_config_t(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int),
+        ("in_features", ctypes.c_int),
+        ("out_features", ctypes.c_int),
+        ("groups", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("activation", ctypes.c_int),
+    ]
+
+
+class moe_linear_args_t(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64),
+        ("offsets", ctypes.c_void_p),
+        ("w", ctypes.c_void_p),
+        ("ld_w", ctypes.c_int64),
+        ("group_stride_w", ctypes.c_int64),
+        ("bias", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("ld_residual", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("preact", ctypes.c_void_p),
+        ("ld_preact", ctypes.c_int64),
+    ]
+
+
+class moe_linear_grads_t(ctypes.Structure):
+    _fields_ = [
+        ("dout", ctypes.c_void_p),
+        ("ld_dout", ctypes.c_int64),
+        ("x", ctypes.c_void_p),
+        ("ld_x", ctypes.c_int64),
+        ("offsets", ctypes.c_void_p),
+        ("w", ctypes.c_void_p),
+        ("ld_w", ctypes.c_int64),
+        ("group_stride_w", ctypes.c_int64),
+        ("preact", ctypes.c_void_p),
+        ("ld_preact", ctypes.c_int64),
+        ("dx", ctypes.c_void_p),
+        ("ld_dx", ctypes.c_int64),
+        ("dw", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p),
+    ]
+
+
+class moe_swiglu_config_t(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int),
+        ("width", ctypes.c_int),
+        ("groups", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("limit", ctypes.c_float),
     ]
 
 
@@ -142,6 +203,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_set_path.argtypes = [vp, i]
     lib.moe_check_fused_timeout.argtypes = [vp, vp, i, vp, vp, sz, i, ctypes.POINTER(i)]
     lib.moe_forward_path.argtypes = [vp, i]
+    lc, la, lg = (ctypes.POINTER(t) for t in
+                  (moe_linear_config_t, moe_linear_args_t, moe_linear_grads_t))
+    i64 = ctypes.c_int64
+    lib.moe_linear_config_check.argtypes = [lc]
+    lib.moe_linear_workspace_size.argtypes = [lc, la, ctypes.POINTER(sz)]
+    lib.moe_linear_backward_workspace_size.argtypes = [lc, lg, ctypes.POINTER(sz)]
+    lib.moe_linear.argtypes = [lc, la, vp, sz, vp]
+    lib.moe_linear_backward.argtypes = [lc, lg, vp, sz, vp]
+    lib.moe_linear_get_device_error.argtypes = [ctypes.POINTER(i)]
+    sc = ctypes.POINTER(moe_swiglu_config_t)
+    lib.moe_swiglu.argtypes = [sc, vp, i64, vp, i64, vp, vp, vp, i64, vp]
+    lib.moe_swiglu_backward.argtypes = [sc, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,
+                                        vp, vp]
     for name in EXPORTS:
         if name not in ("moe_status_string", "moe_destroy", "moe_dense_destroy"):
             getattr(lib, name).restype = ctypes.c_int
@@ -641,3 +715,287 @@ class DenseMLP:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------- stand-alone products and SwiGLU
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # moe_activation_t
+_OP_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+
+
+class _Launch:
+    """Makes a tensor's device (and the caller's stream, if given) current, so
+    that what a call allocates belongs to the stream that it runs on."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self._ctx = []
+        dev = t.device
+        if dev.type != "cuda":
+            raise ValueError(f"want tensors on a CUDA device, got {dev}")
+        if dev.index != torch.cuda.current_device():
+            self._ctx.append(torch.cuda.device(dev))
+        if stream is not None:
+            s = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(int(stream), device=dev)
+            if s.device != dev:
+                raise ValueError(f"stream on {s.device}, tensors on {dev}")
+            self._ctx.append(torch.cuda.stream(s))
+        self.device = dev
+
+    def __enter__(self):
+        for c in self._ctx:
+            c.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self._ctx):
+            c.__exit__(*exc)
+
+
+def _need_rows(t: torch.Tensor, name: str, like: torch.Tensor, rows: int, cols: int) -> int:
+    """Checks a [rows, cols] tensor of like's type and device with contiguous
+    rows; returns its row stride."""
+    if t.shape != (rows, cols) or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name}: want {like.dtype} {(rows, cols)} on {like.device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: want rows of contiguous elements, got strides {t.stride()}")
+    if rows <= 1:
+        return (cols + 7) // 8 * 8  # one row has no stride: take an aligned one
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return t.stride(0)
+
+
+def _need_vec(t: torch.Tensor, name: str, like: torch.Tensor, shape, dtype=None):
+    dtype = like.dtype if dtype is None else dtype
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {like.device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _product_setup(x_or_dout, w, offsets, cols_dim, activation, name):
+    """Shared checks of the products: the configuration and W's strides."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation: want one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    t = x_or_dout
+    grouped = offsets is not None
+    if t.dim() != 2:
+        raise ValueError(f"{name}: want [rows, features], got {tuple(t.shape)}")
+    if w.dim() != (3 if grouped else 2) or w.dtype != t.dtype or w.device != t.device:
+        raise ValueError(f"w: want {t.dtype} {'[G, K, N]' if grouped else '[K, N]'} on {t.device}, "
+                         f"got {w.dtype} {tuple(w.shape)} on {w.device}")
+    K, N = w.shape[-2], w.shape[-1]
+    if t.shape[1] != (K, N)[cols_dim]:
+        raise ValueError(f"{name}: want {(K, N)[cols_dim]} features, got {t.shape[1]}")
+    if N > 1 and w.stride(-1) != 1:
+        raise ValueError(f"w: want rows of contiguous elements, got strides {w.stride()}")
+    ld = (N + 7) // 8 * 8 if K <= 1 else w.stride(-2)
+    gs = 0
+    G = 0
+    if grouped:
+        G = w.shape[0]
+        if G < 1:
+            raise ValueError("w: want at least one group")
+        gs = (K - 1) * ld + N if G == 1 else w.stride(0)
+        _need_vec(offsets, "offsets", t, (G + 1,), torch.int32)
+    if ld < N or (G > 1 and gs < (K - 1) * ld + N):
+        raise ValueError(f"w: rows or groups overlap (strides {w.stride()})")
+    if t.dtype not in _OP_DTYPES:
+        raise ValueError(f"{name}: unsupported type {t.dtype}")
+    cfg = moe_linear_config_t(t.shape[0], K, N, G, _OP_DTYPES[t.dtype], ACTIVATIONS[activation])
+    return cfg, K, N, G, ld, gs
+
+
+def _workspace(n: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _linear(x, offsets, w, bias, residual, activation, out, preact, stream):
+    lib = load_library()
+    cfg, K, N, G, ld_w, gs = _product_setup(x, w, offsets, 0, activation, "x")
+    R = x.shape[0]
+    ld_x = _need_rows(x, "x", x, R, K)
+    if bias is not None:
+        _need_vec(bias, "bias", x, (G, N) if G else (N,))
+    ld_res = _need_rows(residual, "residual", x, R, N) if residual is not None else 0
+    ld_pre = _need_rows(preact, "preact", x, R, N) if preact is not None else 0
+    with _Launch(x, stream) as st:
+        if out is None:
+            out = torch.empty(R, N, dtype=x.dtype, device=x.device)
+        ld_out = _need_rows(out, "out", x, R, N)
+        args = moe_linear_args_t(x.data_ptr(), ld_x, _ptr(offsets), w.data_ptr(), ld_w, gs,
+                                 _ptr(bias), _ptr(residual), ld_res, out.data_ptr(), ld_out,
+                                 _ptr(preact), ld_pre)
+        n = ctypes.c_size_t()
+        _check(lib.moe_linear_workspace_size(ctypes.byref(cfg), ctypes.byref(args),
+                                             ctypes.byref(n)), "moe_linear")
+        ws = _workspace(n.value, x.device)
+        _check(lib.moe_linear(ctypes.byref(cfg), ctypes.byref(args), _ptr(ws), n.value, st),
+               "moe_linear")
+    return out
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+           residual: Optional[torch.Tensor] = None, activation: str = "none",
+           out: Optional[torch.Tensor] = None, preact: Optional[torch.Tensor] = None,
+           stream=None) -> torch.Tensor:
+    """act(x . w + bias) + residual (moe_linear): x [R, K], w [K, N], bias [N],
+    residual and out [R, N], bf16 or fp16.  preact [R, N], if given, receives
+    x . w + bias for linear_backward.  residual may be out itself.  Rows may
+    have any stride; misaligned operands are copied first."""
+    return _linear(x, None, w, bias, residual, activation, out, preact, stream)
+
+
+def grouped_linear(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, *,
+                   residual: Optional[torch.Tensor] = None, activation: str = "none",
+                   out: Optional[torch.Tensor] = None, preact: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """linear with the weights of each row's group: rows [offsets[g],
+    offsets[g + 1]) of x meet w[g] (w [G, K, N], bias [G, N], offsets [G + 1]
+    int32 on the device, as the layer's routing returns them).  Rows of no
+    group are not written: their values in a new out are undefined."""
+    if offsets is None:
+        raise ValueError("offsets: want an int32 tensor [G + 1]")
+    return _linear(x, offsets, w, bias, residual, activation, out, preact, stream)
+
+
+def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream):
+    lib = load_library()
+    cfg, K, N, G, ld_w, gs = _product_setup(dout, w, offsets, 1, activation, "dout")
+    R = dout.shape[0]
+    ld_dout = _need_rows(dout, "dout", dout, R, N)
+    if x is not None:
+        ld_x = _need_rows(x, "x", dout, R, K)
+    elif need[1]:
+        raise ValueError("x: needed for dw")
+    else:
+        ld_x = 0
+    if (activation == "none") != (preact is None):
+        raise ValueError("preact: wanted exactly when there is an activation")
+    ld_pre = _need_rows(preact, "preact", dout, R, N) if preact is not None else 0
+    dx, dw, db = into
+    with _Launch(dout, stream) as st:
+        if need[0] and dx is None:
+            dx = torch.empty(R, K, dtype=dout.dtype, device=dout.device)
+        if need[1] and dw is None:
+            dw = torch.empty(w.shape, dtype=dout.dtype, device=dout.device)
+        if need[2] and db is None:
+            db = torch.empty((G, N) if G else (N,), dtype=dout.dtype, device=dout.device)
+        dx, dw, db = (t if n else None for t, n in zip((dx, dw, db), need))
+        ld_dx = _need_rows(dx, "dx", dout, R, K) if dx is not None else 0
+        if dw is not None:
+            _need_vec(dw, "dw", dout, w.shape)
+        if db is not None:
+            _need_vec(db, "db", dout, (G, N) if G else (N,))
+        grads = moe_linear_grads_t(dout.data_ptr(), ld_dout, _ptr(x) if need[1] else None, ld_x,
+                                   _ptr(offsets), w.data_ptr() if need[0] else None, ld_w, gs,
+                                   _ptr(preact), ld_pre, _ptr(dx), ld_dx, _ptr(dw), _ptr(db))
+        n = ctypes.c_size_t()
+        _check(lib.moe_linear_backward_workspace_size(ctypes.byref(cfg), ctypes.byref(grads),
+                                                      ctypes.byref(n)), "moe_linear_backward")
+        ws = _workspace(n.value, dout.device)
+        _check(lib.moe_linear_backward(ctypes.byref(cfg), ctypes.byref(grads), _ptr(ws), n.value,
+                                       st), "moe_linear_backward")
+    return dx, dw, db
+
+
+def linear_backward(dout: torch.Tensor, x: Optional[torch.Tensor], w: torch.Tensor, *,
+                    preact: Optional[torch.Tensor] = None, activation: str = "none",
+                    need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                    dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                    db: Optional[torch.Tensor] = None, stream=None):
+    """(dx, dw, db) of linear (moe_linear_backward), None where not needed:
+    dz = dout * act'(preact), dx = dz . w^T, dw = x^T . dz, db = column sums.
+    preact is what the forward pass kept; the residual's gradient is dout."""
+    return _linear_backward(dout, x, None, w, preact, activation, (need_dx, need_dw, need_db),
+                            (dx, dw, db), stream)
+
+
+def grouped_linear_backward(dout: torch.Tensor, x: Optional[torch.Tensor],
+                            offsets: torch.Tensor, w: torch.Tensor, *,
+                            preact: Optional[torch.Tensor] = None, activation: str = "none",
+                            need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                            dx: Optional[torch.Tensor] = None,
+                            dw: Optional[torch.Tensor] = None,
+                            db: Optional[torch.Tensor] = None, stream=None):
+    """(dx, dw, db) of grouped_linear: dw [G, K, N] and db [G, N] are zero for
+    empty groups; dx rows of no group are not written."""
+    if offsets is None:
+        raise ValueError("offsets: want an int32 tensor [G + 1]")
+    return _linear_backward(dout, x, offsets, w, preact, activation, (need_dx, need_dw, need_db),
+                            (dx, dw, db), stream)
+
+
+def linear_device_error(device=None) -> int:
+    """Synchronises the device, then reads and clears its products' status
+    word (0: no bounded wait gave up)."""
+    v = ctypes.c_int()
+    with torch.cuda.device(device):
+        load_library().moe_linear_get_device_error(ctypes.byref(v))
+    return v.value
+
+
+def _swiglu_setup(gate, up, scale, limit, offsets):
+    if gate.dim() != 2 or gate.dtype not in _OP_DTYPES:
+        raise ValueError(f"gate: want [rows, width] in fp32, bf16 or fp16, got {gate.dtype} "
+                         f"{tuple(gate.shape)}")
+    R, W = gate.shape
+    lds = _need_rows(gate, "gate", gate, R, W), _need_rows(up, "up", gate, R, W)
+    if scale is not None:
+        _need_vec(scale, "scale", gate, (R,), torch.float32)
+    G = 0
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 2:
+            raise ValueError(f"offsets: want [G + 1], got {tuple(offsets.shape)}")
+        G = offsets.numel() - 1
+        _need_vec(offsets, "offsets", gate, (G + 1,), torch.int32)
+    return moe_swiglu_config_t(R, W, G, _OP_DTYPES[gate.dtype], float(limit)), R, W, lds
+
+
+def swiglu(gate: torch.Tensor, up: torch.Tensor, scale: Optional[torch.Tensor] = None, *,
+           limit: float = 0.0, offsets: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """scale * silu(min(gate, limit)) * clip(up, -limit, limit) (moe_swiglu;
+    limit 0: no clamp): gate, up, out [R, W] with any row stride (the halves of
+    one [R, 2W] tensor, say), fp32, bf16 or fp16; scale [R] fp32.  offsets:
+    rows outside [offsets[0], offsets[-1]) are not written."""
+    lib = load_library()
+    cfg, R, W, (ldg, ldu) = _swiglu_setup(gate, up, scale, limit, offsets)
+    with _Launch(gate, stream) as st:
+        if out is None:
+            out = torch.empty(R, W, dtype=gate.dtype, device=gate.device)
+        ldo = _need_rows(out, "out", gate, R, W)
+        _check(lib.moe_swiglu(ctypes.byref(cfg), gate.data_ptr(), ldg, up.data_ptr(), ldu,
+                              _ptr(scale), _ptr(offsets), out.data_ptr(), ldo, st), "moe_swiglu")
+    return out
+
+
+def swiglu_backward(dout: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                    scale: Optional[torch.Tensor] = None, *, limit: float = 0.0,
+                    offsets: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                    dup: Optional[torch.Tensor] = None, dscale: Optional[torch.Tensor] = None,
+                    stream=None):
+    """(dgate, dup, dscale) of swiglu (moe_swiglu_backward); dscale [R] fp32 is
+    None without scale.  dgate and dup may be gate, up or dout themselves."""
+    lib = load_library()
+    cfg, R, W, (ldg, ldu) = _swiglu_setup(gate, up, scale, limit, offsets)
+    ldd = _need_rows(dout, "dout", gate, R, W)
+    if dscale is not None and scale is None:
+        raise ValueError("dscale: there is no scale")
+    with _Launch(gate, stream) as st:
+        if dgate is None:
+            dgate = torch.empty(R, W, dtype=gate.dtype, device=gate.device)
+        if dup is None:
+            dup = torch.empty(R, W, dtype=gate.dtype, device=gate.device)
+        if dscale is None and scale is not None:
+            dscale = torch.empty(R, dtype=torch.float32, device=gate.device)
+        if dscale is not None:
+            _need_vec(dscale, "dscale", gate, (R,), torch.float32)
+        ldg2, ldu2 = _need_rows(dgate, "dgate", gate, R, W), _need_rows(dup, "dup", gate, R, W)
+        _check(lib.moe_swiglu_backward(ctypes.byref(cfg), dout.data_ptr(), ldd, gate.data_ptr(),
+                                       ldg, up.data_ptr(), ldu, _ptr(scale), _ptr(offsets),
+                                       dgate.data_ptr(), ldg2, dup.data_ptr(), ldu2, _ptr(dscale),
+                                       st), "moe_swiglu_backward")
+    return dgate, dup, dscale

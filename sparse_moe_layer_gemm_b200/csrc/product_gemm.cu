@@ -1,0 +1,512 @@
+// The stand-alone products on one-CTA tiles (see products.h for the three
+// forms): 128 features x up to 128 rows per tile, tcgen05 MMAs into tensor
+// memory, TMA-fed slots of 64 contraction steps.
+//
+// Operands come straight from the caller's tensors.  A tile whose contraction
+// index is contiguous in memory is K-major (rows of 128 swizzled bytes); one
+// whose feature / row index is contiguous is MN-major: boxes of 64 elements x
+// 64 contraction steps, 1024-byte groups of 8 steps (stride offset) and 8 KB
+// from one 64-element chunk to the next (leading offset).  So W [K, N] serves
+// the forward and dx, and x and dz the weight gradient, with no transposed
+// copies.
+//
+// Few tiles (a decode batch): `split` CTAs of a cluster share a tile, each
+// taking a part of its contraction.  The parts meet in shared memory over the
+// cluster: the rows of the tile are dealt out to the CTAs, every CTA sends
+// its fp32 partial of a row to the row's owner, and the owner adds them in
+// rank order (the same sum on every run; no workspace, no counters) and
+// finishes the row.
+//
+// Roles per CTA (6 warps): warp 0 TMA producer, warp 1 tensor memory and MMA
+// issue, warps 2-5 epilogue (one accumulator lane quadrant each).  Persistent
+// over tiles w = cluster, cluster + clusters, ...; the accumulator is
+// double-buffered.  Every wait is bounded (moe_ptx.cuh).
+//
+// Weight gradient: the contraction runs over the group's rows, which end
+// inside a slot; the rows behind the last one belong to the next group.  The
+// issuing warp clears them in shared memory (both operands: 0 x NaN is NaN)
+// up to the MMA's 16 steps before it issues that slot.
+#include <algorithm>
+
+#include "moe_internal.h"
+#include "product_device.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace product;
+
+constexpr int kThreads = 32 * 6;
+constexpr int kSubBytes = 64 * 128;  // one MN-major box: 64 steps x 64 elements
+constexpr int kABytes = 2 * kSubBytes;
+constexpr int kMaxStages = 12;
+constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
+
+// bytes of the B operand of one slot
+__host__ __device__ constexpr int b_bytes(int mode, int bn) {
+  return mode == kProductDw ? (bn + 63) / 64 * kSubBytes : bn * 128;
+}
+
+// fp32 partials received for this CTA's share of a tile's rows
+__host__ __device__ constexpr int exchange_bytes(int split, int bn) {
+  return split > 1 ? split * ((bn + split - 1) / split) * kProductBM * 4 : 0;
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait with cluster scope: what the arriving CTAs wrote here is visible.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort, int* status) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicOr(status, kDevErrTimeout);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Shared-memory matrix descriptor of an MN-major operand with the 128-byte
+// swizzle: 64-element chunks 8 KB apart (leading byte offset), groups of 8
+// contraction steps 1 KB apart (stride byte offset), descriptor version 1,
+// layout type 2.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kSubBytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Instruction descriptor of kind::f16 with 128 x n accumulators in fp32.
+__device__ __forceinline__ uint32_t product_idesc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
+         ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+struct Tile {
+  int g;        // group
+  int f0;       // first feature
+  int j0;       // first row of the tile: of the tensor (forward, dx) or of the group's output (dw)
+  int n_valid;  // rows of the tile
+  int c0;       // first contraction index (dw: row of the tensor)
+  int depth;    // contraction length
+};
+
+// Row blocks per ordering chunk: inside a group, chunks of 4 row blocks run
+// feature-major, so a weight tile's readers follow one another and the
+// chunk's rows stay in L2 across its weight tiles.
+constexpr int kChunk = 4;
+
+template <int MODE>
+__device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable& t, int w) {
+  Tile r;
+  const int f_tiles = (p.feats + kProductBM - 1) / kProductBM;
+  int local, blocks, in_chunk_first;
+  if (MODE == kProductDw) {
+    blocks = (p.cols + p.bn - 1) / p.bn;
+    const int per_group = f_tiles * blocks;
+    r.g = w / per_group;
+    local = w - r.g * per_group;
+  } else {
+    // tiles before group g: block_start[g] * f_tiles
+    const int b = w / f_tiles;
+    r.g = group_of_block(t, p.groups, b);
+    local = w - t.block_start[r.g] * f_tiles;
+    blocks = t.block_start[r.g + 1] - t.block_start[r.g];
+  }
+  const int per_chunk = f_tiles * kChunk;
+  const int c = local / per_chunk;
+  const int rem = local - c * per_chunk;
+  in_chunk_first = c * kChunk;
+  const int in_chunk = min(kChunk, blocks - in_chunk_first);
+  const int ft = rem / in_chunk;
+  const int nb = in_chunk_first + (rem - ft * in_chunk);
+  r.f0 = ft * kProductBM;
+  if (MODE == kProductDw) {
+    r.j0 = nb * p.bn;
+    r.n_valid = min(p.bn, p.cols - r.j0);
+    r.c0 = t.row0[r.g];
+    r.depth = t.count(r.g);
+  } else {
+    r.j0 = t.row0[r.g] + nb * p.bn;
+    r.n_valid = min(p.bn, t.count(r.g) - nb * p.bn);
+    r.c0 = 0;
+    r.depth = p.depth;
+  }
+  return r;
+}
+
+template <int MODE, typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+    product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const ProductParams p) {
+  constexpr bool kAMn = MODE != kProductDx;
+  constexpr bool kBMn = MODE == kProductDw;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int stages = p.stages;
+  const int slot_bytes = kABytes + b_bytes(MODE, p.bn);
+  float* xch = reinterpret_cast<float*>(smem + stages * slot_bytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xch) +
+                                               exchange_bytes(p.split, p.bn));
+  const uint32_t full0 = smem_u32(bars);
+  const uint32_t empty0 = full0 + 8 * kMaxStages;
+  const uint32_t tfull0 = empty0 + 8 * kMaxStages;
+  const uint32_t tempty0 = tfull0 + 16;
+  const uint32_t drain = tempty0 + 16;
+  const uint32_t xfull = drain + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* tab_mem = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int split = p.split;
+  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cluster = blockIdx.x / split;
+  const int clusters = gridDim.x / split;
+  // accumulator columns, two buffers (a power of two, at least 32)
+  uint32_t acc_cols = 16;
+  while (acc_cols < static_cast<uint32_t>(p.bn)) acc_cols <<= 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 4);
+    }
+    mbar_init(drain, 1);
+    mbar_init(xfull, 4 * split);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 2 * acc_cols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, p.bn);
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync_all();  // every CTA's barriers are ready before remote use
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int f_tiles = (p.feats + kProductBM - 1) / kProductBM;
+  const int total = MODE == kProductDw
+                        ? p.groups * f_tiles * ((p.cols + p.bn - 1) / p.bn)
+                        : tab.block_start[p.groups] * f_tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      uint32_t it = 0;
+      bool ok = true;
+      for (int w = cluster; w < total && ok; w += clusters) {
+        const Tile t = decode<MODE>(p, tab, w);
+        const int nkb = (t.depth + 63) >> 6;
+        const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
+        for (int kb = static_cast<int>(static_cast<int64_t>(nkb) * rank / split); kb < kb1; ++kb) {
+          const uint32_t s = it % stages;
+          const uint32_t ph = (it / stages) & 1u;
+          if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = full0 + 8 * s;
+          mbar_arrive_expect_tx(bar, slot_bytes);
+          const uint32_t sa = smem_u32(smem + s * slot_bytes);
+          const uint32_t sb = sa + kABytes;
+          const int c = t.c0 + kb * 64;
+          if (MODE == kProductForward) {
+            tma_load_3d(sa, &tmA, bar, t.f0, c, t.g, pol);
+            tma_load_3d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, t.g, pol);
+          } else if (MODE == kProductDx) {
+            tma_load_3d(sa, &tmA, bar, c, t.f0, t.g, pol);
+          } else {
+            tma_load_2d(sa, &tmA, bar, t.f0, c, pol);
+            tma_load_2d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, pol);
+          }
+          if (kBMn) {
+            for (int h = 0; h < p.bn; h += 64)
+              tma_load_2d(sb + h * 128, &tmB, bar, t.j0 + h, c, pol);
+          } else {
+            tma_load_2d(sb, &tmB, bar, c, t.j0, pol);
+          }
+          ++it;
+        }
+      }
+      // every load issued lands before the CTA can end
+      const uint32_t used = it < static_cast<uint32_t>(stages) ? it : stages;
+      for (uint32_t s = 0; s < used; ++s) {
+        const uint32_t last = (it - 1u) - ((it - 1u - s) % stages);
+        mbar_wait(full0 + 8 * s, (last / stages) & 1u, nullptr, p.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr bool kIsBf16 = sizeof(T) == 2 && !__is_same(T, __half);
+    uint32_t it = 0, tc = 0;
+    bool ok = true;
+    for (int w = cluster; w < total && ok; w += clusters) {
+      const Tile t = decode<MODE>(p, tab, w);
+      const int nkb = (t.depth + 63) >> 6;
+      const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / split);
+      const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
+      if (kb0 == kb1) continue;  // nothing to add: the epilogue takes zeros
+      const uint32_t idesc =
+          product_idesc(kIsBf16, kAMn, kBMn, kProductBM, (t.n_valid + 15) & ~15);
+      const uint32_t buf = tc & 1u;
+      int go = 1;
+      if (lane == 0)
+        go = mbar_wait(tempty0 + 8 * buf, ((tc >> 1) & 1u) ^ 1u, abort_flag, p.status) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + buf * acc_cols;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t s = it % stages;
+        if (lane == 0)
+          go = mbar_wait(full0 + 8 * s, (it / stages) & 1u, abort_flag, p.status) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, go, 0)) {
+          ok = false;
+          break;
+        }
+        uint8_t* slot = smem + s * slot_bytes;
+        const int left = t.depth - kb * 64;  // contraction steps that exist from here on
+        const int steps = min(4, (left + 15) >> 4);
+        if (MODE == kProductDw && (left & 15) != 0 && left < 64) {
+          // steps [left, steps * 16) are another group's rows: clear them in every box
+          const int n16 = (steps * 16 - left) * 8;  // 16-byte pieces per box
+          const int boxes = slot_bytes / kSubBytes;
+          for (int i = lane; i < n16 * boxes; i += 32) {
+            const int box = i / n16;
+            *reinterpret_cast<uint4*>(slot + box * kSubBytes + left * 128 + (i - box * n16) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t sa = smem_u32(slot);
+          const uint64_t ad = kAMn ? sdesc_mn_sw128(sa) : sdesc_k_sw<128>(sa);
+          const uint64_t bd = kBMn ? sdesc_mn_sw128(sa + kABytes) : sdesc_k_sw<128>(sa + kABytes);
+          constexpr uint64_t kStepA = (kAMn ? 2048 : 32) >> 4;
+          constexpr uint64_t kStepB = (kBMn ? 2048 : 32) >> 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < steps)
+              tc_mma_bf16(d, ad + i * kStepA, bd + i * kStepB, idesc, (kb > kb0 || i > 0) ? 1u : 0u);
+          tc_commit(empty0 + 8 * s);
+          if (kb == kb1 - 1) tc_commit(tfull0 + 8 * buf);
+        }
+        __syncwarp();
+        ++it;
+      }
+      ++tc;
+    }
+    if (lane == 0 && it > 0) {  // no MMA may still be writing TMEM at deallocation
+      tc_commit(drain);
+      mbar_wait(drain, 0, nullptr, p.status);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // the TMEM lane quadrant this warp may read
+    uint32_t tc = 0;
+    const T* bias = static_cast<const T*>(p.bias);
+    const T* residual = static_cast<const T*>(p.residual);
+    T* preact = static_cast<T*>(p.preact);
+    for (int w = cluster; w < total; w += clusters) {
+      const Tile t = decode<MODE>(p, tab, w);
+      const int nkb = (t.depth + 63) >> 6;
+      const bool empty = static_cast<int64_t>(nkb) * rank / split ==
+                         static_cast<int64_t>(nkb) * (rank + 1) / split;
+      const uint32_t buf = tc & 1u;
+      const int feat = t.f0 + q * 32 + lane;
+      const bool live = feat < p.feats;
+      const int64_t row0 = MODE == kProductDw
+                               ? static_cast<int64_t>(t.g) * p.cols + t.j0
+                               : static_cast<int64_t>(t.j0);
+      const float b = (MODE == kProductForward && bias != nullptr && live)
+                          ? to_f32<T>(bias[static_cast<int64_t>(t.g) * p.feats + feat])
+                          : 0.f;
+      T* out = static_cast<T*>(p.out) + row0 * p.ld_out + feat;
+      // one finished value: forward adds the bias, keeps z if asked, applies
+      // the activation, adds the residual; rounded once to the output type
+      auto finish = [&](int j, float v) {
+        if (MODE == kProductForward) {
+          v += b;
+          if (preact != nullptr) preact[(row0 + j) * p.ld_preact + feat] = from_f32<T>(v);
+          v = activate(v, p.act);
+          if (residual != nullptr) v += to_f32<T>(residual[(row0 + j) * p.ld_residual + feat]);
+        }
+        out[static_cast<int64_t>(j) * p.ld_out] = from_f32<T>(v);
+      };
+      if (!empty) {
+        int go = 1;
+        if (lane == 0)
+          go = mbar_wait(tfull0 + 8 * buf, (tc >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        tc_fence_after();
+      }
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
+      const int share = (t.n_valid + split - 1) / split;  // rows each CTA of the cluster finishes
+      const uint32_t xch_addr = smem_u32(xch) + (q * 32 + lane) * 4;
+      for (int c = 0; c < t.n_valid; c += 16) {
+        uint32_t r[16];
+        if (empty) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = 0;
+        } else {
+          tmem_ld_x16(taddr + c, r);
+          tmem_ld_wait();
+        }
+        if (split == 1) {
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c + i < t.n_valid) finish(c + i, __uint_as_float(r[i]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i < t.n_valid) {
+              const int owner = (c + i) / share;
+              const uint32_t at =
+                  xch_addr + (rank * share + (c + i) - owner * share) * (kProductBM * 4);
+              st_cluster_f32(mapa_shared(at, owner), __uint_as_float(r[i]));
+            }
+        }
+      }
+      if (!empty) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty0 + 8 * buf);
+        ++tc;
+      }
+      if (split > 1) {
+        // one tile per cluster in this form (the launch has a cluster per
+        // tile), so the exchange area is written once
+        __syncwarp();
+        if (lane < split) mbar_arrive_cluster(mapa_shared(xfull, lane));
+        int go = 1;
+        if (lane == 0) go = mbar_wait_cluster(xfull, 0, abort_flag, p.status) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        // the waiting lane's acquire orders the other lanes' reads too
+        __syncwarp();
+        const int mine = min(share, t.n_valid - rank * share);
+        for (int j = 0; j < mine; ++j) {
+          float v = 0.f;
+          for (int s = 0; s < split; ++s)
+            v += xch[(s * share + j) * kProductBM + q * 32 + lane];
+          if (live) finish(rank * share + j, v);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync_all();  // no CTA leaves while its peers may still reach it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 2 * acc_cols);
+  }
+}
+
+template <int MODE, typename T>
+cudaError_t launch(const ProductMaps& m, const ProductParams& p, size_t smem, int grid,
+                   cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(product_kernel<MODE, T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, product_kernel<MODE, T>, m.a, m.b, p);
+}
+
+}  // namespace
+
+size_t product_slot_bytes(int mode, int bn) {
+  return static_cast<size_t>(kABytes) + b_bytes(mode, bn);
+}
+
+cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p0,
+                           int num_sms, cudaStream_t st) {
+  ProductParams p = p0;
+  const size_t fixed = 1024 + exchange_bytes(p.split, p.bn) + kBarBytes +
+                       static_cast<size_t>(group_table_bytes(p.groups));
+  const size_t slot = product_slot_bytes(mode, p.bn);
+  const int64_t f_tiles = (p.feats + kProductBM - 1) / kProductBM;
+  // the most tiles the launch can have (a ragged problem's count is known on the device only)
+  int64_t tiles;
+  if (mode == kProductDw) {
+    tiles = p.groups * f_tiles * ((p.cols + p.bn - 1) / p.bn);
+  } else {
+    const int64_t blocks = p.offsets == nullptr
+                               ? (p.rows + p.bn - 1) / p.bn
+                               : std::min<int64_t>(p.rows, p.rows / p.bn + p.groups);
+    tiles = blocks * f_tiles;
+  }
+  if (tiles <= 0) return cudaSuccess;
+  if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
+  p.stages = static_cast<int>(
+      std::min<size_t>(kMaxStages, (static_cast<size_t>(227) * 1024 - fixed) / slot));
+  const size_t smem = fixed + p.stages * slot;
+  const int grid =
+      p.split > 1 ? static_cast<int>(tiles) * p.split : static_cast<int>(std::min<int64_t>(tiles, num_sms));
+  if (bf16) {
+    if (mode == kProductForward) return launch<kProductForward, __nv_bfloat16>(m, p, smem, grid, st);
+    if (mode == kProductDx) return launch<kProductDx, __nv_bfloat16>(m, p, smem, grid, st);
+    return launch<kProductDw, __nv_bfloat16>(m, p, smem, grid, st);
+  }
+  if (mode == kProductForward) return launch<kProductForward, __half>(m, p, smem, grid, st);
+  if (mode == kProductDx) return launch<kProductDx, __half>(m, p, smem, grid, st);
+  return launch<kProductDw, __half>(m, p, smem, grid, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,100 @@
+// Internal interface of the stand-alone products (linear, grouped_linear and
+// their gradients): what products_api.cu fills in for the kernels of
+// product_gemm.cu and product_rows.cu.  Not installed, not part of the ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+// One kernel computes all three products, as out[j][f] = sum_c A[f][c] B[j][c]
+// (features f on the MMA's M side and the accumulator's lanes, so a warp's
+// lanes write consecutive outputs; rows j on its N side, 16 at a time, so a
+// tile with few rows costs little):
+//   forward  A = W_g^T (features = N, read MN-major from W [K, N]), B = x,  c = K
+//   dx       A = W_g   (features = K, read K-major),                B = dz, c = N
+//   dw       A = dz^T  (features = N, MN-major), B = x^T (MN-major, j = K),
+//            c = the group's rows
+constexpr int kProductForward = 0;
+constexpr int kProductDx = 1;
+constexpr int kProductDw = 2;
+
+constexpr int kProductMaxGroups = 1024;
+constexpr int kProductBM = 128;     // features per CTA tile
+constexpr int kProductMaxBN = 128;  // rows per one-CTA tile (a multiple of 16)
+constexpr int kProductMaxSplit = 8;
+
+struct ProductParams {
+  const int* offsets;  // [groups + 1] first row of each group; nullptr: one group of all rows
+  int groups;          // >= 1
+  int rows;            // rows of x / dz that exist
+  int feats;           // F: features of the output
+  int cols;            // dw: J, the output's rows per group; else unused
+  int depth;           // contraction length (forward K, dx N; dw: unused)
+  int bn;              // rows per tile, a multiple of 16
+  int stages;          // pipeline slots
+  int split;           // CTAs of a cluster sharing one tile's contraction
+  void* out;
+  int64_t ld_out;      // elements between output rows
+  const void* bias;    // [groups, feats] or nullptr
+  const void* residual;
+  int64_t ld_residual;
+  void* preact;
+  int64_t ld_preact;
+  int act;             // moe_activation_t
+  int* status;         // device status word
+};
+
+struct ProductMaps {
+  CUtensorMap a, b;
+};
+
+// smem bytes of one pipeline slot of a tile of bn rows
+size_t product_slot_bytes(int mode, int bn);
+cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
+                           int num_sms, cudaStream_t st);
+
+// Row kernels (product_rows.cu).
+// Copies groups x rows x cols 2-byte elements into rows of ld_dst elements.
+cudaError_t launch_pack_rows(const void* src, int64_t ld, int64_t group_stride, int groups,
+                             int64_t rows, int cols, void* dst, int64_t ld_dst, cudaStream_t st);
+
+struct RowGradParams {
+  const void* dout;
+  int64_t ld_dout;
+  const void* preact;  // nullptr: dz = dout, not written
+  int64_t ld_preact;
+  void* dz;
+  int64_t ld_dz;
+  const int* offsets;
+  int groups, rows, cols;
+  int act;
+  float* partial;      // [chunks, cols] column sums of 128-row chunks, or nullptr
+  void* db;            // [groups, cols] or nullptr
+};
+constexpr int kRowChunk = 128;
+inline size_t row_grad_chunks(int rows, int groups) {
+  return static_cast<size_t>(rows) / kRowChunk + static_cast<size_t>(groups);
+}
+// dz = dout * act'(preact), and db from dz in fp32 (two launches when db is asked for)
+cudaError_t launch_row_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st);
+
+// SwiGLU (swiglu.cu)
+struct SwigluParams {
+  const void *gate, *up, *dout;
+  int64_t ld_gate, ld_up, ld_dout;
+  void *out, *dgate, *dup;
+  int64_t ld_out, ld_dgate, ld_dup;
+  const float* scale;  // [rows] or nullptr
+  float* dscale;       // [rows] or nullptr
+  const int* offsets;  // rows outside [offsets[0], offsets[groups]) are left alone
+  int groups, rows, cols;
+  float limit;
+};
+cudaError_t launch_swiglu(int dtype, const SwigluParams& p, cudaStream_t st);
+cudaError_t launch_swiglu_backward(int dtype, const SwigluParams& p, cudaStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,566 @@
+// C ABI of the stand-alone operators (moe_linear*, moe_swiglu*): argument
+// checks, tensor maps, the choice of tile and split, the workspace.
+#include <algorithm>
+#include <cmath>
+#include <cudaTypedefs.h>
+
+#include "api_util.h"
+#include "moe_internal.h"
+#include "products.h"
+
+namespace moe {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+}
+
+namespace {
+
+using namespace moe;
+
+constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxFeatures = 65536;
+constexpr int64_t kMaxStride = (1LL << 31) - 1;
+constexpr size_t kWsAlign = 256;
+constexpr int kMaxDevices = 64;
+
+size_t ws_round(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
+
+// The kernels' status word of each device (set by a bounded wait that gave up).
+__device__ int g_product_status;
+
+// The current device's status word and SM count, looked up once per device
+// (and again if a device reset gave the device another context).
+int device_of(int* sms, int** status) {
+  struct Entry {
+    unsigned long long ctx = 0;
+    int sms = 0;
+    int* status = nullptr;
+  };
+  static thread_local Entry cache[kMaxDevices];
+  int dev = -1;
+  MOE_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= kMaxDevices) return MOE_ERR_UNSUPPORTED;
+  Entry& e = cache[dev];
+  CUcontext ctx = nullptr;
+  unsigned long long id = 0;
+  static PFN_cuCtxGetCurrent_v4000 get_ctx = nullptr;
+  static PFN_cuCtxGetId_v12000 get_id = nullptr;
+  if (get_ctx == nullptr || get_id == nullptr) {
+    cudaDriverEntryPointQueryResult q;
+    void *a = nullptr, *b = nullptr;
+    MOE_CUDA(cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &a, 12000, cudaEnableDefault, &q));
+    MOE_CUDA(cudaGetDriverEntryPointByVersion("cuCtxGetId", &b, 12000, cudaEnableDefault, &q));
+    if (a == nullptr || b == nullptr) return MOE_ERR_CUDA;
+    get_ctx = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(a);
+    get_id = reinterpret_cast<PFN_cuCtxGetId_v12000>(b);
+  }
+  const bool have = get_ctx(&ctx) == CUDA_SUCCESS && ctx != nullptr &&
+                    get_id(ctx, &id) == CUDA_SUCCESS;
+  if (e.status == nullptr || !have || id != e.ctx) {
+    void* p = nullptr;
+    MOE_CUDA(cudaGetSymbolAddress(&p, g_product_status));
+    MOE_CUDA(cudaDeviceGetAttribute(&e.sms, cudaDevAttrMultiProcessorCount, dev));
+    e.status = static_cast<int*>(p);
+    if (get_ctx(&ctx) != CUDA_SUCCESS || ctx == nullptr || get_id(ctx, &id) != CUDA_SUCCESS)
+      return MOE_ERR_CUDA;
+    e.ctx = id;
+  }
+  *sms = e.sms;
+  *status = e.status;
+  return MOE_OK;
+}
+
+// A 16-bit tensor as (cols, rows, groups) with its strides, box 64 columns
+// (128 bytes) x box_rows, 128-byte swizzle; out-of-range elements read as zero.
+bool encode(CUtensorMap* m, bool bf16, const void* base, int64_t cols, int64_t rows,
+            int64_t groups, int64_t ld, int64_t group_stride, int dims, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                       static_cast<cuuint64_t>(groups)};
+  cuuint64_t stride[2] = {static_cast<cuuint64_t>(ld) * 2,
+                          static_cast<cuuint64_t>(group_stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             static_cast<cuuint32_t>(dims), const_cast<void*>(base), dim, stride, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tma_ready(const void* p, int64_t ld, int64_t group_stride) {
+  return aligned(p, 16) && ld % 8 == 0 && group_stride % 8 == 0;
+}
+
+// [first, last) bytes of a strided 2-byte tensor
+struct Range {
+  uintptr_t a, b;
+};
+Range range(const void* p, int64_t rows, int64_t cols, int64_t ld, int el = 2) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  if (p == nullptr || rows <= 0) return {0, 0};
+  return {a, a + static_cast<uintptr_t>(((rows - 1) * ld + cols) * el)};
+}
+bool overlap(Range x, Range y) { return x.a < y.b && y.a < x.b; }
+
+bool stride_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxStride; }
+
+int check_config(const moe_linear_config_t* c) {
+  if (c == nullptr || c->rows < 0 || c->in_features < 1 || c->out_features < 1 || c->groups < 0 ||
+      c->activation < MOE_ACT_NONE || c->activation > MOE_ACT_GELU_TANH)
+    return MOE_ERR_INVALID_ARG;
+  if (c->dtype < MOE_F32 || c->dtype > MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_BF16 && c->dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
+  if (c->rows > kMaxRows || c->in_features > kMaxFeatures || c->out_features > kMaxFeatures ||
+      c->groups > kProductMaxGroups)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// W's own checks: strides, and the elements it spans
+int check_w(const moe_linear_config_t* c, const void* w, int64_t ld, int64_t gs, Range* r) {
+  if (w == nullptr || !aligned(w, 2) || !stride_ok(ld, c->out_features)) return MOE_ERR_INVALID_ARG;
+  const int64_t K = c->in_features, G = c->groups;
+  int64_t span = (K - 1) * ld + c->out_features;
+  if (G > 1) {
+    if (gs < span) return MOE_ERR_INVALID_ARG;
+    if (gs > (1LL << 38)) return MOE_ERR_UNSUPPORTED;
+    span += (G - 1) * gs;
+  }
+  *r = range(w, 1, span, span);
+  return MOE_OK;
+}
+
+int check_forward(const moe_linear_config_t* c, const moe_linear_args_t* a) {
+  int r = check_config(c);
+  if (r != MOE_OK) return r;
+  if (a == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->rows == 0) return MOE_OK;
+  const int64_t R = c->rows, K = c->in_features, N = c->out_features;
+  Range w;
+  if (a->x == nullptr || a->out == nullptr || (c->groups > 0) != (a->offsets != nullptr) ||
+      !stride_ok(a->ld_x, K) || !stride_ok(a->ld_out, N) ||
+      (a->residual != nullptr && !stride_ok(a->ld_residual, N)) ||
+      (a->preact != nullptr && !stride_ok(a->ld_preact, N)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(a->x, 2) || !aligned(a->out, 2) || !aligned(a->bias, 2) ||
+      !aligned(a->residual, 2) || !aligned(a->preact, 2) || !aligned(a->offsets, 4))
+    return MOE_ERR_INVALID_ARG;
+  if ((r = check_w(c, a->w, a->ld_w, a->group_stride_w, &w)) != MOE_OK) return r;
+  const Range x = range(a->x, R, K, a->ld_x), out = range(a->out, R, N, a->ld_out);
+  const Range pre = range(a->preact, R, N, a->ld_preact);
+  const Range res = range(a->residual, R, N, a->ld_residual);
+  const Range bias = range(a->bias, 1, std::max(1, c->groups) * N, 0);
+  const bool in_place = a->residual == a->out && a->ld_residual == a->ld_out;
+  for (const Range& o : {out, pre})
+    if (overlap(o, x) || overlap(o, w) || overlap(o, bias)) return MOE_ERR_INVALID_ARG;
+  if (overlap(out, pre) || overlap(pre, res) || (overlap(out, res) && !in_place))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int check_backward(const moe_linear_config_t* c, const moe_linear_grads_t* a) {
+  int r = check_config(c);
+  if (r != MOE_OK) return r;
+  if (a == nullptr) return MOE_ERR_INVALID_ARG;
+  const int64_t R = c->rows, K = c->in_features, N = c->out_features;
+  const int64_t G = std::max(1, c->groups);
+  if (!aligned(a->dw, 2) || !aligned(a->dbias, 2) || !aligned(a->dx, 2)) return MOE_ERR_INVALID_ARG;
+  if (R == 0) return MOE_OK;
+  if (a->dout == nullptr || !aligned(a->dout, 2) || !stride_ok(a->ld_dout, N) ||
+      (c->groups > 0) != (a->offsets != nullptr) || !aligned(a->offsets, 4) ||
+      (c->activation != MOE_ACT_NONE) != (a->preact != nullptr) || !aligned(a->preact, 2) ||
+      (a->preact != nullptr && !stride_ok(a->ld_preact, N)) ||
+      (a->dx != nullptr && !stride_ok(a->ld_dx, K)) ||
+      (a->dw != nullptr && (a->x == nullptr || !aligned(a->x, 2) || !stride_ok(a->ld_x, K))))
+    return MOE_ERR_INVALID_ARG;
+  Range w{0, 0};
+  if (a->dx != nullptr && (r = check_w(c, a->w, a->ld_w, a->group_stride_w, &w)) != MOE_OK) return r;
+  const Range in[4] = {range(a->dout, R, N, a->ld_dout), w, range(a->preact, R, N, a->ld_preact),
+                       a->dw != nullptr ? range(a->x, R, K, a->ld_x) : Range{0, 0}};
+  const Range out[3] = {range(a->dx, R, K, a->ld_dx), range(a->dw, 1, G * K * N, 0),
+                        range(a->dbias, 1, G * N, 0)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& v : in)
+      if (overlap(out[i], v)) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }
+size_t copy_bytes(int64_t rows, int64_t cols) {
+  return ws_round(static_cast<size_t>(rows) * static_cast<size_t>(padded(cols)) * 2);
+}
+
+struct ForwardWs {
+  bool copy_x, copy_w;
+  size_t x, w, total;
+};
+int64_t group_stride(const moe_linear_config_t* c, int64_t gs, int64_t ld) {
+  return c->groups > 1 ? gs : ld * c->in_features;
+}
+ForwardWs forward_ws(const moe_linear_config_t* c, const moe_linear_args_t* a) {
+  ForwardWs w{};
+  if (c->rows == 0) return w;
+  w.copy_x = !tma_ready(a->x, a->ld_x, 0);
+  w.copy_w = !tma_ready(a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w));
+  w.x = w.total;
+  if (w.copy_x) w.total += copy_bytes(c->rows, c->in_features);
+  w.w = w.total;
+  if (w.copy_w)
+    w.total += copy_bytes(static_cast<int64_t>(std::max(1, c->groups)) * c->in_features,
+                          c->out_features);
+  return w;
+}
+
+struct BackwardWs {
+  bool copy_x, copy_w, copy_dout, make_dz;
+  size_t x, w, dz, partial, total;
+};
+BackwardWs backward_ws(const moe_linear_config_t* c, const moe_linear_grads_t* a) {
+  BackwardWs w{};
+  if (c->rows == 0) return w;
+  const int G = std::max(1, c->groups);
+  const bool products = a->dx != nullptr || a->dw != nullptr;
+  w.make_dz = c->activation != MOE_ACT_NONE;
+  w.copy_dout = !w.make_dz && products && !tma_ready(a->dout, a->ld_dout, 0);
+  w.copy_x = a->dw != nullptr && !tma_ready(a->x, a->ld_x, 0);
+  w.copy_w = a->dx != nullptr &&
+             !tma_ready(a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w));
+  w.x = w.total;
+  if (w.copy_x) w.total += copy_bytes(c->rows, c->in_features);
+  w.w = w.total;
+  if (w.copy_w)
+    w.total += copy_bytes(static_cast<int64_t>(G) * c->in_features, c->out_features);
+  w.dz = w.total;
+  if (w.make_dz || w.copy_dout) w.total += copy_bytes(c->rows, c->out_features);
+  w.partial = w.total;
+  if (a->dbias != nullptr)
+    w.total += ws_round(row_grad_chunks(c->rows, G) * static_cast<size_t>(c->out_features) * 4);
+  return w;
+}
+
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return MOE_OK;
+  return ws == nullptr || !aligned(ws, kWsAlign) || have < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+// Rows per tile and the contraction's split of a forward / dx product.
+void choose(ProductParams* p, int depth_blocks, int num_sms) {
+  const int64_t groups = p->offsets == nullptr ? 1 : p->groups;
+  const int64_t filled = std::max<int64_t>(1, std::min<int64_t>(groups, p->rows));
+  const int64_t mean = (p->rows + filled - 1) / filled;  // rows of a group that has any
+  int bn = 16;
+  while (bn < kProductMaxBN && bn < mean) bn *= 2;
+  const int64_t f_tiles = (p->feats + kProductBM - 1) / kProductBM;
+  const int64_t tiles = f_tiles * filled * ((mean + bn - 1) / bn);
+  int split = 1;
+  while (split < kProductMaxSplit && tiles * split * 2 <= num_sms && depth_blocks >= 4 * split)
+    split *= 2;
+  p->bn = bn;
+  p->split = split;
+}
+
+struct Operand {
+  const void* p;
+  int64_t ld, gs;
+};
+
+}  // namespace
+
+extern "C" {
+
+int moe_linear_config_check(const moe_linear_config_t* cfg) { return check_config(cfg); }
+
+int moe_linear_workspace_size(const moe_linear_config_t* cfg, const moe_linear_args_t* args,
+                              size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  const int r = check_forward(cfg, args);
+  if (r != MOE_OK) return r;
+  *bytes = forward_ws(cfg, args).total;
+  return MOE_OK;
+}
+
+int moe_linear_backward_workspace_size(const moe_linear_config_t* cfg,
+                                       const moe_linear_grads_t* grads, size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  const int r = check_backward(cfg, grads);
+  if (r != MOE_OK) return r;
+  *bytes = backward_ws(cfg, grads).total;
+  return MOE_OK;
+}
+
+int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* workspace,
+               size_t ws_bytes, void* stream) {
+  int r = check_forward(c, a);
+  if (r != MOE_OK) return r;
+  if (c->rows == 0) return MOE_OK;
+  const ForwardWs ws = forward_ws(c, a);
+  if ((r = check_ws(workspace, ws_bytes, ws.total)) != MOE_OK) return r;
+  int sms = 0;
+  int* status = nullptr;
+  if ((r = device_of(&sms, &status)) != MOE_OK) return r;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  const int64_t R = c->rows, K = c->in_features, N = c->out_features;
+  const int G = std::max(1, c->groups);
+  const bool bf16 = c->dtype == MOE_BF16;
+  Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
+  if (ws.copy_x) {
+    MOE_CUDA(launch_pack_rows(x.p, x.ld, 0, 1, R, static_cast<int>(K), base + ws.x, padded(K), st));
+    x = {base + ws.x, padded(K), 0};
+  }
+  if (ws.copy_w) {
+    MOE_CUDA(launch_pack_rows(w.p, w.ld, w.gs, G, K, static_cast<int>(N), base + ws.w, padded(N), st));
+    w = {base + ws.w, padded(N), padded(N) * K};
+  }
+  ProductParams p{};
+  p.offsets = a->offsets;
+  p.groups = G;
+  p.rows = c->rows;
+  p.feats = c->out_features;
+  p.depth = c->in_features;
+  choose(&p, static_cast<int>((K + 63) / 64), sms);
+  p.out = a->out;
+  p.ld_out = a->ld_out;
+  p.bias = a->bias;
+  p.residual = a->residual;
+  p.ld_residual = a->ld_residual;
+  p.preact = a->preact;
+  p.ld_preact = a->ld_preact;
+  p.act = c->activation;
+  p.status = status;
+  ProductMaps m;
+  if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, 64) ||
+      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, p.bn))
+    return MOE_ERR_CUDA;
+  MOE_CUDA(launch_product(kProductForward, bf16, m, p, sms, st));
+  return MOE_OK;
+}
+
+int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* a,
+                        void* workspace, size_t ws_bytes, void* stream) {
+  int r = check_backward(c, a);
+  if (r != MOE_OK) return r;
+  const BackwardWs ws = backward_ws(c, a);
+  if ((r = check_ws(workspace, ws_bytes, ws.total)) != MOE_OK) return r;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t R = c->rows, K = c->in_features, N = c->out_features;
+  const int G = std::max(1, c->groups);
+  const bool bf16 = c->dtype == MOE_BF16;
+  if (R == 0) {
+    if (a->dw != nullptr) MOE_CUDA(cudaMemsetAsync(a->dw, 0, static_cast<size_t>(G) * K * N * 2, st));
+    if (a->dbias != nullptr) MOE_CUDA(cudaMemsetAsync(a->dbias, 0, static_cast<size_t>(G) * N * 2, st));
+    return MOE_OK;
+  }
+  int sms = 0;
+  int* status = nullptr;
+  if ((r = device_of(&sms, &status)) != MOE_OK) return r;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
+  Operand dz{a->dout, a->ld_dout, 0};
+  const bool products = a->dx != nullptr || a->dw != nullptr;
+  if (ws.make_dz || a->dbias != nullptr) {
+    RowGradParams q{};
+    q.dout = a->dout;
+    q.ld_dout = a->ld_dout;
+    q.preact = a->preact;
+    q.ld_preact = a->ld_preact;
+    q.dz = base + ws.dz;
+    q.ld_dz = padded(N);
+    q.offsets = a->offsets;
+    q.groups = G;
+    q.rows = c->rows;
+    q.cols = c->out_features;
+    q.act = c->activation;
+    q.partial = a->dbias != nullptr ? reinterpret_cast<float*>(base + ws.partial) : nullptr;
+    q.db = a->dbias;
+    if (products || a->dbias != nullptr) MOE_CUDA(launch_row_grad(bf16, q, sms, st));
+    if (ws.make_dz) dz = {base + ws.dz, padded(N), 0};
+  }
+  if (ws.copy_dout) {
+    MOE_CUDA(launch_pack_rows(dz.p, dz.ld, 0, 1, R, static_cast<int>(N), base + ws.dz, padded(N), st));
+    dz = {base + ws.dz, padded(N), 0};
+  }
+  if (ws.copy_w) {
+    MOE_CUDA(launch_pack_rows(w.p, w.ld, w.gs, G, K, static_cast<int>(N), base + ws.w, padded(N), st));
+    w = {base + ws.w, padded(N), padded(N) * K};
+  }
+  if (ws.copy_x) {
+    MOE_CUDA(launch_pack_rows(x.p, x.ld, 0, 1, R, static_cast<int>(K), base + ws.x, padded(K), st));
+    x = {base + ws.x, padded(K), 0};
+  }
+  ProductParams p{};
+  p.offsets = a->offsets;
+  p.groups = G;
+  p.rows = c->rows;
+  p.status = status;
+  ProductMaps m;
+  if (a->dx != nullptr) {
+    p.feats = c->in_features;
+    p.depth = c->out_features;
+    p.out = a->dx;
+    p.ld_out = a->ld_dx;
+    choose(&p, static_cast<int>((N + 63) / 64), sms);
+    if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, kProductBM) ||
+        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, 2, p.bn))
+      return MOE_ERR_CUDA;
+    MOE_CUDA(launch_product(kProductDx, bf16, m, p, sms, st));
+  }
+  if (a->dw != nullptr) {
+    p.feats = c->out_features;
+    p.cols = c->in_features;
+    p.depth = 0;
+    p.out = a->dw;
+    p.ld_out = N;
+    p.bn = kProductMaxBN;
+    const int64_t tiles = static_cast<int64_t>(G) * ((N + kProductBM - 1) / kProductBM) *
+                          ((K + p.bn - 1) / p.bn);
+    const int64_t blocks = (R / G + 63) / 64;
+    p.split = 1;
+    while (p.split < kProductMaxSplit && tiles * p.split * 2 <= sms && blocks >= 4 * p.split)
+      p.split *= 2;
+    if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 2, 64) ||
+        !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, 64))
+      return MOE_ERR_CUDA;
+    MOE_CUDA(launch_product(kProductDw, bf16, m, p, sms, st));
+  }
+  return MOE_OK;
+}
+
+int moe_linear_get_device_error(int* device_err) {
+  int sms = 0;
+  int* status = nullptr;
+  if (device_err == nullptr) return MOE_ERR_INVALID_ARG;
+  const int r = device_of(&sms, &status);
+  if (r != MOE_OK) return r;
+  MOE_CUDA(cudaDeviceSynchronize());
+  MOE_CUDA(cudaMemcpy(device_err, status, sizeof(int), cudaMemcpyDeviceToHost));
+  if (*device_err == 0) return MOE_OK;
+  MOE_CUDA(cudaMemset(status, 0, sizeof(int)));
+  return MOE_ERR_DEVICE_TIMEOUT;
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_swiglu(const moe_swiglu_config_t* c) {
+  if (c == nullptr || c->rows < 0 || c->width < 1 || c->groups < 0 || !std::isfinite(c->limit) ||
+      c->limit < 0.f || c->dtype < MOE_F32 || c->dtype > MOE_F16)
+    return MOE_ERR_INVALID_ARG;
+  if (c->dtype == MOE_FP8_E4M3 || c->rows > kMaxRows || c->width > kMaxFeatures ||
+      c->groups > kProductMaxGroups)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// an output may be one of the inputs (the same rows, read before written by
+// the thread that writes them) or apart from it
+bool apart_or_same(const void* o, int64_t ld_o, const void* i, int64_t ld_i, int64_t rows,
+                   int64_t cols, int el) {
+  if (o == i && ld_o == ld_i) return true;
+  // interleaved halves of one tensor: the same stride, columns apart
+  if (ld_o == ld_i) {
+    const intptr_t row = static_cast<intptr_t>(ld_o) * el;
+    intptr_t d = (reinterpret_cast<intptr_t>(i) - reinterpret_cast<intptr_t>(o)) % row;
+    if (d < 0) d += row;
+    if (d >= cols * el && row - d >= cols * el) return true;
+  }
+  return !overlap(range(o, rows, cols, ld_o, el), range(i, rows, cols, ld_i, el));
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_swiglu(const moe_swiglu_config_t* c, const void* gate, int64_t ld_gate, const void* up,
+               int64_t ld_up, const float* scale, const int32_t* offsets, void* out,
+               int64_t ld_out, void* stream) {
+  const int r = check_swiglu(c);
+  if (r != MOE_OK) return r;
+  if (c->rows == 0) return MOE_OK;
+  const int el = c->dtype == MOE_F32 ? 4 : 2;
+  const int64_t R = c->rows, W = c->width;
+  if (gate == nullptr || up == nullptr || out == nullptr || !aligned(gate, el) ||
+      !aligned(up, el) || !aligned(out, el) || !aligned(scale, 4) || !aligned(offsets, 4) ||
+      !stride_ok(ld_gate, W) || !stride_ok(ld_up, W) || !stride_ok(ld_out, W) ||
+      (c->groups > 0) != (offsets != nullptr) ||
+      !apart_or_same(out, ld_out, gate, ld_gate, R, W, el) ||
+      !apart_or_same(out, ld_out, up, ld_up, R, W, el) ||
+      overlap(range(out, R, W, ld_out, el), range(scale, 1, R, 0, 4)))
+    return MOE_ERR_INVALID_ARG;
+  SwigluParams p{};
+  p.gate = gate;
+  p.ld_gate = ld_gate;
+  p.up = up;
+  p.ld_up = ld_up;
+  p.out = out;
+  p.ld_out = ld_out;
+  p.scale = scale;
+  p.offsets = offsets;
+  p.groups = c->groups;
+  p.rows = c->rows;
+  p.cols = c->width;
+  p.limit = c->limit;
+  MOE_CUDA(launch_swiglu(c->dtype, p, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int moe_swiglu_backward(const moe_swiglu_config_t* c, const void* dout, int64_t ld_dout,
+                        const void* gate, int64_t ld_gate, const void* up, int64_t ld_up,
+                        const float* scale, const int32_t* offsets, void* dgate, int64_t ld_dgate,
+                        void* dup, int64_t ld_dup, float* dscale, void* stream) {
+  const int r = check_swiglu(c);
+  if (r != MOE_OK) return r;
+  if (c->rows == 0) return MOE_OK;
+  const int el = c->dtype == MOE_F32 ? 4 : 2;
+  const int64_t R = c->rows, W = c->width;
+  if (dout == nullptr || gate == nullptr || up == nullptr || dgate == nullptr || dup == nullptr ||
+      !aligned(dout, el) || !aligned(gate, el) || !aligned(up, el) || !aligned(dgate, el) ||
+      !aligned(dup, el) || !aligned(scale, 4) || !aligned(dscale, 4) || !aligned(offsets, 4) ||
+      !stride_ok(ld_dout, W) || !stride_ok(ld_gate, W) || !stride_ok(ld_up, W) ||
+      !stride_ok(ld_dgate, W) || !stride_ok(ld_dup, W) || (c->groups > 0) != (offsets != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  struct {
+    const void* p;
+    int64_t ld;
+  } in[3] = {{dout, ld_dout}, {gate, ld_gate}, {up, ld_up}}, outs[2] = {{dgate, ld_dgate}, {dup, ld_dup}};
+  for (const auto& o : outs) {
+    for (const auto& i : in)
+      if (!apart_or_same(o.p, o.ld, i.p, i.ld, R, W, el)) return MOE_ERR_INVALID_ARG;
+    if (overlap(range(o.p, R, W, o.ld, el), range(scale, 1, R, 0, 4)) ||
+        overlap(range(o.p, R, W, o.ld, el), range(dscale, 1, R, 0, 4)))
+      return MOE_ERR_INVALID_ARG;
+  }
+  if (dgate == dup || !apart_or_same(dgate, ld_dgate, dup, ld_dup, R, W, el))
+    return MOE_ERR_INVALID_ARG;
+  for (const auto& i : in)
+    if (overlap(range(i.p, R, W, i.ld, el), range(dscale, 1, R, 0, 4))) return MOE_ERR_INVALID_ARG;
+  if (dscale != nullptr && overlap(range(dscale, 1, R, 0, 4), range(scale, 1, R, 0, 4)))
+    return MOE_ERR_INVALID_ARG;
+  SwigluParams p{};
+  p.gate = gate;
+  p.ld_gate = ld_gate;
+  p.up = up;
+  p.ld_up = ld_up;
+  p.dout = dout;
+  p.ld_dout = ld_dout;
+  p.dgate = dgate;
+  p.ld_dgate = ld_dgate;
+  p.dup = dup;
+  p.ld_dup = ld_dup;
+  p.scale = scale;
+  p.dscale = dscale;
+  p.offsets = offsets;
+  p.groups = c->groups;
+  p.rows = c->rows;
+  p.cols = c->width;
+  p.limit = c->limit;
+  MOE_CUDA(launch_swiglu_backward(c->dtype, p, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+}  // extern "C"
