@@ -156,5 +156,130 @@ __device__ __forceinline__ int group_of_block(const GroupTable& t, int groups, i
   return lo;
 }
 
+constexpr int kSubBytes = 64 * 128;  // one MN-major box: 64 steps x 64 elements
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait with cluster scope: what the arriving CTAs wrote here is visible.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  volatile int* abort, int* status) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicOr(status, kDevErrTimeout);
+      return false;
+    }
+  }
+}
+
+// Shared-memory matrix descriptor of an MN-major operand with the 128-byte
+// swizzle: 64-element chunks 8 KB apart (leading byte offset), groups of 8
+// contraction steps 1 KB apart (stride byte offset), descriptor version 1,
+// layout type 2.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kSubBytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Instruction descriptor of kind::f16 with 128 x n accumulators in fp32.
+__device__ __forceinline__ uint32_t product_idesc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
+         ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+struct Tile {
+  int g;        // group
+  int f0;       // first feature
+  int j0;       // first row of the tile: of the tensor (forward, dx) or of the group's output (dw)
+  int n_valid;  // rows of the tile
+  int c0;       // first contraction index (dw: row of the tensor)
+  int depth;    // contraction length
+};
+
+// Row blocks per ordering chunk: inside a group, chunks of 4 row blocks run
+// feature-major, so a weight tile's readers follow one another and the
+// chunk's rows stay in L2 across its weight tiles.
+constexpr int kChunk = 4;
+
+template <int MODE, int BM>
+__device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable& t, int w) {
+  Tile r;
+  const int f_tiles = (p.feats + BM - 1) / BM;
+  int local, blocks, in_chunk_first;
+  if (MODE == kProductDw) {
+    blocks = (p.cols + p.bn - 1) / p.bn;
+    const int per_group = f_tiles * blocks;
+    r.g = w / per_group;
+    local = w - r.g * per_group;
+  } else {
+    // tiles before group g: block_start[g] * f_tiles
+    const int b = w / f_tiles;
+    r.g = group_of_block(t, p.groups, b);
+    local = w - t.block_start[r.g] * f_tiles;
+    blocks = t.block_start[r.g + 1] - t.block_start[r.g];
+  }
+  const int per_chunk = f_tiles * kChunk;
+  const int c = local / per_chunk;
+  const int rem = local - c * per_chunk;
+  in_chunk_first = c * kChunk;
+  const int in_chunk = min(kChunk, blocks - in_chunk_first);
+  const int ft = rem / in_chunk;
+  const int nb = in_chunk_first + (rem - ft * in_chunk);
+  r.f0 = ft * BM;
+  if (MODE == kProductDw) {
+    r.j0 = nb * p.bn;
+    r.n_valid = min(p.bn, p.cols - r.j0);
+    r.c0 = t.row0[r.g];
+    r.depth = t.count(r.g);
+  } else {
+    r.j0 = t.row0[r.g] + nb * p.bn;
+    r.n_valid = min(p.bn, t.count(r.g) - nb * p.bn);
+    r.c0 = 0;
+    r.depth = p.depth;
+  }
+  return r;
+}
+
+// One finished value: the forward adds the bias, keeps z if asked, applies
+// the activation and adds the residual; rounded once to the output type.
+template <int MODE, typename T>
+__device__ __forceinline__ void finish_value(const ProductParams& p, int64_t row, int feat,
+                                             float bias, float v) {
+  if (MODE == kProductForward) {
+    v += bias;
+    if (p.preact != nullptr) static_cast<T*>(p.preact)[row * p.ld_preact + feat] = from_f32<T>(v);
+    v = activate(v, p.act);
+    if (p.residual != nullptr)
+      v += to_f32<T>(static_cast<const T*>(p.residual)[row * p.ld_residual + feat]);
+  }
+  static_cast<T*>(p.out)[row * p.ld_out + feat] = from_f32<T>(v);
+}
+
+template <typename T>
+constexpr bool is_bf16() {
+  return __is_same(T, __nv_bfloat16);
+}
+
 }  // namespace product
 }  // namespace moe

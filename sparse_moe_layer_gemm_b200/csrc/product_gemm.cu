@@ -38,7 +38,6 @@ namespace {
 using namespace product;
 
 constexpr int kThreads = 32 * 6;
-constexpr int kSubBytes = 64 * 128;  // one MN-major box: 64 steps x 64 elements
 constexpr int kABytes = 2 * kSubBytes;
 constexpr int kMaxStages = 12;
 constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
@@ -53,111 +52,8 @@ __host__ __device__ constexpr int exchange_bytes(int split, int bn) {
   return split > 1 ? split * ((bn + split - 1) / split) * kProductBM * 4 : 0;
 }
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// mbar_wait with cluster scope: what the arriving CTAs wrote here is visible.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
-                                                  volatile int* abort, int* status) {
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*abort) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      *abort = 1;
-      atomicOr(status, kDevErrTimeout);
-      return false;
-    }
-  }
-}
-
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// Shared-memory matrix descriptor of an MN-major operand with the 128-byte
-// swizzle: 64-element chunks 8 KB apart (leading byte offset), groups of 8
-// contraction steps 1 KB apart (stride byte offset), descriptor version 1,
-// layout type 2.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kSubBytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-// Instruction descriptor of kind::f16 with 128 x n accumulators in fp32.
-__device__ __forceinline__ uint32_t product_idesc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
-  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
-         ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-struct Tile {
-  int g;        // group
-  int f0;       // first feature
-  int j0;       // first row of the tile: of the tensor (forward, dx) or of the group's output (dw)
-  int n_valid;  // rows of the tile
-  int c0;       // first contraction index (dw: row of the tensor)
-  int depth;    // contraction length
-};
-
-// Row blocks per ordering chunk: inside a group, chunks of 4 row blocks run
-// feature-major, so a weight tile's readers follow one another and the
-// chunk's rows stay in L2 across its weight tiles.
-constexpr int kChunk = 4;
-
-template <int MODE>
-__device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable& t, int w) {
-  Tile r;
-  const int f_tiles = (p.feats + kProductBM - 1) / kProductBM;
-  int local, blocks, in_chunk_first;
-  if (MODE == kProductDw) {
-    blocks = (p.cols + p.bn - 1) / p.bn;
-    const int per_group = f_tiles * blocks;
-    r.g = w / per_group;
-    local = w - r.g * per_group;
-  } else {
-    // tiles before group g: block_start[g] * f_tiles
-    const int b = w / f_tiles;
-    r.g = group_of_block(t, p.groups, b);
-    local = w - t.block_start[r.g] * f_tiles;
-    blocks = t.block_start[r.g + 1] - t.block_start[r.g];
-  }
-  const int per_chunk = f_tiles * kChunk;
-  const int c = local / per_chunk;
-  const int rem = local - c * per_chunk;
-  in_chunk_first = c * kChunk;
-  const int in_chunk = min(kChunk, blocks - in_chunk_first);
-  const int ft = rem / in_chunk;
-  const int nb = in_chunk_first + (rem - ft * in_chunk);
-  r.f0 = ft * kProductBM;
-  if (MODE == kProductDw) {
-    r.j0 = nb * p.bn;
-    r.n_valid = min(p.bn, p.cols - r.j0);
-    r.c0 = t.row0[r.g];
-    r.depth = t.count(r.g);
-  } else {
-    r.j0 = t.row0[r.g] + nb * p.bn;
-    r.n_valid = min(p.bn, t.count(r.g) - nb * p.bn);
-    r.c0 = 0;
-    r.depth = p.depth;
-  }
-  return r;
 }
 
 template <int MODE, typename T>
@@ -235,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t it = 0;
       bool ok = true;
       for (int w = cluster; w < total && ok; w += clusters) {
-        const Tile t = decode<MODE>(p, tab, w);
+        const Tile t = decode<MODE, kProductBM>(p, tab, w);
         const int nkb = (t.depth + 63) >> 6;
         const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
         for (int kb = static_cast<int>(static_cast<int64_t>(nkb) * rank / split); kb < kb1; ++kb) {
@@ -277,17 +173,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    constexpr bool kIsBf16 = sizeof(T) == 2 && !__is_same(T, __half);
     uint32_t it = 0, tc = 0;
     bool ok = true;
     for (int w = cluster; w < total && ok; w += clusters) {
-      const Tile t = decode<MODE>(p, tab, w);
+      const Tile t = decode<MODE, kProductBM>(p, tab, w);
       const int nkb = (t.depth + 63) >> 6;
       const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / split);
       const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
       if (kb0 == kb1) continue;  // nothing to add: the epilogue takes zeros
       const uint32_t idesc =
-          product_idesc(kIsBf16, kAMn, kBMn, kProductBM, (t.n_valid + 15) & ~15);
+          product_idesc(is_bf16<T>(), kAMn, kBMn, kProductBM, (t.n_valid + 15) & ~15);
       const uint32_t buf = tc & 1u;
       int go = 1;
       if (lane == 0)
@@ -306,8 +201,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint8_t* slot = smem + s * slot_bytes;
         const int left = t.depth - kb * 64;  // contraction steps that exist from here on
         const int steps = min(4, (left + 15) >> 4);
-        if (MODE == kProductDw && (left & 15) != 0 && left < 64) {
-          // steps [left, steps * 16) are another group's rows: clear them in every box
+        if (MODE == kProductDw && (left & 15) != 0 && left < 64 && t.c0 + t.depth < p.rows) {
+          // steps [left, steps * 16) are another group's rows (behind the tensor's last
+          // row the load fills zeros): clear them in every box
           const int n16 = (steps * 16 - left) * 8;  // 16-byte pieces per box
           const int boxes = slot_bytes / kSubBytes;
           for (int i = lane; i < n16 * boxes; i += 32) {
@@ -346,10 +242,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int q = warp & 3;  // the TMEM lane quadrant this warp may read
     uint32_t tc = 0;
     const T* bias = static_cast<const T*>(p.bias);
-    const T* residual = static_cast<const T*>(p.residual);
-    T* preact = static_cast<T*>(p.preact);
     for (int w = cluster; w < total; w += clusters) {
-      const Tile t = decode<MODE>(p, tab, w);
+      const Tile t = decode<MODE, kProductBM>(p, tab, w);
       const int nkb = (t.depth + 63) >> 6;
       const bool empty = static_cast<int64_t>(nkb) * rank / split ==
                          static_cast<int64_t>(nkb) * (rank + 1) / split;
@@ -362,18 +256,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float b = (MODE == kProductForward && bias != nullptr && live)
                           ? to_f32<T>(bias[static_cast<int64_t>(t.g) * p.feats + feat])
                           : 0.f;
-      T* out = static_cast<T*>(p.out) + row0 * p.ld_out + feat;
-      // one finished value: forward adds the bias, keeps z if asked, applies
-      // the activation, adds the residual; rounded once to the output type
-      auto finish = [&](int j, float v) {
-        if (MODE == kProductForward) {
-          v += b;
-          if (preact != nullptr) preact[(row0 + j) * p.ld_preact + feat] = from_f32<T>(v);
-          v = activate(v, p.act);
-          if (residual != nullptr) v += to_f32<T>(residual[(row0 + j) * p.ld_residual + feat]);
-        }
-        out[static_cast<int64_t>(j) * p.ld_out] = from_f32<T>(v);
-      };
       if (!empty) {
         int go = 1;
         if (lane == 0)
@@ -397,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (live) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (c + i < t.n_valid) finish(c + i, __uint_as_float(r[i]));
+              if (c + i < t.n_valid) finish_value<MODE, T>(p, row0 + c + i, feat, b, __uint_as_float(r[i]));
           }
         } else {
 #pragma unroll
@@ -431,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           float v = 0.f;
           for (int s = 0; s < split; ++s)
             v += xch[(s * share + j) * kProductBM + q * 32 + lane];
-          if (live) finish(rank * share + j, v);
+          if (live) finish_value<MODE, T>(p, row0 + rank * share + j, feat, b, v);
         }
       }
     }

@@ -57,6 +57,12 @@ size_t product_slot_bytes(int mode, int bn);
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                            int num_sms, cudaStream_t st);
 
+// The same on CTA pairs (product_pair.cu): tiles of 256 features x bn <= 256
+// rows; map b's box is bn / 2 rows high (dw: 64 steps, as for one CTA).
+constexpr int kProductPairMaxBN = 256;
+cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
+                                int num_sms, cudaStream_t st);
+
 // Row kernels (product_rows.cu).
 // Copies groups x rows x cols 2-byte elements into rows of ld_dst elements.
 cudaError_t launch_pack_rows(const void* src, int64_t ld, int64_t group_stride, int groups,

@@ -247,20 +247,50 @@ int check_ws(const void* ws, size_t have, size_t need) {
   return ws == nullptr || !aligned(ws, kWsAlign) || have < need ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
-// Rows per tile and the contraction's split of a forward / dx product.
-void choose(ProductParams* p, int depth_blocks, int num_sms) {
-  const int64_t groups = p->offsets == nullptr ? 1 : p->groups;
-  const int64_t filled = std::max<int64_t>(1, std::min<int64_t>(groups, p->rows));
-  const int64_t mean = (p->rows + filled - 1) / filled;  // rows of a group that has any
+// Tile and split of a product: `blocks64` slots of 64 contraction steps,
+// `groups` groups of `mean` rows (dw: output rows) each.
+struct Choice {
+  bool pair;
+  int bn, split;
+};
+
+Choice choose(int64_t feats, int64_t groups, int64_t mean, int64_t blocks64, int num_sms) {
+  if (mean > kProductMaxBN) {
+    const int64_t f_tiles = (feats + 2 * kProductBM - 1) / (2 * kProductBM);
+    const int64_t pairs = num_sms / 2;
+    Choice best{true, 0, 1};
+    int64_t best_cost = 0;
+    for (int bn = kProductPairMaxBN; bn >= 128; bn -= 16) {
+      const int64_t tiles = groups * f_tiles * ((mean + bn - 1) / bn);
+      const int64_t cost = (tiles + pairs - 1) / pairs * std::max(104, bn / 2);
+      if (best.bn == 0 || cost < best_cost) {
+        best.bn = bn;
+        best_cost = cost;
+      }
+    }
+    const int64_t tiles = groups * f_tiles * ((mean + best.bn - 1) / best.bn);
+    if (2 * tiles >= pairs) return best;
+  }
   int bn = 16;
   while (bn < kProductMaxBN && bn < mean) bn *= 2;
-  const int64_t f_tiles = (p->feats + kProductBM - 1) / kProductBM;
-  const int64_t tiles = f_tiles * filled * ((mean + bn - 1) / bn);
+  const int64_t f_tiles = (feats + kProductBM - 1) / kProductBM;
+  const int64_t tiles = f_tiles * groups * ((mean + bn - 1) / bn);
   int split = 1;
-  while (split < kProductMaxSplit && tiles * split * 2 <= num_sms && depth_blocks >= 4 * split)
+  while (split < kProductMaxSplit && tiles * split * 2 <= num_sms && blocks64 >= 4 * split)
     split *= 2;
-  p->bn = bn;
-  p->split = split;
+  return {false, bn, split};
+}
+
+// Groups that can have rows, and their mean size.
+void filled(const int32_t* offsets, int64_t groups, int64_t rows, int64_t* n, int64_t* mean) {
+  *n = offsets == nullptr ? 1 : std::min(groups, rows);
+  *mean = (rows + *n - 1) / *n;
+}
+
+cudaError_t launch_any(const Choice& ch, int mode, bool bf16, const ProductMaps& m,
+                       const ProductParams& p, int sms, cudaStream_t st) {
+  return ch.pair ? launch_product_pair(mode, bf16, m, p, sms, st)
+                 : launch_product(mode, bf16, m, p, sms, st);
 }
 
 struct Operand {
@@ -322,7 +352,11 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.rows = c->rows;
   p.feats = c->out_features;
   p.depth = c->in_features;
-  choose(&p, static_cast<int>((K + 63) / 64), sms);
+  int64_t n_groups, mean;
+  filled(a->offsets, G, R, &n_groups, &mean);
+  const Choice ch = choose(N, n_groups, mean, (K + 63) / 64, sms);
+  p.bn = ch.bn;
+  p.split = ch.split;
   p.out = a->out;
   p.ld_out = a->ld_out;
   p.bias = a->bias;
@@ -334,9 +368,9 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.status = status;
   ProductMaps m;
   if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, 64) ||
-      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, p.bn))
+      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, ch.pair ? p.bn / 2 : p.bn))
     return MOE_ERR_CUDA;
-  MOE_CUDA(launch_product(kProductForward, bf16, m, p, sms, st));
+  MOE_CUDA(launch_any(ch, kProductForward, bf16, m, p, sms, st));
   return MOE_OK;
 }
 
@@ -403,11 +437,15 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.depth = c->out_features;
     p.out = a->dx;
     p.ld_out = a->ld_dx;
-    choose(&p, static_cast<int>((N + 63) / 64), sms);
+    int64_t n_groups, mean;
+    filled(a->offsets, G, R, &n_groups, &mean);
+    const Choice ch = choose(K, n_groups, mean, (N + 63) / 64, sms);
+    p.bn = ch.bn;
+    p.split = ch.split;
     if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, kProductBM) ||
-        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, 2, p.bn))
+        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, 2, ch.pair ? p.bn / 2 : p.bn))
       return MOE_ERR_CUDA;
-    MOE_CUDA(launch_product(kProductDx, bf16, m, p, sms, st));
+    MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
   }
   if (a->dw != nullptr) {
     p.feats = c->out_features;
@@ -415,17 +453,13 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.depth = 0;
     p.out = a->dw;
     p.ld_out = N;
-    p.bn = kProductMaxBN;
-    const int64_t tiles = static_cast<int64_t>(G) * ((N + kProductBM - 1) / kProductBM) *
-                          ((K + p.bn - 1) / p.bn);
-    const int64_t blocks = (R / G + 63) / 64;
-    p.split = 1;
-    while (p.split < kProductMaxSplit && tiles * p.split * 2 <= sms && blocks >= 4 * p.split)
-      p.split *= 2;
+    const Choice ch = choose(N, G, K, (R / G + 63) / 64, sms);
+    p.bn = ch.bn;
+    p.split = ch.split;
     if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 2, 64) ||
         !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, 64))
       return MOE_ERR_CUDA;
-    MOE_CUDA(launch_product(kProductDw, bf16, m, p, sms, st));
+    MOE_CUDA(launch_any(ch, kProductDw, bf16, m, p, sms, st));
   }
   return MOE_OK;
 }

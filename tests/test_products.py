@@ -246,6 +246,27 @@ def test_gradients_against_differences(act):
         assert abs(float(got - want)) <= float((2 * u * s * v.abs()).sum()) + 1e-6
 
 
+# large enough for CTA pairs: whole and ragged 256 x 256 tiles, odd depths
+LARGE = [(2048, 512, 4096), (2500, 1000, 2312), (4111, 136, 1800), (1024, 4096, 2048),
+         (1500, 3016, 2600)]
+
+
+@gpu
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("rows,k,n", LARGE)
+def test_linear_large(rows, k, n, act):
+    gen = torch.Generator().manual_seed(rows + k)
+    dt = torch.float16 if rows % 2 else torch.bfloat16
+    x, w = normal(gen, dt, rows, k), normal(gen, dt, k, n, std=k ** -0.5)
+    bias, res = normal(gen, dt, n), normal(gen, dt, rows, n)
+    pre = torch.empty(rows, n, dtype=dt, device="cuda")
+    out = B.linear(x, w, bias, residual=res, activation=act, preact=pre)
+    check_rows(out, x, w, bias, res, act, pre)
+    dout = normal(gen, dt, rows, n)
+    grads = B.linear_backward(dout, x, w, preact=None if act == "none" else pre, activation=act)
+    check_grads(*grads, dout, x, w, pre, act)
+
+
 # ----------------------------------------------------------------- grouped
 def offsets_of(sizes, first=0):
     o = torch.tensor([first] + list(sizes), dtype=torch.int64).cumsum(0)
@@ -314,6 +335,38 @@ def test_grouped_linear_backward(sizes, k, n, act):
             continue
         check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g],
                     None if pre is None else pre[a:b], act)
+
+
+@gpu
+@pytest.mark.parametrize("sizes,k,n", [
+    ([700, 1, 0, 513, 256, 255, 900], 512, 2304), ([3, 2000, 17, 1999], 1288, 1032),
+    ([1100, 900, 30], 2600, 264),
+])
+def test_grouped_large(sizes, k, n):
+    """Ragged groups on CTA pairs; the rows around the groups hold NaN."""
+    gen = torch.Generator().manual_seed(k)
+    G, first, behind = len(sizes), 5, 70
+    rows = first + sum(sizes) + behind
+    x, dout = normal(gen, torch.bfloat16, rows, k), normal(gen, torch.bfloat16, rows, n)
+    w = normal(gen, torch.bfloat16, G, k, n, std=k ** -0.5)
+    for t in (x, dout):
+        t[:first] = math.nan
+        t[rows - behind:] = math.inf
+    off = offsets_of(sizes, first)
+    out = torch.full((rows, n), 3.0, dtype=x.dtype, device="cuda")
+    dx = torch.full((rows, k), 3.0, dtype=x.dtype, device="cuda")
+    B.grouped_linear(x, off, w, out=out)
+    _, dw, db = B.grouped_linear_backward(dout, x, off, w, dx=dx)
+    for t in (out, dx):
+        assert (t[:first] == 3).all() and (t[rows - behind:] == 3).all()
+    o = off.tolist()
+    for g in range(G):
+        a, b = o[g], o[g + 1]
+        if a == b:
+            assert (dw[g] == 0).all() and (db[g] == 0).all()
+            continue
+        check_rows(out[a:b], x[a:b], w[g], None, None, "none")
+        check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g], None, "none")
 
 
 @gpu
