@@ -47,9 +47,10 @@ __host__ __device__ constexpr int b_bytes(int mode, int bn) {
   return mode == kProductDw ? (bn + 63) / 64 * kSubBytes : bn * 128;
 }
 
-// fp32 partials received for this CTA's share of a tile's rows
+// fp32 partials received for this CTA's share of a tile's rows (split), or the
+// epilogue warps' staged chunks
 __host__ __device__ constexpr int exchange_bytes(int split, int bn) {
-  return split > 1 ? split * ((bn + split - 1) / split) * kProductBM * 4 : 0;
+  return split > 1 ? split * ((bn + split - 1) / split) * kProductBM * 4 : 4 * kEpiWarpBytes;
 }
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int q = warp & 3;  // the TMEM lane quadrant this warp may read
     uint32_t tc = 0;
     const T* bias = static_cast<const T*>(p.bias);
+    uint8_t* stg = reinterpret_cast<uint8_t*>(xch) + (warp - 2) * kEpiWarpBytes;
     for (int w = cluster; w < total; w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
       const int nkb = (t.depth + 63) >> 6;
@@ -266,22 +268,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
       const int share = (t.n_valid + split - 1) / split;  // rows each CTA of the cluster finishes
       const uint32_t xch_addr = smem_u32(xch) + (q * 32 + lane) * 4;
-      for (int c = 0; c < t.n_valid; c += 16) {
-        uint32_t r[16];
-        if (empty) {
+      if (split == 1) {
+        store_tile<MODE, T>(p, taddr, 0, 16, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
+      } else {
+        for (int c = 0; c < t.n_valid; c += 16) {
+          uint32_t r[16];
+          if (empty) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = 0;
-        } else {
-          tmem_ld_x16(taddr + c, r);
-          tmem_ld_wait();
-        }
-        if (split == 1) {
-          if (live) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c + i < t.n_valid) finish_value<MODE, T>(p, row0 + c + i, feat, b, __uint_as_float(r[i]));
+            for (int i = 0; i < 16; ++i) r[i] = 0;
+          } else {
+            tmem_ld_x16(taddr + c, r);
+            tmem_ld_wait();
           }
-        } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (c + i < t.n_valid) {

@@ -11,9 +11,8 @@
 // Roles per CTA (10 warps): warp 0 TMA producer (own halves; every load
 // completes on the leader's full barrier), warp 1 tensor memory and (leader)
 // MMA issue, warps 2-9 epilogue, two per accumulator lane quadrant on
-// alternate 16-row chunks, so the epilogue of one tile (activation, 2-byte
-// stores of 64 contiguous bytes per warp) stays below the next tile's
-// mainloop.  Every wait is bounded.  No TMA multicast.
+// alternate 16-row chunks, so the epilogue of one tile stays below the next
+// tile's mainloop.  Every wait is bounded.  No TMA multicast.
 //
 // Weight gradient: the rows behind the group's last one in its last slot are
 // cleared by each CTA's producer warp, which waits for that slot's loads on a
@@ -52,7 +51,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kSlot);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kSlot + kEpiWarps * kEpiWarpBytes);
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = full0 + 8 * kStages;
   const uint32_t tfull0 = empty0 + 8 * kStages;
@@ -237,20 +236,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3;           // the TMEM lane quadrant this warp may read
     const int part = (warp - 2) >> 2;  // which of its quadrant's two warps
     const uint32_t tempty_leader = mapa_shared(tempty0, 0);
-    const T* bias = static_cast<const T*>(p.bias);
+    uint8_t* stg = smem + kStages * kSlot + (warp - 2) * kEpiWarpBytes;
     uint32_t tc = 0;
     for (int w = pair; w < total; w += n_pairs) {
       const Tile t = decode<MODE, kPairBM>(p, tab, w);
       const bool empty = t.depth <= 0;
       const uint32_t buf = tc & 1u;
-      const int feat = t.f0 + static_cast<int>(rank) * kProductBM + q * 32 + lane;
-      const bool live = feat < p.feats;
       const int64_t row0 = MODE == kProductDw
                                ? static_cast<int64_t>(t.g) * p.cols + t.j0
                                : static_cast<int64_t>(t.j0);
-      const float b = (MODE == kProductForward && bias != nullptr && live)
-                          ? to_f32<T>(bias[static_cast<int64_t>(t.g) * p.feats + feat])
-                          : 0.f;
       if (!empty) {
         int go = 1;
         if (lane == 0)
@@ -259,22 +253,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
-      for (int c = 16 * part; c < t.n_valid; c += 32) {
-        uint32_t r[16];
-        if (empty) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = 0;
-        } else {
-          tmem_ld_x16(taddr + c, r);
-          tmem_ld_wait();
-        }
-        if (live) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < t.n_valid)
-              finish_value<MODE, T>(p, row0 + c + i, feat, b, __uint_as_float(r[i]));
-        }
-      }
+      store_tile<MODE, T>(p, taddr, 16 * part, 32, t.n_valid, row0,
+                          t.f0 + static_cast<int>(rank) * kProductBM + q * 32, t.g, empty, stg, lane);
       if (!empty) {
         tc_fence_before();
         __syncwarp();
@@ -309,7 +289,8 @@ cudaError_t launch(const ProductMaps& m, const ProductParams& p, size_t smem, in
 
 cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                                 int num_sms, cudaStream_t st) {
-  const size_t smem = 1024 + static_cast<size_t>(kStages) * kSlot + kBarBytes +
+  const size_t smem = 1024 + static_cast<size_t>(kStages) * kSlot +
+                      kEpiWarps * kEpiWarpBytes + kBarBytes +
                       static_cast<size_t>(group_table_bytes(p.groups));
   const int64_t f_tiles = (p.feats + kPairBM - 1) / kPairBM;
   int64_t tiles;

@@ -45,6 +45,8 @@ struct ProductParams {
   void* preact;
   int64_t ld_preact;
   int act;             // moe_activation_t
+  // rows at 16-byte boundaries, feats a multiple of 8: 16-byte accesses
+  bool vec_out, vec_residual, vec_preact;
   int* status;         // device status word
 };
 

@@ -92,6 +92,11 @@ bool tma_ready(const void* p, int64_t ld, int64_t group_stride) {
   return aligned(p, 16) && ld % 8 == 0 && group_stride % 8 == 0;
 }
 
+// rows of 16-byte pieces
+bool vec_rows(const void* p, int64_t ld, int64_t cols) {
+  return aligned(p, 16) && ld % 8 == 0 && cols % 8 == 0;
+}
+
 // [first, last) bytes of a strided 2-byte tensor
 struct Range {
   uintptr_t a, b;
@@ -365,6 +370,9 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.preact = a->preact;
   p.ld_preact = a->ld_preact;
   p.act = c->activation;
+  p.vec_out = vec_rows(a->out, a->ld_out, N);
+  p.vec_residual = vec_rows(a->residual, a->ld_residual, N);
+  p.vec_preact = vec_rows(a->preact, a->ld_preact, N);
   p.status = status;
   ProductMaps m;
   if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, 64) ||
@@ -437,6 +445,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.depth = c->out_features;
     p.out = a->dx;
     p.ld_out = a->ld_dx;
+    p.vec_out = vec_rows(a->dx, a->ld_dx, K);
     int64_t n_groups, mean;
     filled(a->offsets, G, R, &n_groups, &mean);
     const Choice ch = choose(K, n_groups, mean, (N + 63) / 64, sms);
@@ -453,6 +462,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.depth = 0;
     p.out = a->dw;
     p.ld_out = N;
+    p.vec_out = vec_rows(a->dw, N, N);
     const Choice ch = choose(N, G, K, (R / G + 63) / 64, sms);
     p.bn = ch.bn;
     p.split = ch.split;
