@@ -724,27 +724,31 @@ _OP_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: M
 
 class _Launch:
     """Makes a tensor's device (and the caller's stream, if given) current, so
-    that what a call allocates belongs to the stream that it runs on."""
+    that what a call allocates belongs to the stream that it runs on; enters
+    as the raw stream."""
+
+    __slots__ = ("_ctx", "_raw")
 
     def __init__(self, t: torch.Tensor, stream):
-        self._ctx = []
         dev = t.device
         if dev.type != "cuda":
             raise ValueError(f"want tensors on a CUDA device, got {dev}")
-        if dev.index != torch.cuda.current_device():
-            self._ctx.append(torch.cuda.device(dev))
-        if stream is not None:
-            s = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(int(stream), device=dev)
-            if s.device != dev:
-                raise ValueError(f"stream on {s.device}, tensors on {dev}")
-            self._ctx.append(torch.cuda.stream(s))
-        self.device = dev
+        if stream is None and dev.index == torch.cuda.current_device():
+            self._ctx = ()
+            self._raw = torch._C._cuda_getCurrentRawStream(dev.index)
+            return
+        s = torch.cuda.current_stream(dev) if stream is None else \
+            stream if isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(int(stream), device=dev)
+        if s.device != dev:
+            raise ValueError(f"stream on {s.device}, tensors on {dev}")
+        self._ctx = (torch.cuda.device(dev), torch.cuda.stream(s))
+        self._raw = s.cuda_stream
 
     def __enter__(self):
         for c in self._ctx:
             c.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return self._raw
 
     def __exit__(self, *exc):
         for c in reversed(self._ctx):
@@ -754,57 +758,60 @@ class _Launch:
 def _need_rows(t: torch.Tensor, name: str, like: torch.Tensor, rows: int, cols: int) -> int:
     """Checks a [rows, cols] tensor of like's type and device with contiguous
     rows; returns its row stride."""
-    if t.shape != (rows, cols) or t.dtype != like.dtype or t.device != like.device:
+    if t is not like and (t.shape != (rows, cols) or t.dtype != like.dtype
+                          or t.device != like.device):
         raise ValueError(f"{name}: want {like.dtype} {(rows, cols)} on {like.device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: want rows of contiguous elements, got strides {t.stride()}")
     if rows <= 1:
         return (cols + 7) // 8 * 8  # one row has no stride: take an aligned one
-    if t.stride(0) < cols:
+    if ld < cols:
         raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
-    return t.stride(0)
+    return ld
 
 
 def _need_vec(t: torch.Tensor, name: str, like: torch.Tensor, shape, dtype=None):
     dtype = like.dtype if dtype is None else dtype
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != like.device or \
+    if t.shape != shape or t.dtype != dtype or t.device != like.device or \
             not t.is_contiguous():
         raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {like.device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _product_setup(x_or_dout, w, offsets, cols_dim, activation, name):
+def _product_setup(t, w, offsets, cols_dim, activation, name):
     """Shared checks of the products: the configuration and W's strides."""
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation: want one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    t = x_or_dout
-    grouped = offsets is not None
-    if t.dim() != 2:
-        raise ValueError(f"{name}: want [rows, features], got {tuple(t.shape)}")
-    if w.dim() != (3 if grouped else 2) or w.dtype != t.dtype or w.device != t.device:
-        raise ValueError(f"w: want {t.dtype} {'[G, K, N]' if grouped else '[K, N]'} on {t.device}, "
-                         f"got {w.dtype} {tuple(w.shape)} on {w.device}")
-    K, N = w.shape[-2], w.shape[-1]
-    if t.shape[1] != (K, N)[cols_dim]:
-        raise ValueError(f"{name}: want {(K, N)[cols_dim]} features, got {t.shape[1]}")
-    if N > 1 and w.stride(-1) != 1:
-        raise ValueError(f"w: want rows of contiguous elements, got strides {w.stride()}")
-    ld = (N + 7) // 8 * 8 if K <= 1 else w.stride(-2)
-    gs = 0
-    G = 0
-    if grouped:
-        G = w.shape[0]
+    shape, ws = t.shape, w.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: want [rows, features], got {tuple(shape)}")
+    if len(ws) != (2 if offsets is None else 3) or w.dtype != t.dtype or w.device != t.device:
+        raise ValueError(f"w: want {t.dtype} {'[K, N]' if offsets is None else '[G, K, N]'} on "
+                         f"{t.device}, got {w.dtype} {tuple(ws)} on {w.device}")
+    K, N = ws[-2], ws[-1]
+    if shape[1] != (K, N)[cols_dim]:
+        raise ValueError(f"{name}: want {(K, N)[cols_dim]} features, got {shape[1]}")
+    strides = w.stride()
+    if strides[-1] != 1 and N > 1:
+        raise ValueError(f"w: want rows of contiguous elements, got strides {strides}")
+    ld = (N + 7) // 8 * 8 if K <= 1 else strides[-2]
+    gs = G = 0
+    if offsets is not None:
+        G = ws[0]
         if G < 1:
             raise ValueError("w: want at least one group")
-        gs = (K - 1) * ld + N if G == 1 else w.stride(0)
+        if G > 1:
+            gs = strides[0]
         _need_vec(offsets, "offsets", t, (G + 1,), torch.int32)
     if ld < N or (G > 1 and gs < (K - 1) * ld + N):
-        raise ValueError(f"w: rows or groups overlap (strides {w.stride()})")
-    if t.dtype not in _OP_DTYPES:
+        raise ValueError(f"w: rows or groups overlap (strides {strides})")
+    dtype = _OP_DTYPES.get(t.dtype)
+    if dtype is None:
         raise ValueError(f"{name}: unsupported type {t.dtype}")
-    cfg = moe_linear_config_t(t.shape[0], K, N, G, _OP_DTYPES[t.dtype], ACTIVATIONS[activation])
-    return cfg, K, N, G, ld, gs
+    return moe_linear_config_t(shape[0], K, N, G, dtype, act), K, N, G, ld, gs
 
 
 def _workspace(n: int, device) -> Optional[torch.Tensor]:
@@ -822,17 +829,18 @@ def _linear(x, offsets, w, bias, residual, activation, out, preact, stream):
     ld_pre = _need_rows(preact, "preact", x, R, N) if preact is not None else 0
     with _Launch(x, stream) as st:
         if out is None:
-            out = torch.empty(R, N, dtype=x.dtype, device=x.device)
+            out = x.new_empty((R, N))
         ld_out = _need_rows(out, "out", x, R, N)
         args = moe_linear_args_t(x.data_ptr(), ld_x, _ptr(offsets), w.data_ptr(), ld_w, gs,
                                  _ptr(bias), _ptr(residual), ld_res, out.data_ptr(), ld_out,
                                  _ptr(preact), ld_pre)
-        n = ctypes.c_size_t()
-        _check(lib.moe_linear_workspace_size(ctypes.byref(cfg), ctypes.byref(args),
-                                             ctypes.byref(n)), "moe_linear")
-        ws = _workspace(n.value, x.device)
-        _check(lib.moe_linear(ctypes.byref(cfg), ctypes.byref(args), _ptr(ws), n.value, st),
-               "moe_linear")
+        status = lib.moe_linear(cfg, args, None, 0, st)
+        if status == MOE_ERR_WORKSPACE:  # misaligned operands are copied first
+            n = ctypes.c_size_t()
+            _check(lib.moe_linear_workspace_size(cfg, args, n), "moe_linear")
+            ws = _workspace(n.value, x.device)
+            status = lib.moe_linear(cfg, args, ws.data_ptr(), n.value, st)
+        _check(status, "moe_linear")
     return out
 
 
@@ -878,11 +886,11 @@ def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream
     dx, dw, db = into
     with _Launch(dout, stream) as st:
         if need[0] and dx is None:
-            dx = torch.empty(R, K, dtype=dout.dtype, device=dout.device)
+            dx = dout.new_empty((R, K))
         if need[1] and dw is None:
-            dw = torch.empty(w.shape, dtype=dout.dtype, device=dout.device)
+            dw = dout.new_empty(w.shape)
         if need[2] and db is None:
-            db = torch.empty((G, N) if G else (N,), dtype=dout.dtype, device=dout.device)
+            db = dout.new_empty((G, N) if G else (N,))
         dx, dw, db = (t if n else None for t, n in zip((dx, dw, db), need))
         ld_dx = _need_rows(dx, "dx", dout, R, K) if dx is not None else 0
         if dw is not None:
@@ -893,11 +901,9 @@ def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream
                                    _ptr(offsets), w.data_ptr() if need[0] else None, ld_w, gs,
                                    _ptr(preact), ld_pre, _ptr(dx), ld_dx, _ptr(dw), _ptr(db))
         n = ctypes.c_size_t()
-        _check(lib.moe_linear_backward_workspace_size(ctypes.byref(cfg), ctypes.byref(grads),
-                                                      ctypes.byref(n)), "moe_linear_backward")
+        _check(lib.moe_linear_backward_workspace_size(cfg, grads, n), "moe_linear_backward")
         ws = _workspace(n.value, dout.device)
-        _check(lib.moe_linear_backward(ctypes.byref(cfg), ctypes.byref(grads), _ptr(ws), n.value,
-                                       st), "moe_linear_backward")
+        _check(lib.moe_linear_backward(cfg, grads, _ptr(ws), n.value, st), "moe_linear_backward")
     return dx, dw, db
 
 
@@ -965,9 +971,9 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, scale: Optional[torch.Tensor] =
     cfg, R, W, (ldg, ldu) = _swiglu_setup(gate, up, scale, limit, offsets)
     with _Launch(gate, stream) as st:
         if out is None:
-            out = torch.empty(R, W, dtype=gate.dtype, device=gate.device)
+            out = gate.new_empty((R, W))
         ldo = _need_rows(out, "out", gate, R, W)
-        _check(lib.moe_swiglu(ctypes.byref(cfg), gate.data_ptr(), ldg, up.data_ptr(), ldu,
+        _check(lib.moe_swiglu(cfg, gate.data_ptr(), ldg, up.data_ptr(), ldu,
                               _ptr(scale), _ptr(offsets), out.data_ptr(), ldo, st), "moe_swiglu")
     return out
 
@@ -986,15 +992,15 @@ def swiglu_backward(dout: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
         raise ValueError("dscale: there is no scale")
     with _Launch(gate, stream) as st:
         if dgate is None:
-            dgate = torch.empty(R, W, dtype=gate.dtype, device=gate.device)
+            dgate = gate.new_empty((R, W))
         if dup is None:
-            dup = torch.empty(R, W, dtype=gate.dtype, device=gate.device)
+            dup = gate.new_empty((R, W))
         if dscale is None and scale is not None:
             dscale = torch.empty(R, dtype=torch.float32, device=gate.device)
         if dscale is not None:
             _need_vec(dscale, "dscale", gate, (R,), torch.float32)
         ldg2, ldu2 = _need_rows(dgate, "dgate", gate, R, W), _need_rows(dup, "dup", gate, R, W)
-        _check(lib.moe_swiglu_backward(ctypes.byref(cfg), dout.data_ptr(), ldd, gate.data_ptr(),
+        _check(lib.moe_swiglu_backward(cfg, dout.data_ptr(), ldd, gate.data_ptr(),
                                        ldg, up.data_ptr(), ldu, _ptr(scale), _ptr(offsets),
                                        dgate.data_ptr(), ldg2, dup.data_ptr(), ldu2, _ptr(dscale),
                                        st), "moe_swiglu_backward")
