@@ -173,6 +173,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 // mbar_wait with cluster scope: what the arriving CTAs wrote here is visible.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
                                                   volatile int* abort, int* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
 #pragma unroll 1
@@ -217,11 +218,9 @@ struct Tile {
   int depth;    // contraction length
 };
 
-// Row blocks per ordering chunk: inside a group, chunks of 4 row blocks run
-// feature-major, so a weight tile's readers follow one another and the
-// chunk's rows stay in L2 across its weight tiles.
-constexpr int kChunk = 4;
-
+// Tile w.  Inside a group, chunks of p.chunk row blocks run feature-major: a
+// weight tile's readers follow one another, and the chunk's rows stay in L2
+// across its weight tiles.
 template <int MODE, int BM>
 __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable& t, int w) {
   Tile r;
@@ -239,11 +238,11 @@ __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable&
     local = w - t.block_start[r.g] * f_tiles;
     blocks = t.block_start[r.g + 1] - t.block_start[r.g];
   }
-  const int per_chunk = f_tiles * kChunk;
+  const int per_chunk = f_tiles * p.chunk;
   const int c = local / per_chunk;
   const int rem = local - c * per_chunk;
-  in_chunk_first = c * kChunk;
-  const int in_chunk = min(kChunk, blocks - in_chunk_first);
+  in_chunk_first = c * p.chunk;
+  const int in_chunk = min(p.chunk, blocks - in_chunk_first);
   const int ft = rem / in_chunk;
   const int nb = in_chunk_first + (rem - ft * in_chunk);
   r.f0 = ft * BM;

@@ -1,18 +1,29 @@
 // The stand-alone products on CTA pairs (2-SM MMA, M = 256): 256 features x
-// up to 256 rows per tile, for problems with enough tiles to be bound by the
+// up to 512 rows per tile, for problems with enough tiles to be bound by the
 // tensor cores.  Same orientation, operands and epilogue as product_gemm.cu.
 //
 // Operand split of the pair MMA: CTA r supplies features [128 r, 128 r + 128)
-// of the tile and rows [r N/2, (r + 1) N/2), and holds its features x all N
-// rows of the accumulator.  One instruction keeps both SMs' tensor cores busy
-// for N / 2 cycles, above its issue cost of about 100 from N = 208 on, and a
-// byte loaded into shared memory feeds twice the MMAs of a one-CTA tile.
+// of the tile and half of its rows, and holds its features x all rows of the
+// accumulator.
+//
+// Why two accumulators per tile (HALVES = 2, rows 0-255 and 256-511): MMAs
+// into one accumulator follow one another every ~165 cycles whatever their N
+// (4096^3: 25.6 us per wave of tiles at N = 128 and at N = 256), above the 128
+// cycles of work of an N = 256 instruction; alternating between two
+// accumulators hides that latency.  A tile of twice the rows also loads a
+// quarter less per flop, which matters at the 64 bytes per cycle that an SM
+// draws from L2.  The two accumulators fill tensor memory, so the epilogue
+// overlaps the next tile by skewing them: a tile's first kLead slots go to
+// the first accumulator before the second (which still drains), its last
+// kLead slots too (the first drains while the second finishes).
+// HALVES = 1 keeps 256-row tiles for problems of few tiles.
 //
 // Roles per CTA (10 warps): warp 0 TMA producer (own halves; every load
 // completes on the leader's full barrier), warp 1 tensor memory and (leader)
 // MMA issue, warps 2-9 epilogue, two per accumulator lane quadrant on
-// alternate 16-row chunks, so the epilogue of one tile stays below the next
-// tile's mainloop.  Every wait is bounded.  No TMA multicast.
+// alternate 16-row chunks.  Accumulators are taken in turn, one per half, so
+// tiles of one half still double-buffer.  Every wait is bounded.  No TMA
+// multicast.
 //
 // Weight gradient: the rows behind the group's last one in its last slot are
 // cleared by each CTA's producer warp, which waits for that slot's loads on a
@@ -33,21 +44,33 @@ using namespace product;
 constexpr int kPairBM = 2 * kProductBM;
 constexpr int kThreads = 32 * 10;
 constexpr int kEpiWarps = 8;
-constexpr int kStages = 6;
 constexpr int kOperand = 2 * kSubBytes;  // 128 rows or features of 64 steps
-constexpr int kSlot = 2 * kOperand;
 constexpr int kAccCols = 256;
-constexpr int kBarBytes = (2 * kStages + 6) * 8 + 16;
+constexpr int kLead = 2;  // slots by which the first accumulator leads at a tile's ends
 
-template <int MODE, typename T>
+template <int HALVES>
+struct PairShape {
+  static constexpr int kSlot = (1 + HALVES) * kOperand;
+  static constexpr int kStages = HALVES == 1 ? 6 : 4;
+  static constexpr int kBarBytes = (2 * kStages + 6) * 8 + 16;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kSlot +
+                                  kEpiWarps * kEpiWarpBytes + kBarBytes;
+  static_assert(kLead < kStages, "the leading accumulator waits for slots that the other frees");
+  static_assert(kSmem + group_table_bytes(kProductMaxGroups) <= 227 * 1024, "shared memory");
+};
+
+template <int MODE, int HALVES, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB, const ProductParams p) {
   constexpr bool kAMn = MODE != kProductDx;
   constexpr bool kBMn = MODE == kProductDw;
-  // this CTA's bytes of a slot: its features, and half of the tile's rows
-  const uint32_t box_bytes =
-      kOperand + (kBMn ? (p.bn / 2 + 63) / 64 * kSubBytes : p.bn / 2 * 128);
+  constexpr int kSlot = PairShape<HALVES>::kSlot;
+  constexpr int kStages = PairShape<HALVES>::kStages;
+  constexpr int kBarBytes = PairShape<HALVES>::kBarBytes;
+  // rows per accumulator, and this CTA's bytes of one half's rows in a slot
+  const int hn = HALVES == 1 ? p.bn : kAccCols;
+  const uint32_t half_bytes = kBMn ? (hn / 2 + 63) / 64 * kSubBytes : hn / 2 * 128;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -106,22 +129,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     const uint64_t pol = l2_policy_evict_normal();
     const uint32_t full_leader = mapa_shared(full0, 0);
-    uint32_t it = 0, tails = 0;
+    uint32_t it = 0, tails = 0, s = 0, ph = 0;
     bool ok = true;
-    for (int w = pair; w < total && ok; w += n_pairs) {
+    // (the whole warp walks the tiles for dw, whose last slots it clears)
+    for (int w = pair; w < total && ok && (MODE == kProductDw || lane == 0); w += n_pairs) {
       const Tile t = decode<MODE, kPairBM>(p, tab, w);
-      const int nkb = (t.depth + 63) >> 6;
-      const int half = ((t.n_valid + 15) & ~15) >> 1;  // this CTA's rows of the MMA
       const int f = t.f0 + static_cast<int>(rank) * kProductBM;
-      const int j = t.j0 + static_cast<int>(rank) * half;
-      for (int kb = 0; kb < nkb; ++kb) {
-        const uint32_t s = it % kStages;
-        const int left = t.depth - kb * 64;
+      // this CTA's first row in each half's MMA
+      int j[HALVES], halves = 0;
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const int n = min(hn, t.n_valid - h * hn);
+        if (n > 0) ++halves;
+        j[h] = t.j0 + h * hn + static_cast<int>(rank) * (((n + 15) & ~15) >> 1);
+      }
+      const uint32_t box_bytes = kOperand + halves * half_bytes;
+      for (int left = t.depth, c = t.c0; left > 0; left -= 64, c += 64) {
         const bool clear = MODE == kProductDw && left < 64 && (left & 15) != 0 &&
                            t.c0 + t.depth < p.rows;
         int go = 1;
         if (lane == 0) {
-          go = mbar_wait(empty0 + 8 * s, ((it / kStages) & 1u) ^ 1u, abort_flag, p.status) ? 1 : 0;
+          go = mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status) ? 1 : 0;
           if (go) {
             if (clear) {
               mbar_arrive_expect_tx(tail, box_bytes);
@@ -130,9 +158,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               mbar_arrive(full0 + 8 * s);
             }
             const uint32_t bar = clear ? mapa_shared(tail, rank) : full_leader + 8 * s;
-            const uint32_t sa = smem_u32(smem + s * kSlot);
+            const uint32_t sa = smem_u32(smem) + s * kSlot;
             const uint32_t sb = sa + kOperand;
-            const int c = t.c0 + kb * 64;
             if (MODE == kProductForward) {
               tma_load_3d_pair(sa, &tmA, bar, f, c, t.g, pol);
               tma_load_3d_pair(sa + kSubBytes, &tmA, bar, f + 64, c, t.g, pol);
@@ -142,24 +169,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tma_load_2d_pair(sa, &tmA, bar, f, c, pol);
               tma_load_2d_pair(sa + kSubBytes, &tmA, bar, f + 64, c, pol);
             }
-            if (kBMn) {
-              tma_load_2d_pair(sb, &tmB, bar, j, c, pol);
-              if (p.bn > 128) tma_load_2d_pair(sb + kSubBytes, &tmB, bar, j + 64, c, pol);
-            } else {
-              tma_load_2d_pair(sb, &tmB, bar, c, j, pol);
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+              if (h >= halves) break;
+              if (kBMn) {
+                tma_load_2d_pair(sb + h * kOperand, &tmB, bar, j[h], c, pol);
+                if (hn > 128)
+                  tma_load_2d_pair(sb + h * kOperand + kSubBytes, &tmB, bar, j[h] + 64, c, pol);
+              } else {
+                tma_load_2d_pair(sb + h * kOperand, &tmB, bar, c, j[h], pol);
+              }
             }
             if (clear) go = mbar_wait(tail, tails & 1u, abort_flag, p.status) ? 1 : 0;
           }
         }
-        if (!__shfl_sync(0xffffffffu, go, 0)) {
+        if (MODE == kProductDw) go = __shfl_sync(0xffffffffu, go, 0);
+        if (!go) {
           ok = false;
           break;
         }
         if (clear) {
           const int n16 = (((left + 15) & ~15) - left) * 8;  // 16-byte pieces per box
-          const int boxes = static_cast<int>(box_bytes) / kSubBytes;
           uint8_t* slot = smem + s * kSlot;
-          for (int i = lane; i < n16 * boxes; i += 32) {
+          // (boxes that this tile did not load are cleared too, harmlessly)
+          for (int i = lane; i < n16 * (kSlot / kSubBytes); i += 32) {
             const int box = i / n16;
             *reinterpret_cast<uint4*>(slot + box * kSubBytes + left * 128 + (i - box * n16) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -170,6 +203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++tails;
         }
         ++it;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
     }
     // the leader sees every armed slot complete (both CTAs' loads); the peer is
@@ -189,44 +226,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t sa = smem_u32(smem);
       const uint64_t ad0 = kAMn ? sdesc_mn_sw128(sa) : sdesc_k_sw<128>(sa);
       const uint64_t bd0 = kBMn ? sdesc_mn_sw128(sa + kOperand) : sdesc_k_sw<128>(sa + kOperand);
-      uint32_t it = 0, tc = 0;
-      bool ok = true;
+      uint32_t s = 0, ph = 0, tc = 0;
+      bool any = false, ok = true;
       for (int w = pair; w < total && ok; w += n_pairs) {
         const Tile t = decode<MODE, kPairBM>(p, tab, w);
         const int nkb = (t.depth + 63) >> 6;
         if (nkb == 0) continue;  // an empty group's gradient: the epilogue takes zeros
-        const uint32_t idesc =
-            product_idesc(is_bf16<T>(), kAMn, kBMn, kPairBM, (t.n_valid + 15) & ~15);
-        const uint32_t buf = tc & 1u;
-        if (!mbar_wait_cluster(tempty0 + 8 * buf, ((tc >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + buf * kAccCols;
-        for (int kb = 0; kb < nkb; ++kb) {
-          const uint32_t s = it % kStages;
-          const uint32_t ph = (it / kStages) & 1u;
-          // a cleared slot's zeros come from the peer's threads: cluster scope
-          if (!(MODE == kProductDw ? mbar_wait_cluster(full0 + 8 * s, ph, abort_flag, p.status)
-                                   : mbar_wait(full0 + 8 * s, ph, abort_flag, p.status))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = ad0 + static_cast<uint64_t>((s * kSlot) >> 4);
-          const uint64_t bd = bd0 + static_cast<uint64_t>((s * kSlot) >> 4);
-          const int steps = min(4, (t.depth - kb * 64 + 15) >> 4);
+        any = true;
+        uint32_t idesc[HALVES], d[HALVES];
+        int halves = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < steps)
-              gemm::mma_issue_pair(d, ad + i * kStepA, bd + i * kStepB, idesc,
-                                   (kb > 0 || i > 0) ? 1u : 0u);
-          tc_commit_pair_mc(empty0 + 8 * s, 3);  // frees the slot in both CTAs
-          ++it;
+        for (int h = 0; h < HALVES; ++h) {
+          const int n = min(hn, t.n_valid - h * hn);
+          if (n > 0) ++halves;
+          idesc[h] = product_idesc(is_bf16<T>(), kAMn, kBMn, kPairBM, (n + 15) & ~15);
+          d[h] = tmem_base + ((tc + h) & 1u) * kAccCols;
         }
-        if (!ok) break;
-        tc_commit_pair_mc(tfull0 + 8 * buf, 3);
-        ++tc;
+        // half h's accumulator is drained
+        auto acquire = [&](int h) {
+          const uint32_t c = tc + h;
+          const bool r = mbar_wait_cluster(tempty0 + 8 * (c & 1u), ((c >> 1) & 1u) ^ 1u, abort_flag,
+                                           p.status);
+          tc_fence_after();
+          return r;
+        };
+        // slot k slots on from the current one holds its loads
+        auto wait_slot = [&](uint32_t k) {
+          const uint32_t q = s + k;
+          const uint32_t bar = full0 + 8 * (q < kStages ? q : q - kStages);
+          const uint32_t par = q < kStages ? ph : ph ^ 1u;
+          // a cleared slot's zeros come from the peer's threads: cluster scope
+          const bool r = MODE == kProductDw ? mbar_wait_cluster(bar, par, abort_flag, p.status)
+                                            : mbar_wait(bar, par, abort_flag, p.status);
+          tc_fence_after();
+          return r;
+        };
+        // the MMAs of half h on that slot, `left` contraction steps remaining
+        auto issue = [&](int h, uint32_t k, int left) {
+          const uint32_t q = s + k;
+          const uint64_t at = static_cast<uint64_t>((q < kStages ? q : q - kStages) * (kSlot >> 4));
+          const uint64_t ad = ad0 + at;
+          const uint64_t bd = bd0 + at + static_cast<uint64_t>(h * (kOperand >> 4));
+          gemm::mma_issue_pair(d[h], ad, bd, idesc[h], left < t.depth ? 1u : 0u);
+          if (left > 48) {
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+              gemm::mma_issue_pair(d[h], ad + i * kStepA, bd + i * kStepB, idesc[h], 1u);
+          } else {
+            for (int i = 1; i < (left + 15) >> 4; ++i)
+              gemm::mma_issue_pair(d[h], ad + i * kStepA, bd + i * kStepB, idesc[h], 1u);
+          }
+        };
+        auto release = [&]() {
+          tc_commit_pair_mc(empty0 + 8 * s, 3);  // frees the slot in both CTAs
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        };
+        auto finish = [&](int h) { tc_commit_pair_mc(tfull0 + 8 * ((tc + h) & 1u), 3); };
+        if (!(ok = acquire(0))) break;
+        int left = t.depth;
+        if (HALVES == 1 || halves == 1) {
+          for (; left > 0; left -= 64) {
+            if (!(ok = wait_slot(0))) break;
+            issue(0, 0, left);
+            release();
+          }
+          if (!ok) break;
+          finish(0);
+        } else {
+          // kLead slots to the first accumulator, then to the second; both on
+          // the slots between; the last kLead slots again one after the other
+          const int lead = min(kLead, nkb);
+          for (int k = 0; k < lead && ok; ++k)
+            if ((ok = wait_slot(k))) issue(0, k, left - 64 * k);
+          if (ok && nkb <= kLead) finish(0);
+          if (!ok || !(ok = acquire(1))) break;
+          for (int k = 0; k < lead; ++k, left -= 64) {
+            issue(1, 0, left);
+            release();
+          }
+          for (; left > 64 * kLead; left -= 64) {
+            if (!(ok = wait_slot(0))) break;
+            issue(0, 0, left);
+            issue(1, 0, left);
+            release();
+          }
+          if (!ok) break;
+          if (left > 0) {
+            const int rest = (left + 63) >> 6;
+            for (int k = 0; k < rest && ok; ++k)
+              if ((ok = wait_slot(k))) issue(0, k, left - 64 * k);
+            if (!ok) break;
+            finish(0);
+            for (; left > 0; left -= 64) {
+              issue(1, 0, left);
+              release();
+            }
+          }
+          finish(1);
+        }
+        tc += halves;
       }
-      if (it > 0) {  // no MMA may still be writing TMEM at deallocation
+      if (any) {  // no MMA may still be writing TMEM at deallocation
         tc_commit_pair(drain);
         mbar_wait(drain, 0, nullptr, p.status);
       }
@@ -241,26 +344,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int w = pair; w < total; w += n_pairs) {
       const Tile t = decode<MODE, kPairBM>(p, tab, w);
       const bool empty = t.depth <= 0;
-      const uint32_t buf = tc & 1u;
       const int64_t row0 = MODE == kProductDw
                                ? static_cast<int64_t>(t.g) * p.cols + t.j0
                                : static_cast<int64_t>(t.j0);
-      if (!empty) {
-        int go = 1;
-        if (lane == 0)
-          go = mbar_wait(tfull0 + 8 * buf, (tc >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, go, 0)) break;
-        tc_fence_after();
+      bool ok = true;
+      for (int h = 0; h * hn < t.n_valid; ++h) {
+        const uint32_t buf = tc & 1u;
+        if (!empty) {
+          int go = 1;
+          if (lane == 0)
+            go = mbar_wait(tfull0 + 8 * buf, (tc >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
+          if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
+          tc_fence_after();
+        }
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
+        store_tile<MODE, T>(p, taddr, 16 * part, 32, min(hn, t.n_valid - h * hn), row0 + h * hn,
+                            t.f0 + static_cast<int>(rank) * kProductBM + q * 32, t.g, empty, stg,
+                            lane);
+        if (!empty) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty_leader + 8 * buf);
+          ++tc;
+        }
       }
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
-      store_tile<MODE, T>(p, taddr, 16 * part, 32, t.n_valid, row0,
-                          t.f0 + static_cast<int>(rank) * kProductBM + q * 32, t.g, empty, stg, lane);
-      if (!empty) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty_leader + 8 * buf);
-        ++tc;
-      }
+      if (!ok) break;
     }
   }
 
@@ -275,23 +383,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int MODE, typename T>
-cudaError_t launch(const ProductMaps& m, const ProductParams& p, size_t smem, int grid,
-                   cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(product_pair_kernel<MODE, T>,
+template <int MODE, int HALVES, typename T>
+cudaError_t launch(const ProductMaps& m, const ProductParams& p, int grid, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(product_pair_kernel<MODE, HALVES, T>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(product_pair_kernel<MODE, T>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                    smem, st, m.a, m.b, p);
+  return launch_pdl(product_pair_kernel<MODE, HALVES, T>, dim3(static_cast<unsigned>(grid)),
+                    dim3(kThreads), PairShape<HALVES>::kSmem + group_table_bytes(p.groups), st, m.a,
+                    m.b, p);
+}
+
+template <int MODE>
+cudaError_t launch_mode(bool bf16, const ProductMaps& m, const ProductParams& p, int grid,
+                        cudaStream_t st) {
+  if (p.bn <= kAccCols)
+    return bf16 ? launch<MODE, 1, __nv_bfloat16>(m, p, grid, st)
+                : launch<MODE, 1, __half>(m, p, grid, st);
+  return bf16 ? launch<MODE, 2, __nv_bfloat16>(m, p, grid, st)
+              : launch<MODE, 2, __half>(m, p, grid, st);
 }
 
 }  // namespace
 
 cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                                 int num_sms, cudaStream_t st) {
-  const size_t smem = 1024 + static_cast<size_t>(kStages) * kSlot +
-                      kEpiWarps * kEpiWarpBytes + kBarBytes +
-                      static_cast<size_t>(group_table_bytes(p.groups));
   const int64_t f_tiles = (p.feats + kPairBM - 1) / kPairBM;
   int64_t tiles;
   if (mode == kProductDw)
@@ -303,14 +418,9 @@ cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const
   if (tiles <= 0) return cudaSuccess;
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(std::min<int64_t>(2 * tiles, num_sms & ~1));
-  if (bf16) {
-    if (mode == kProductForward) return launch<kProductForward, __nv_bfloat16>(m, p, smem, grid, st);
-    if (mode == kProductDx) return launch<kProductDx, __nv_bfloat16>(m, p, smem, grid, st);
-    return launch<kProductDw, __nv_bfloat16>(m, p, smem, grid, st);
-  }
-  if (mode == kProductForward) return launch<kProductForward, __half>(m, p, smem, grid, st);
-  if (mode == kProductDx) return launch<kProductDx, __half>(m, p, smem, grid, st);
-  return launch<kProductDw, __half>(m, p, smem, grid, st);
+  if (mode == kProductForward) return launch_mode<kProductForward>(bf16, m, p, grid, st);
+  if (mode == kProductDx) return launch_mode<kProductDx>(bf16, m, p, grid, st);
+  return launch_mode<kProductDw>(bf16, m, p, grid, st);
 }
 
 }  // namespace moe

@@ -35,6 +35,7 @@ struct ProductParams {
   int cols;            // dw: J, the output's rows per group; else unused
   int depth;           // contraction length (forward K, dx N; dw: unused)
   int bn;              // rows per tile, a multiple of 16
+  int chunk;           // row blocks per ordering chunk
   int stages;          // pipeline slots
   int split;           // CTAs of a cluster sharing one tile's contraction
   void* out;
@@ -59,9 +60,11 @@ size_t product_slot_bytes(int mode, int bn);
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                            int num_sms, cudaStream_t st);
 
-// The same on CTA pairs (product_pair.cu): tiles of 256 features x bn <= 256
-// rows; map b's box is bn / 2 rows high (dw: 64 steps, as for one CTA).
-constexpr int kProductPairMaxBN = 256;
+// The same on CTA pairs (product_pair.cu): tiles of 256 features x bn rows, up
+// to 256 with one accumulator per tile, up to 512 with two; map b's box has
+// product_pair_box(bn) rows (dw: 64 steps, as for one CTA).
+constexpr int kProductPairMaxBN = 512;
+constexpr int product_pair_box(int bn) { return bn <= 256 ? bn / 2 : 128; }
 cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                                 int num_sms, cudaStream_t st);
 

@@ -252,38 +252,53 @@ int check_ws(const void* ws, size_t have, size_t need) {
   return ws == nullptr || !aligned(ws, kWsAlign) || have < need ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
-// Tile and split of a product: `blocks64` slots of 64 contraction steps,
-// `groups` groups of `mean` rows (dw: output rows) each.
+// Tile, split and order of a product: `blocks64` slots of 64 contraction
+// steps, `groups` groups of `mean` rows (dw: output rows) each.
 struct Choice {
   bool pair;
-  int bn, split;
+  int bn, split, chunk;
 };
 
+// Cycles of a CTA pair per 16 contraction steps of a tile of bn rows: with one
+// accumulator the MMAs follow each other every ~165 cycles whatever their
+// rows; with two, 128 cycles of work for the first 256 rows and at least ~88
+// for the second MMA (4096 x 4096 -> 1280, one wave: 53.7 us at 512 rows, 45.9
+// at 384, 45.4 at 320 and 304; two waves of 256 rows 59.8).
+int pair_step_cost(int bn) { return bn <= 256 ? 165 : 128 + std::max(88, (bn - 256) / 2); }
+
 Choice choose(int64_t feats, int64_t groups, int64_t mean, int64_t blocks64, int num_sms) {
+  Choice best{true, 0, 1, 1};
   if (mean > kProductMaxBN) {
     const int64_t f_tiles = (feats + 2 * kProductBM - 1) / (2 * kProductBM);
     const int64_t pairs = num_sms / 2;
-    Choice best{true, 0, 1};
-    int64_t best_cost = 0;
+    int64_t best_cost = 0, tiles = 0;
     for (int bn = kProductPairMaxBN; bn >= 128; bn -= 16) {
-      const int64_t tiles = groups * f_tiles * ((mean + bn - 1) / bn);
-      const int64_t cost = (tiles + pairs - 1) / pairs * std::max(104, bn / 2);
+      const int64_t n = groups * f_tiles * ((mean + bn - 1) / bn);
+      const int64_t cost = (n + pairs - 1) / pairs * pair_step_cost(bn);
       if (best.bn == 0 || cost < best_cost) {
         best.bn = bn;
         best_cost = cost;
+        tiles = n;
       }
     }
-    const int64_t tiles = groups * f_tiles * ((mean + best.bn - 1) / best.bn);
-    if (2 * tiles >= pairs) return best;
+    if (2 * tiles < pairs) best.bn = 0;
   }
-  int bn = 16;
-  while (bn < kProductMaxBN && bn < mean) bn *= 2;
-  const int64_t f_tiles = (feats + kProductBM - 1) / kProductBM;
-  const int64_t tiles = f_tiles * groups * ((mean + bn - 1) / bn);
-  int split = 1;
-  while (split < kProductMaxSplit && tiles * split * 2 <= num_sms && blocks64 >= 4 * split)
-    split *= 2;
-  return {false, bn, split};
+  if (best.bn == 0) {
+    best.pair = false;
+    best.bn = 16;
+    while (best.bn < kProductMaxBN && best.bn < mean) best.bn *= 2;
+    const int64_t f_tiles = (feats + kProductBM - 1) / kProductBM;
+    const int64_t tiles = f_tiles * groups * ((mean + best.bn - 1) / best.bn);
+    while (best.split < kProductMaxSplit && tiles * best.split * 2 <= num_sms &&
+           blocks64 >= 4 * best.split)
+      best.split *= 2;
+  }
+  // a chunk's rows stay in L2 across its weight tiles: up to 32 MB of them
+  // (4096 x 4096 -> 11264: 259 us with 8 blocks, 274 with 4; its dx, with rows
+  // of 22 KB, 254 with 2 and 272 with 8)
+  const int64_t block_bytes = static_cast<int64_t>(best.bn) * blocks64 * 128;
+  best.chunk = static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, (32 << 20) / block_bytes)));
+  return best;
 }
 
 // Groups that can have rows, and their mean size.
@@ -361,6 +376,7 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   filled(a->offsets, G, R, &n_groups, &mean);
   const Choice ch = choose(N, n_groups, mean, (K + 63) / 64, sms);
   p.bn = ch.bn;
+  p.chunk = ch.chunk;
   p.split = ch.split;
   p.out = a->out;
   p.ld_out = a->ld_out;
@@ -376,7 +392,7 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.status = status;
   ProductMaps m;
   if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, 64) ||
-      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, ch.pair ? p.bn / 2 : p.bn))
+      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, ch.pair ? product_pair_box(p.bn) : p.bn))
     return MOE_ERR_CUDA;
   MOE_CUDA(launch_any(ch, kProductForward, bf16, m, p, sms, st));
   return MOE_OK;
@@ -450,9 +466,10 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     filled(a->offsets, G, R, &n_groups, &mean);
     const Choice ch = choose(K, n_groups, mean, (N + 63) / 64, sms);
     p.bn = ch.bn;
+  p.chunk = ch.chunk;
     p.split = ch.split;
     if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, kProductBM) ||
-        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, 2, ch.pair ? p.bn / 2 : p.bn))
+        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, 2, ch.pair ? product_pair_box(p.bn) : p.bn))
       return MOE_ERR_CUDA;
     MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
   }
@@ -463,8 +480,9 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.out = a->dw;
     p.ld_out = N;
     p.vec_out = vec_rows(a->dw, N, N);
-    const Choice ch = choose(N, G, K, (R / G + 63) / 64, sms);
+    const Choice ch = choose(N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), sms);
     p.bn = ch.bn;
+  p.chunk = ch.chunk;
     p.split = ch.split;
     if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 2, 64) ||
         !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, 64))
