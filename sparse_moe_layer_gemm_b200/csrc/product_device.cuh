@@ -415,11 +415,13 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
 // One warp's part of a tile: lanes [32 q, 32 q + 32) of the accumulator at
 // taddr (quadrant and buffer included), 16-row chunks c0, c0 + step, ... below
 // n_valid; row0 the tile's first output row, f0 the warp's first feature.
-// zeros: the contraction was empty.
+// zeros: the contraction was empty.  chains accumulators, chain_cols columns
+// apart, are added.
 template <int MODE, typename T>
 __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t taddr, int c0, int step,
                                            int n_valid, int64_t row0, int f0, int g, bool zeros,
-                                           uint8_t* stg, int lane) {
+                                           uint8_t* stg, int lane, int chains = 1,
+                                           uint32_t chain_cols = 0) {
   const int nf = p.feats - f0;
   if (nf <= 0) return;
   // matrix m: features 8 m + lane / 4
@@ -456,6 +458,19 @@ __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t tadd
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           v[8 * k + 2 * m + e] = __uint_as_float(r[m >> 1][4 * k + 2 * (m & 1) + e]) + bias[m];
+    for (int h = 1; h < chains; ++h) {
+      if (zeros) break;
+      tmem_ld_16x256b_x2(taddr + h * chain_cols + c, r[0]);
+      tmem_ld_16x256b_x2(taddr + (16u << 16) + h * chain_cols + c, r[1]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            v[8 * k + 2 * m + e] += __uint_as_float(r[m >> 1][4 * k + 2 * (m & 1) + e]);
+    }
     // the next chunk's load runs below this one's arithmetic and stores
     if (!zeros && c + step < n_valid) {
       tmem_ld_16x256b_x2(taddr + c + step, r[0]);

@@ -17,6 +17,11 @@
 // rank order (the same sum on every run; no workspace, no counters) and
 // finishes the row.
 //
+// MMAs into one accumulator follow one another only every ~250 cycles at these
+// tile sizes (64 slots of a 16-row tile took 35 us, 16 KB per 1000 cycles,
+// below what one SM's share of HBM delivers), so a tile keeps 2 or 4
+// accumulators, takes them in turn step by step and adds them at the end.
+//
 // Roles per CTA (6 warps): warp 0 TMA producer, warp 1 tensor memory and MMA
 // issue, warps 2-5 epilogue (one accumulator lane quadrant each).  Persistent
 // over tiles w = cluster, cluster + clusters, ...; the accumulator is
@@ -57,6 +62,13 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// This CTA's slots [kb0, kb1) of a contraction shared by `split` CTAs.
+__device__ __forceinline__ void my_slots(int depth, int rank, int split, int* kb0, int* kb1) {
+  const int nkb = (depth + 63) >> 6;
+  *kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / split);
+  *kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
+}
+
 template <int MODE, typename T>
 __global__ void __launch_bounds__(kThreads, 2)
     product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -87,9 +99,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster = blockIdx.x / split;
   const int clusters = gridDim.x / split;
-  // accumulator columns, two buffers (a power of two, at least 32)
-  uint32_t acc_cols = 16;
-  while (acc_cols < static_cast<uint32_t>(p.bn)) acc_cols <<= 1;
+  // columns of one accumulator (a power of two); a tile's accumulators, and two
+  // sets of them except where the CTA has one tile
+  uint32_t chain_cols = 16;
+  while (chain_cols < static_cast<uint32_t>(p.bn)) chain_cols <<= 1;
+  const int chains = p.bn <= 64 ? 4 : 2;
+  const uint32_t acc_cols = chains * chain_cols;
+  const uint32_t tmem_cols = split > 1 ? acc_cols : 2 * acc_cols;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -110,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     prefetch_tmap(&tmB);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 2 * acc_cols);
+    tmem_alloc(smem_u32(tmem_slot), tmem_cols);
     tmem_relinquish();
   }
   pdl_wait();
@@ -129,24 +145,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_normal();
-      uint32_t it = 0;
+      uint32_t it = 0, s = 0, ph = 0;
       bool ok = true;
       for (int w = cluster; w < total && ok; w += clusters) {
         const Tile t = decode<MODE, kProductBM>(p, tab, w);
-        const int nkb = (t.depth + 63) >> 6;
-        const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
-        for (int kb = static_cast<int>(static_cast<int64_t>(nkb) * rank / split); kb < kb1; ++kb) {
-          const uint32_t s = it % stages;
-          const uint32_t ph = (it / stages) & 1u;
+        int kb0, kb1;
+        my_slots(t.depth, rank, split, &kb0, &kb1);
+        for (int c = t.c0 + kb0 * 64, c1 = t.c0 + kb1 * 64; c < c1; c += 64) {
           if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
           }
           const uint32_t bar = full0 + 8 * s;
           mbar_arrive_expect_tx(bar, slot_bytes);
-          const uint32_t sa = smem_u32(smem + s * slot_bytes);
+          const uint32_t sa = smem_u32(smem) + s * slot_bytes;
           const uint32_t sb = sa + kABytes;
-          const int c = t.c0 + kb * 64;
           if (MODE == kProductForward) {
             tma_load_3d(sa, &tmA, bar, t.f0, c, t.g, pol);
             tma_load_3d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, t.g, pol);
@@ -163,6 +176,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             tma_load_2d(sb, &tmB, bar, c, t.j0, pol);
           }
           ++it;
+          if (++s == static_cast<uint32_t>(stages)) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       }
       // every load issued lands before the CTA can end
@@ -174,13 +191,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    uint32_t it = 0, tc = 0;
-    bool ok = true;
-    for (int w = cluster; w < total && ok; w += clusters) {
+    constexpr uint64_t kStepA = (kAMn ? 2048 : 32) >> 4;
+    constexpr uint64_t kStepB = (kBMn ? 2048 : 32) >> 4;
+    const uint32_t sa0 = smem_u32(smem);
+    const uint64_t ad0 = kAMn ? sdesc_mn_sw128(sa0) : sdesc_k_sw<128>(sa0);
+    const uint64_t bd0 = kBMn ? sdesc_mn_sw128(sa0 + kABytes) : sdesc_k_sw<128>(sa0 + kABytes);
+    uint32_t s = 0, ph = 0, tc = 0;
+    bool any = false, ok = true;
+    // (the whole warp walks the tiles for dw, whose last slots it clears)
+    for (int w = cluster; w < total && ok && (MODE == kProductDw || lane == 0); w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
-      const int nkb = (t.depth + 63) >> 6;
-      const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / split);
-      const int kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
+      int kb0, kb1;
+      my_slots(t.depth, rank, split, &kb0, &kb1);
       if (kb0 == kb1) continue;  // nothing to add: the epilogue takes zeros
       const uint32_t idesc =
           product_idesc(is_bf16<T>(), kAMn, kBMn, kProductBM, (t.n_valid + 15) & ~15);
@@ -188,23 +210,24 @@ __global__ void __launch_bounds__(kThreads, 2)
       int go = 1;
       if (lane == 0)
         go = mbar_wait(tempty0 + 8 * buf, ((tc >> 1) & 1u) ^ 1u, abort_flag, p.status) ? 1 : 0;
-      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      if (MODE == kProductDw) go = __shfl_sync(0xffffffffu, go, 0);
+      if (!go) break;
       tc_fence_after();
+      any = true;
       const uint32_t d = tmem_base + buf * acc_cols;
       for (int kb = kb0; kb < kb1; ++kb) {
-        const uint32_t s = it % stages;
-        if (lane == 0)
-          go = mbar_wait(full0 + 8 * s, (it / stages) & 1u, abort_flag, p.status) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, go, 0)) {
+        if (lane == 0) go = mbar_wait(full0 + 8 * s, ph, abort_flag, p.status) ? 1 : 0;
+        if (MODE == kProductDw) go = __shfl_sync(0xffffffffu, go, 0);
+        if (!go) {
           ok = false;
           break;
         }
-        uint8_t* slot = smem + s * slot_bytes;
         const int left = t.depth - kb * 64;  // contraction steps that exist from here on
         const int steps = min(4, (left + 15) >> 4);
         if (MODE == kProductDw && (left & 15) != 0 && left < 64 && t.c0 + t.depth < p.rows) {
           // steps [left, steps * 16) are another group's rows (behind the tensor's last
           // row the load fills zeros): clear them in every box
+          uint8_t* slot = smem + s * slot_bytes;
           const int n16 = (steps * 16 - left) * 8;  // 16-byte pieces per box
           const int boxes = slot_bytes / kSubBytes;
           for (int i = lane; i < n16 * boxes; i += 32) {
@@ -217,24 +240,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (lane == 0) {
           tc_fence_after();
-          const uint32_t sa = smem_u32(slot);
-          const uint64_t ad = kAMn ? sdesc_mn_sw128(sa) : sdesc_k_sw<128>(sa);
-          const uint64_t bd = kBMn ? sdesc_mn_sw128(sa + kABytes) : sdesc_k_sw<128>(sa + kABytes);
-          constexpr uint64_t kStepA = (kAMn ? 2048 : 32) >> 4;
-          constexpr uint64_t kStepB = (kBMn ? 2048 : 32) >> 4;
+          const uint64_t at = static_cast<uint64_t>((s * slot_bytes) >> 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (i < steps)
-              tc_mma_bf16(d, ad + i * kStepA, bd + i * kStepB, idesc, (kb > kb0 || i > 0) ? 1u : 0u);
+              tc_mma_bf16(d + (chains == 4 ? i : i & 1) * chain_cols, ad0 + at + i * kStepA,
+                          bd0 + at + i * kStepB, idesc, (kb > kb0 || i >= chains) ? 1u : 0u);
           tc_commit(empty0 + 8 * s);
           if (kb == kb1 - 1) tc_commit(tfull0 + 8 * buf);
         }
-        __syncwarp();
-        ++it;
+        if (++s == static_cast<uint32_t>(stages)) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
       ++tc;
     }
-    if (lane == 0 && it > 0) {  // no MMA may still be writing TMEM at deallocation
+    if (lane == 0 && any) {  // no MMA may still be writing TMEM at deallocation
       tc_commit(drain);
       mbar_wait(drain, 0, nullptr, p.status);
     }
@@ -246,9 +268,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint8_t* stg = reinterpret_cast<uint8_t*>(xch) + (warp - 2) * kEpiWarpBytes;
     for (int w = cluster; w < total; w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
-      const int nkb = (t.depth + 63) >> 6;
-      const bool empty = static_cast<int64_t>(nkb) * rank / split ==
-                         static_cast<int64_t>(nkb) * (rank + 1) / split;
+      int kb0, kb1;
+      my_slots(t.depth, rank, split, &kb0, &kb1);
+      const bool empty = kb0 == kb1;
+      // accumulators in use: all, unless the only slot has fewer steps
+      const int used = kb1 - kb0 > 1 ? chains : min(chains, (t.depth - kb0 * 64 + 15) >> 4);
       const uint32_t buf = tc & 1u;
       const int feat = t.f0 + q * 32 + lane;
       const bool live = feat < p.feats;
@@ -267,27 +291,36 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
       const int share = (t.n_valid + split - 1) / split;  // rows each CTA of the cluster finishes
-      const uint32_t xch_addr = smem_u32(xch) + (q * 32 + lane) * 4;
+      // where the row's owner takes this CTA's partial of this lane's feature
+      const uint32_t xch_addr = smem_u32(xch) + (rank * share * kProductBM + q * 32 + lane) * 4;
       if (split == 1) {
-        store_tile<MODE, T>(p, taddr, 0, 16, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
+        store_tile<MODE, T>(p, taddr, 0, 16, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane,
+                            used, chain_cols);
       } else {
+        int owner = 0, local = 0;  // the row's CTA and its place there
+        uint32_t at = mapa_shared(xch_addr, 0);
         for (int c = 0; c < t.n_valid; c += 16) {
-          uint32_t r[16];
-          if (empty) {
+          float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[i] = 0;
-          } else {
-            tmem_ld_x16(taddr + c, r);
-            tmem_ld_wait();
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          if (!empty) {
+            for (int h = 0; h < used; ++h) {
+              uint32_t r[16];
+              tmem_ld_x16(taddr + h * chain_cols + c, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i < t.n_valid) {
-              const int owner = (c + i) / share;
-              const uint32_t at =
-                  xch_addr + (rank * share + (c + i) - owner * share) * (kProductBM * 4);
-              st_cluster_f32(mapa_shared(at, owner), __uint_as_float(r[i]));
+          for (int i = 0; i < 16; ++i) {
+            if (c + i >= t.n_valid) break;
+            st_cluster_f32(at + local * (kProductBM * 4), v[i]);
+            if (++local == share) {
+              local = 0;
+              if (++owner < split) at = mapa_shared(xch_addr, owner);
             }
+          }
         }
       }
       if (!empty) {
@@ -308,9 +341,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
         const int mine = min(share, t.n_valid - rank * share);
         for (int j = 0; j < mine; ++j) {
+          float part[kProductMaxSplit];
+#pragma unroll
+          for (int s = 0; s < kProductMaxSplit; ++s)
+            part[s] = s < split ? xch[(s * share + j) * kProductBM + q * 32 + lane] : 0.f;
           float v = 0.f;
-          for (int s = 0; s < split; ++s)
-            v += xch[(s * share + j) * kProductBM + q * 32 + lane];
+#pragma unroll
+          for (int s = 0; s < kProductMaxSplit; ++s) v += part[s];
           if (live) finish_value<MODE, T>(p, row0 + rank * share + j, feat, b, v);
         }
       }
@@ -322,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (split > 1) cluster_sync_all();  // no CTA leaves while its peers may still reach it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 2 * acc_cols);
+    tmem_dealloc(tmem_base, tmem_cols);
   }
 }
 
