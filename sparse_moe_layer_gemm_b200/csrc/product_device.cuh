@@ -187,6 +187,26 @@ __device__ __forceinline__ int group_of_block(const GroupTable& t, int groups, i
   return lo;
 }
 
+// One lane of the (converged) warp, the same at every call.  The tcgen05 and
+// TMA instructions take warp-uniform registers: issued inside a loop that the
+// whole warp walks, under this predicate, their operands stay there; a loop
+// walked by one lane alone cost ~590 cycles per slot on top of its MMAs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// mbar_wait by the whole warp, which continues or stops together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
 constexpr int kSubBytes = 64 * 128;  // one MN-major box: 64 steps x 64 elements
 
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
@@ -415,13 +435,11 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
 // One warp's part of a tile: lanes [32 q, 32 q + 32) of the accumulator at
 // taddr (quadrant and buffer included), 16-row chunks c0, c0 + step, ... below
 // n_valid; row0 the tile's first output row, f0 the warp's first feature.
-// zeros: the contraction was empty.  chains accumulators, chain_cols columns
-// apart, are added.
+// zeros: the contraction was empty.
 template <int MODE, typename T>
 __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t taddr, int c0, int step,
                                            int n_valid, int64_t row0, int f0, int g, bool zeros,
-                                           uint8_t* stg, int lane, int chains = 1,
-                                           uint32_t chain_cols = 0) {
+                                           uint8_t* stg, int lane) {
   const int nf = p.feats - f0;
   if (nf <= 0) return;
   // matrix m: features 8 m + lane / 4
@@ -458,19 +476,6 @@ __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t tadd
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           v[8 * k + 2 * m + e] = __uint_as_float(r[m >> 1][4 * k + 2 * (m & 1) + e]) + bias[m];
-    for (int h = 1; h < chains; ++h) {
-      if (zeros) break;
-      tmem_ld_16x256b_x2(taddr + h * chain_cols + c, r[0]);
-      tmem_ld_16x256b_x2(taddr + (16u << 16) + h * chain_cols + c, r[1]);
-      tmem_ld_wait();
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            v[8 * k + 2 * m + e] += __uint_as_float(r[m >> 1][4 * k + 2 * (m & 1) + e]);
-    }
     // the next chunk's load runs below this one's arithmetic and stores
     if (!zeros && c + step < n_valid) {
       tmem_ld_16x256b_x2(taddr + c + step, r[0]);

@@ -11,21 +11,20 @@
 // copies.
 //
 // Few tiles (a decode batch): `split` CTAs of a cluster share a tile, each
-// taking a part of its contraction.  The parts meet in shared memory over the
-// cluster: the rows of the tile are dealt out to the CTAs, every CTA sends
-// its fp32 partial of a row to the row's owner, and the owner adds them in
-// rank order (the same sum on every run; no workspace, no counters) and
-// finishes the row.
-//
-// MMAs into one accumulator follow one another only every ~250 cycles at these
-// tile sizes (64 slots of a 16-row tile took 35 us, 16 KB per 1000 cycles,
-// below what one SM's share of HBM delivers), so a tile keeps 2 or 4
-// accumulators, takes them in turn step by step and adds them at the end.
+// taking a part of its contraction.  Every CTA leaves its fp32 partial in its
+// own shared memory (the pipeline's, done by then); the rows of the tile are
+// dealt out to the CTAs, which read the others' partials of their rows over
+// the cluster and add them in rank order: the same sum on every run, no
+// workspace, no counters.
 //
 // Roles per CTA (6 warps): warp 0 TMA producer, warp 1 tensor memory and MMA
 // issue, warps 2-5 epilogue (one accumulator lane quadrant each).  Persistent
 // over tiles w = cluster, cluster + clusters, ...; the accumulator is
-// double-buffered.  Every wait is bounded (moe_ptx.cuh).
+// double-buffered.  A slot holds two sub-slots of 64 steps: with few rows the
+// weights stream no faster than the issuing warps turn slots over (16-row
+// tile, 64 x 64 steps: 35.6 us with one-lane loops, 22.5 with whole-warp loops
+// and elect, and two sub-slots per turn on top).  Every wait is bounded
+// (moe_ptx.cuh).
 //
 // Weight gradient: the contraction runs over the group's rows, which end
 // inside a slot; the rows behind the last one belong to the next group.  The
@@ -44,7 +43,9 @@ using namespace product;
 
 constexpr int kThreads = 32 * 6;
 constexpr int kABytes = 2 * kSubBytes;
-constexpr int kMaxStages = 12;
+constexpr int kSubs = 2;  // sub-slots of 64 contraction steps per slot
+constexpr int kMaxStages = 6;
+constexpr int kEpiBytes = 4 * kEpiWarpBytes;
 constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
 
 // bytes of the B operand of one slot
@@ -52,17 +53,13 @@ __host__ __device__ constexpr int b_bytes(int mode, int bn) {
   return mode == kProductDw ? (bn + 63) / 64 * kSubBytes : bn * 128;
 }
 
-// fp32 partials received for this CTA's share of a tile's rows (split), or the
-// epilogue warps' staged chunks
-__host__ __device__ constexpr int exchange_bytes(int split, int bn) {
-  return split > 1 ? split * ((bn + split - 1) / split) * kProductBM * 4 : 4 * kEpiWarpBytes;
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// This CTA's slots [kb0, kb1) of a contraction shared by `split` CTAs.
+// This CTA's sub-slots [kb0, kb1) of a contraction shared by `split` CTAs.
 __device__ __forceinline__ void my_slots(int depth, int rank, int split, int* kb0, int* kb1) {
   const int nkb = (depth + 63) >> 6;
   *kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / split);
@@ -79,10 +76,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int stages = p.stages;
-  const int slot_bytes = kABytes + b_bytes(MODE, p.bn);
-  float* xch = reinterpret_cast<float*>(smem + stages * slot_bytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xch) +
-                                               exchange_bytes(p.split, p.bn));
+  const int sub_bytes = kABytes + b_bytes(MODE, p.bn);
+  const int slot_bytes = kSubs * sub_bytes;
+  uint8_t* epi = smem + stages * slot_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + kEpiBytes);
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = full0 + 8 * kMaxStages;
   const uint32_t tfull0 = empty0 + 8 * kMaxStages;
@@ -99,13 +96,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster = blockIdx.x / split;
   const int clusters = gridDim.x / split;
-  // columns of one accumulator (a power of two); a tile's accumulators, and two
-  // sets of them except where the CTA has one tile
-  uint32_t chain_cols = 16;
-  while (chain_cols < static_cast<uint32_t>(p.bn)) chain_cols <<= 1;
-  const int chains = p.bn <= 64 ? 4 : 2;
-  const uint32_t acc_cols = chains * chain_cols;
-  const uint32_t tmem_cols = split > 1 ? acc_cols : 2 * acc_cols;
+  // accumulator columns, two buffers (a power of two, at least 32)
+  uint32_t acc_cols = 16;
+  while (acc_cols < static_cast<uint32_t>(p.bn)) acc_cols <<= 1;
+  const uint32_t tmem_cols = 2 * acc_cols;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
@@ -143,50 +137,54 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
-      uint32_t it = 0, s = 0, ph = 0;
-      bool ok = true;
-      for (int w = cluster; w < total && ok; w += clusters) {
-        const Tile t = decode<MODE, kProductBM>(p, tab, w);
-        int kb0, kb1;
-        my_slots(t.depth, rank, split, &kb0, &kb1);
-        for (int c = t.c0 + kb0 * 64, c1 = t.c0 + kb1 * 64; c < c1; c += 64) {
-          if (!mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+    const uint64_t pol = l2_policy_evict_normal();
+    uint32_t it = 0, s = 0, ph = 0;
+    bool ok = true;
+    for (int w = cluster; w < total && ok; w += clusters) {
+      const Tile t = decode<MODE, kProductBM>(p, tab, w);
+      int kb0, kb1;
+      my_slots(t.depth, rank, split, &kb0, &kb1);
+      for (int kb = kb0; kb < kb1; kb += kSubs) {
+        if (!(ok = warp_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status))) break;
+        const int subs = min(kSubs, kb1 - kb);
+        if (elect_one()) {
           const uint32_t bar = full0 + 8 * s;
-          mbar_arrive_expect_tx(bar, slot_bytes);
-          const uint32_t sa = smem_u32(smem) + s * slot_bytes;
-          const uint32_t sb = sa + kABytes;
-          if (MODE == kProductForward) {
-            tma_load_3d(sa, &tmA, bar, t.f0, c, t.g, pol);
-            tma_load_3d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, t.g, pol);
-          } else if (MODE == kProductDx) {
-            tma_load_3d(sa, &tmA, bar, c, t.f0, t.g, pol);
-          } else {
-            tma_load_2d(sa, &tmA, bar, t.f0, c, pol);
-            tma_load_2d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, pol);
-          }
-          if (kBMn) {
-            for (int h = 0; h < p.bn; h += 64)
-              tma_load_2d(sb + h * 128, &tmB, bar, t.j0 + h, c, pol);
-          } else {
-            tma_load_2d(sb, &tmB, bar, c, t.j0, pol);
-          }
-          ++it;
-          if (++s == static_cast<uint32_t>(stages)) {
-            s = 0;
-            ph ^= 1u;
+          mbar_arrive_expect_tx(bar, subs * sub_bytes);
+          uint32_t sa = smem_u32(smem) + s * slot_bytes;
+          int c = t.c0 + kb * 64;
+          for (int i = 0; i < subs; ++i, sa += sub_bytes, c += 64) {
+            const uint32_t sb = sa + kABytes;
+            if (MODE == kProductForward) {
+              tma_load_3d(sa, &tmA, bar, t.f0, c, t.g, pol);
+              tma_load_3d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, t.g, pol);
+            } else if (MODE == kProductDx) {
+              tma_load_3d(sa, &tmA, bar, c, t.f0, t.g, pol);
+            } else {
+              tma_load_2d(sa, &tmA, bar, t.f0, c, pol);
+              tma_load_2d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, pol);
+            }
+            if (kBMn) {
+              tma_load_2d(sb, &tmB, bar, t.j0, c, pol);
+              if (p.bn > 64) tma_load_2d(sb + kSubBytes, &tmB, bar, t.j0 + 64, c, pol);
+            } else {
+              tma_load_2d(sb, &tmB, bar, c, t.j0, pol);
+            }
           }
         }
+        __syncwarp();
+        ++it;
+        if (++s == static_cast<uint32_t>(stages)) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
-      // every load issued lands before the CTA can end
+    }
+    // every load issued lands before the CTA can end
+    if (lane == 0) {
       const uint32_t used = it < static_cast<uint32_t>(stages) ? it : stages;
-      for (uint32_t s = 0; s < used; ++s) {
-        const uint32_t last = (it - 1u) - ((it - 1u - s) % stages);
-        mbar_wait(full0 + 8 * s, (last / stages) & 1u, nullptr, p.status);
+      for (uint32_t q = 0; q < used; ++q) {
+        const uint32_t last = (it - 1u) - ((it - 1u - q) % stages);
+        mbar_wait(full0 + 8 * q, (last / stages) & 1u, nullptr, p.status);
       }
     }
   } else if (warp == 1) {
@@ -198,8 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint64_t bd0 = kBMn ? sdesc_mn_sw128(sa0 + kABytes) : sdesc_k_sw<128>(sa0 + kABytes);
     uint32_t s = 0, ph = 0, tc = 0;
     bool any = false, ok = true;
-    // (the whole warp walks the tiles for dw, whose last slots it clears)
-    for (int w = cluster; w < total && ok && (MODE == kProductDw || lane == 0); w += clusters) {
+    for (int w = cluster; w < total && ok; w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
       int kb0, kb1;
       my_slots(t.depth, rank, split, &kb0, &kb1);
@@ -207,48 +204,58 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t idesc =
           product_idesc(is_bf16<T>(), kAMn, kBMn, kProductBM, (t.n_valid + 15) & ~15);
       const uint32_t buf = tc & 1u;
-      int go = 1;
-      if (lane == 0)
-        go = mbar_wait(tempty0 + 8 * buf, ((tc >> 1) & 1u) ^ 1u, abort_flag, p.status) ? 1 : 0;
-      if (MODE == kProductDw) go = __shfl_sync(0xffffffffu, go, 0);
-      if (!go) break;
+      if (!warp_wait(tempty0 + 8 * buf, ((tc >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
       tc_fence_after();
       any = true;
       const uint32_t d = tmem_base + buf * acc_cols;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (lane == 0) go = mbar_wait(full0 + 8 * s, ph, abort_flag, p.status) ? 1 : 0;
-        if (MODE == kProductDw) go = __shfl_sync(0xffffffffu, go, 0);
-        if (!go) {
-          ok = false;
-          break;
-        }
-        const int left = t.depth - kb * 64;  // contraction steps that exist from here on
-        const int steps = min(4, (left + 15) >> 4);
-        if (MODE == kProductDw && (left & 15) != 0 && left < 64 && t.c0 + t.depth < p.rows) {
-          // steps [left, steps * 16) are another group's rows (behind the tensor's last
-          // row the load fills zeros): clear them in every box
-          uint8_t* slot = smem + s * slot_bytes;
-          const int n16 = (steps * 16 - left) * 8;  // 16-byte pieces per box
-          const int boxes = slot_bytes / kSubBytes;
+      uint32_t acc = 0;
+      for (int kb = kb0; kb < kb1; kb += kSubs) {
+        if (!(ok = warp_wait(full0 + 8 * s, ph, abort_flag, p.status))) break;
+        // contraction steps of this CTA that exist from here on
+        const int left = min(t.depth, kb1 * 64) - kb * 64;
+        if (MODE == kProductDw && (left & 15) != 0 && left < 64 * kSubs &&
+            t.c0 + t.depth < p.rows) {
+          // up to the next multiple of 16 the steps are another group's rows (behind
+          // the tensor's last row the load fills zeros): clear them in every box
+          uint8_t* sub = smem + s * slot_bytes + (left >> 6) * sub_bytes;
+          const int from = left & 63;
+          const int n16 = (((from + 15) & ~15) - from) * 8;  // 16-byte pieces per box
+          const int boxes = sub_bytes / kSubBytes;
           for (int i = lane; i < n16 * boxes; i += 32) {
             const int box = i / n16;
-            *reinterpret_cast<uint4*>(slot + box * kSubBytes + left * 128 + (i - box * n16) * 16) =
+            *reinterpret_cast<uint4*>(sub + box * kSubBytes + from * 128 + (i - box * n16) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0) {
-          tc_fence_after();
-          const uint64_t at = static_cast<uint64_t>((s * slot_bytes) >> 4);
+        tc_fence_after();
+        if (elect_one()) {
+          uint64_t ad = ad0 + static_cast<uint64_t>((s * slot_bytes) >> 4);
+          uint64_t bd = bd0 + static_cast<uint64_t>((s * slot_bytes) >> 4);
+          if (left > 64 * kSubs - 16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < steps)
-              tc_mma_bf16(d + (chains == 4 ? i : i & 1) * chain_cols, ad0 + at + i * kStepA,
-                          bd0 + at + i * kStepB, idesc, (kb > kb0 || i >= chains) ? 1u : 0u);
+            for (int h = 0; h < kSubs; ++h) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                tc_mma_bf16(d, ad + i * kStepA, bd + i * kStepB, idesc, h + i > 0 ? 1u : acc);
+              ad += sub_bytes >> 4;
+              bd += sub_bytes >> 4;
+            }
+          } else {
+            for (int i = 0; i < (left + 15) >> 4; ++i) {
+              if (i == 4) {
+                ad += (sub_bytes >> 4) - 4 * kStepA;
+                bd += (sub_bytes >> 4) - 4 * kStepB;
+              }
+              tc_mma_bf16(d, ad + i * kStepA, bd + i * kStepB, idesc, i > 0 ? 1u : acc);
+            }
+          }
           tc_commit(empty0 + 8 * s);
-          if (kb == kb1 - 1) tc_commit(tfull0 + 8 * buf);
+          if (kb + kSubs >= kb1) tc_commit(tfull0 + 8 * buf);
         }
+        __syncwarp();
+        acc = 1;
         if (++s == static_cast<uint32_t>(stages)) {
           s = 0;
           ph ^= 1u;
@@ -256,8 +263,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       ++tc;
     }
-    if (lane == 0 && any) {  // no MMA may still be writing TMEM at deallocation
-      tc_commit(drain);
+    if (any) {  // no MMA may still be writing TMEM at deallocation
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
       mbar_wait(drain, 0, nullptr, p.status);
     }
   } else {
@@ -265,14 +273,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int q = warp & 3;  // the TMEM lane quadrant this warp may read
     uint32_t tc = 0;
     const T* bias = static_cast<const T*>(p.bias);
-    uint8_t* stg = reinterpret_cast<uint8_t*>(xch) + (warp - 2) * kEpiWarpBytes;
+    uint8_t* stg = epi + (warp - 2) * kEpiWarpBytes;
     for (int w = cluster; w < total; w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
       int kb0, kb1;
       my_slots(t.depth, rank, split, &kb0, &kb1);
       const bool empty = kb0 == kb1;
-      // accumulators in use: all, unless the only slot has fewer steps
-      const int used = kb1 - kb0 > 1 ? chains : min(chains, (t.depth - kb0 * 64 + 15) >> 4);
       const uint32_t buf = tc & 1u;
       const int feat = t.f0 + q * 32 + lane;
       const bool live = feat < p.feats;
@@ -290,67 +296,55 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
-      const int share = (t.n_valid + split - 1) / split;  // rows each CTA of the cluster finishes
-      // where the row's owner takes this CTA's partial of this lane's feature
-      const uint32_t xch_addr = smem_u32(xch) + (rank * share * kProductBM + q * 32 + lane) * 4;
       if (split == 1) {
-        store_tile<MODE, T>(p, taddr, 0, 16, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane,
-                            used, chain_cols);
-      } else {
-        int owner = 0, local = 0;  // the row's CTA and its place there
-        uint32_t at = mapa_shared(xch_addr, 0);
-        for (int c = 0; c < t.n_valid; c += 16) {
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = 0.f;
-          if (!empty) {
-            for (int h = 0; h < used; ++h) {
-              uint32_t r[16];
-              tmem_ld_x16(taddr + h * chain_cols + c, r);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (c + i >= t.n_valid) break;
-            st_cluster_f32(at + local * (kProductBM * 4), v[i]);
-            if (++local == share) {
-              local = 0;
-              if (++owner < split) at = mapa_shared(xch_addr, owner);
-            }
-          }
+        store_tile<MODE, T>(p, taddr, 0, 16, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
+        if (!empty) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty0 + 8 * buf);
+          ++tc;
         }
+        continue;
       }
-      if (!empty) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty0 + 8 * buf);
-        ++tc;
-      }
-      if (split > 1) {
-        // one tile per cluster in this form (the launch has a cluster per
-        // tile), so the exchange area is written once
-        __syncwarp();
-        if (lane < split) mbar_arrive_cluster(mapa_shared(xfull, lane));
-        int go = 1;
-        if (lane == 0) go = mbar_wait_cluster(xfull, 0, abort_flag, p.status) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, go, 0)) break;
-        // the waiting lane's acquire orders the other lanes' reads too
-        __syncwarp();
-        const int mine = min(share, t.n_valid - rank * share);
-        for (int j = 0; j < mine; ++j) {
-          float part[kProductMaxSplit];
+      // one tile per cluster in this form (the launch has a cluster per tile):
+      // the partial goes where the slots were, [row][128 features]
+      float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
+      for (int c = 0; c < t.n_valid; c += 16) {
+        uint32_t r[16];
+        if (empty) {
 #pragma unroll
-          for (int s = 0; s < kProductMaxSplit; ++s)
-            part[s] = s < split ? xch[(s * share + j) * kProductBM + q * 32 + lane] : 0.f;
-          float v = 0.f;
-#pragma unroll
-          for (int s = 0; s < kProductMaxSplit; ++s) v += part[s];
-          if (live) finish_value<MODE, T>(p, row0 + rank * share + j, feat, b, v);
+          for (int i = 0; i < 16; ++i) r[i] = 0;
+        } else {
+          tmem_ld_x16(taddr + c, r);
+          tmem_ld_wait();
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < t.n_valid) part[(c + i) * kProductBM] = __uint_as_float(r[i]);
       }
+      __syncwarp();
+      if (lane < split) mbar_arrive_cluster(mapa_shared(xfull, lane));
+      int go = 1;
+      if (lane == 0) go = mbar_wait_cluster(xfull, 0, abort_flag, p.status) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      const int share = (t.n_valid + split - 1) / split;  // rows this CTA finishes
+      const int mine = min(share, t.n_valid - rank * share);
+      const uint32_t own = smem_u32(part) + rank * share * (kProductBM * 4);
+      uint32_t from[kProductMaxSplit];
+#pragma unroll
+      for (int k = 0; k < kProductMaxSplit; ++k) from[k] = mapa_shared(own, min(k, split - 1));
+#pragma unroll 2
+      for (int j = 0; j < mine; ++j) {
+        float got[kProductMaxSplit];
+#pragma unroll
+        for (int k = 0; k < kProductMaxSplit; ++k)
+          got[k] = k < split ? ld_cluster_f32(from[k] + j * (kProductBM * 4)) : 0.f;
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kProductMaxSplit; ++k) v += got[k];
+        if (live) finish_value<MODE, T>(p, row0 + rank * share + j, feat, b, v);
+      }
+      break;
     }
   }
 
@@ -388,16 +382,12 @@ cudaError_t launch(const ProductMaps& m, const ProductParams& p, size_t smem, in
 
 }  // namespace
 
-size_t product_slot_bytes(int mode, int bn) {
-  return static_cast<size_t>(kABytes) + b_bytes(mode, bn);
-}
-
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p0,
                            int num_sms, cudaStream_t st) {
   ProductParams p = p0;
-  const size_t fixed = 1024 + exchange_bytes(p.split, p.bn) + kBarBytes +
+  const size_t fixed = 1024 + kEpiBytes + kBarBytes +
                        static_cast<size_t>(group_table_bytes(p.groups));
-  const size_t slot = product_slot_bytes(mode, p.bn);
+  const size_t slot = kSubs * (kABytes + static_cast<size_t>(b_bytes(mode, p.bn)));
   const int64_t f_tiles = (p.feats + kProductBM - 1) / kProductBM;
   // the most tiles the launch can have (a ragged problem's count is known on the device only)
   int64_t tiles;

@@ -131,8 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full_leader = mapa_shared(full0, 0);
     uint32_t it = 0, tails = 0, s = 0, ph = 0;
     bool ok = true;
-    // (the whole warp walks the tiles for dw, whose last slots it clears)
-    for (int w = pair; w < total && ok && (MODE == kProductDw || lane == 0); w += n_pairs) {
+    for (int w = pair; w < total && ok; w += n_pairs) {
       const Tile t = decode<MODE, kPairBM>(p, tab, w);
       const int f = t.f0 + static_cast<int>(rank) * kProductBM;
       // this CTA's first row in each half's MMA
@@ -147,47 +146,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int left = t.depth, c = t.c0; left > 0; left -= 64, c += 64) {
         const bool clear = MODE == kProductDw && left < 64 && (left & 15) != 0 &&
                            t.c0 + t.depth < p.rows;
-        int go = 1;
-        if (lane == 0) {
-          go = mbar_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status) ? 1 : 0;
-          if (go) {
-            if (clear) {
-              mbar_arrive_expect_tx(tail, box_bytes);
-            } else if (rank == 0) {
-              mbar_arrive_expect_tx(full0 + 8 * s, 2 * box_bytes);
-              mbar_arrive(full0 + 8 * s);
-            }
-            const uint32_t bar = clear ? mapa_shared(tail, rank) : full_leader + 8 * s;
-            const uint32_t sa = smem_u32(smem) + s * kSlot;
-            const uint32_t sb = sa + kOperand;
-            if (MODE == kProductForward) {
-              tma_load_3d_pair(sa, &tmA, bar, f, c, t.g, pol);
-              tma_load_3d_pair(sa + kSubBytes, &tmA, bar, f + 64, c, t.g, pol);
-            } else if (MODE == kProductDx) {
-              tma_load_3d_pair(sa, &tmA, bar, c, f, t.g, pol);
-            } else {
-              tma_load_2d_pair(sa, &tmA, bar, f, c, pol);
-              tma_load_2d_pair(sa + kSubBytes, &tmA, bar, f + 64, c, pol);
-            }
+        if (!(ok = warp_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status))) break;
+        if (elect_one()) {
+          if (clear) {
+            mbar_arrive_expect_tx(tail, box_bytes);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(full0 + 8 * s, 2 * box_bytes);
+            mbar_arrive(full0 + 8 * s);
+          }
+          const uint32_t bar = clear ? mapa_shared(tail, rank) : full_leader + 8 * s;
+          const uint32_t sa = smem_u32(smem) + s * kSlot;
+          const uint32_t sb = sa + kOperand;
+          if (MODE == kProductForward) {
+            tma_load_3d_pair(sa, &tmA, bar, f, c, t.g, pol);
+            tma_load_3d_pair(sa + kSubBytes, &tmA, bar, f + 64, c, t.g, pol);
+          } else if (MODE == kProductDx) {
+            tma_load_3d_pair(sa, &tmA, bar, c, f, t.g, pol);
+          } else {
+            tma_load_2d_pair(sa, &tmA, bar, f, c, pol);
+            tma_load_2d_pair(sa + kSubBytes, &tmA, bar, f + 64, c, pol);
+          }
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-              if (h >= halves) break;
-              if (kBMn) {
-                tma_load_2d_pair(sb + h * kOperand, &tmB, bar, j[h], c, pol);
-                if (hn > 128)
-                  tma_load_2d_pair(sb + h * kOperand + kSubBytes, &tmB, bar, j[h] + 64, c, pol);
-              } else {
-                tma_load_2d_pair(sb + h * kOperand, &tmB, bar, c, j[h], pol);
-              }
+          for (int h = 0; h < HALVES; ++h) {
+            if (h >= halves) break;
+            if (kBMn) {
+              tma_load_2d_pair(sb + h * kOperand, &tmB, bar, j[h], c, pol);
+              if (hn > 128)
+                tma_load_2d_pair(sb + h * kOperand + kSubBytes, &tmB, bar, j[h] + 64, c, pol);
+            } else {
+              tma_load_2d_pair(sb + h * kOperand, &tmB, bar, c, j[h], pol);
             }
-            if (clear) go = mbar_wait(tail, tails & 1u, abort_flag, p.status) ? 1 : 0;
           }
         }
-        if (MODE == kProductDw) go = __shfl_sync(0xffffffffu, go, 0);
-        if (!go) {
-          ok = false;
-          break;
-        }
+        __syncwarp();
+        if (clear && !(ok = warp_wait(tail, tails & 1u, abort_flag, p.status))) break;
         if (clear) {
           const int n16 = (((left + 15) & ~15) - left) * 8;  // 16-byte pieces per box
           uint8_t* slot = smem + s * kSlot;
@@ -220,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       constexpr uint64_t kStepA = (kAMn ? 2048 : 32) >> 4;
       constexpr uint64_t kStepB = (kBMn ? 2048 : 32) >> 4;
       const uint32_t sa = smem_u32(smem);
@@ -245,8 +237,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // half h's accumulator is drained
         auto acquire = [&](int h) {
           const uint32_t c = tc + h;
-          const bool r = mbar_wait_cluster(tempty0 + 8 * (c & 1u), ((c >> 1) & 1u) ^ 1u, abort_flag,
-                                           p.status);
+          const bool r = __all_sync(
+              0xffffffffu, mbar_wait_cluster(tempty0 + 8 * (c & 1u), ((c >> 1) & 1u) ^ 1u, abort_flag,
+                                             p.status));
           tc_fence_after();
           return r;
         };
@@ -256,8 +249,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t bar = full0 + 8 * (q < kStages ? q : q - kStages);
           const uint32_t par = q < kStages ? ph : ph ^ 1u;
           // a cleared slot's zeros come from the peer's threads: cluster scope
-          const bool r = MODE == kProductDw ? mbar_wait_cluster(bar, par, abort_flag, p.status)
-                                            : mbar_wait(bar, par, abort_flag, p.status);
+          const bool r = __all_sync(
+              0xffffffffu, MODE == kProductDw ? mbar_wait_cluster(bar, par, abort_flag, p.status)
+                                              : mbar_wait(bar, par, abort_flag, p.status));
           tc_fence_after();
           return r;
         };
@@ -267,24 +261,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t at = static_cast<uint64_t>((q < kStages ? q : q - kStages) * (kSlot >> 4));
           const uint64_t ad = ad0 + at;
           const uint64_t bd = bd0 + at + static_cast<uint64_t>(h * (kOperand >> 4));
-          gemm::mma_issue_pair(d[h], ad, bd, idesc[h], left < t.depth ? 1u : 0u);
-          if (left > 48) {
+          const uint32_t acc = left < t.depth ? 1u : 0u;
+          if (elect_one()) {
+            if (left > 48) {
 #pragma unroll
-            for (int i = 1; i < 4; ++i)
-              gemm::mma_issue_pair(d[h], ad + i * kStepA, bd + i * kStepB, idesc[h], 1u);
-          } else {
-            for (int i = 1; i < (left + 15) >> 4; ++i)
-              gemm::mma_issue_pair(d[h], ad + i * kStepA, bd + i * kStepB, idesc[h], 1u);
+              for (int i = 0; i < 4; ++i)
+                gemm::mma_issue_pair(d[h], ad + i * kStepA, bd + i * kStepB, idesc[h],
+                                     i > 0 ? 1u : acc);
+            } else {
+              for (int i = 0; i < (left + 15) >> 4; ++i)
+                gemm::mma_issue_pair(d[h], ad + i * kStepA, bd + i * kStepB, idesc[h],
+                                     i > 0 ? 1u : acc);
+            }
           }
+          __syncwarp();
         };
         auto release = [&]() {
-          tc_commit_pair_mc(empty0 + 8 * s, 3);  // frees the slot in both CTAs
+          if (elect_one()) tc_commit_pair_mc(empty0 + 8 * s, 3);  // frees the slot in both CTAs
+          __syncwarp();
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
           }
         };
-        auto finish = [&](int h) { tc_commit_pair_mc(tfull0 + 8 * ((tc + h) & 1u), 3); };
+        auto finish = [&](int h) {
+          if (elect_one()) tc_commit_pair_mc(tfull0 + 8 * ((tc + h) & 1u), 3);
+          __syncwarp();
+        };
         if (!(ok = acquire(0))) break;
         int left = t.depth;
         if (HALVES == 1 || halves == 1) {
@@ -330,7 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc += halves;
       }
       if (any) {  // no MMA may still be writing TMEM at deallocation
-        tc_commit_pair(drain);
+        if (elect_one()) tc_commit_pair(drain);
+        __syncwarp();
         mbar_wait(drain, 0, nullptr, p.status);
       }
     }

@@ -55,8 +55,6 @@ struct ProductMaps {
   CUtensorMap a, b;
 };
 
-// smem bytes of one pipeline slot of a tile of bn rows
-size_t product_slot_bytes(int mode, int bn);
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                            int num_sms, cudaStream_t st);
 
