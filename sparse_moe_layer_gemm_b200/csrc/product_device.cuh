@@ -524,18 +524,41 @@ __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t tadd
   }
 }
 
-// One value of the split form's joined rows.
-template <int MODE, typename T>
-__device__ __forceinline__ void finish_value(const ProductParams& p, int64_t row, int feat,
-                                             float bias, float v) {
-  if (MODE == kProductForward) {
-    v += bias;
-    if (p.preact != nullptr) static_cast<T*>(p.preact)[row * p.ld_preact + feat] = from_f32<T>(v);
-    v = activate(v, p.act);
-    if (p.residual != nullptr)
-      v += to_f32<T>(static_cast<const T*>(p.residual)[row * p.ld_residual + feat]);
+// Four neighbouring features of a row of the split form.
+template <typename T>
+__device__ __forceinline__ void store4(T* at, const float (&v)[4], int n, bool vec) {
+  if (vec && n == 4) {
+    *reinterpret_cast<uint2*>(at) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) at[i] = from_f32<T>(v[i]);
   }
-  static_cast<T*>(p.out)[row * p.ld_out + feat] = from_f32<T>(v);
+}
+
+template <int MODE, typename T>
+__device__ __forceinline__ void finish_row4(const ProductParams& p, int64_t row, int feat, int g,
+                                            float (&v)[4]) {
+  const int n = min(4, p.feats - feat);
+  if (n <= 0) return;
+  if (MODE == kProductForward) {
+    if (p.bias != nullptr) {
+      const T* b = static_cast<const T*>(p.bias) + static_cast<int64_t>(g) * p.feats + feat;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] += to_f32<T>(b[i]);
+    }
+    if (p.preact != nullptr)
+      store4<T>(static_cast<T*>(p.preact) + row * p.ld_preact + feat, v, n, p.vec_preact);
+    activate_all(v, p.act);
+    if (p.residual != nullptr) {
+      const T* r = static_cast<const T*>(p.residual) + row * p.ld_residual + feat;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] += to_f32<T>(r[i]);
+    }
+  }
+  store4<T>(static_cast<T*>(p.out) + row * p.ld_out + feat, v, n, p.vec_out);
 }
 
 template <typename T>

@@ -53,9 +53,12 @@ __host__ __device__ constexpr int b_bytes(int mode, int bn) {
   return mode == kProductDw ? (bn + 63) / 64 * kSubBytes : bn * 128;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -272,7 +275,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // the TMEM lane quadrant this warp may read
     uint32_t tc = 0;
-    const T* bias = static_cast<const T*>(p.bias);
     uint8_t* stg = epi + (warp - 2) * kEpiWarpBytes;
     for (int w = cluster; w < total; w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
@@ -280,14 +282,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       my_slots(t.depth, rank, split, &kb0, &kb1);
       const bool empty = kb0 == kb1;
       const uint32_t buf = tc & 1u;
-      const int feat = t.f0 + q * 32 + lane;
-      const bool live = feat < p.feats;
       const int64_t row0 = MODE == kProductDw
                                ? static_cast<int64_t>(t.g) * p.cols + t.j0
                                : static_cast<int64_t>(t.j0);
-      const float b = (MODE == kProductForward && bias != nullptr && live)
-                          ? to_f32<T>(bias[static_cast<int64_t>(t.g) * p.feats + feat])
-                          : 0.f;
       if (!empty) {
         int go = 1;
         if (lane == 0)
@@ -327,22 +324,36 @@ __global__ void __launch_bounds__(kThreads, 2)
       int go = 1;
       if (lane == 0) go = mbar_wait_cluster(xfull, 0, abort_flag, p.status) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, go, 0)) break;
-      const int share = (t.n_valid + split - 1) / split;  // rows this CTA finishes
-      const int mine = min(share, t.n_valid - rank * share);
-      const uint32_t own = smem_u32(part) + rank * share * (kProductBM * 4);
+      // this CTA's rows, dealt to its warps; a lane joins 4 features of a row, with
+      // two rows' loads under way at once
+      const int share = (t.n_valid + split - 1) / split;
+      const int j0 = rank * share, j1 = min(j0 + share, t.n_valid);
+      const uint32_t mine = smem_u32(smem) + lane * 16;
       uint32_t from[kProductMaxSplit];
 #pragma unroll
-      for (int k = 0; k < kProductMaxSplit; ++k) from[k] = mapa_shared(own, min(k, split - 1));
-#pragma unroll 2
-      for (int j = 0; j < mine; ++j) {
-        float got[kProductMaxSplit];
+      for (int k = 0; k < kProductMaxSplit; ++k) from[k] = mapa_shared(mine, min(k, split - 1));
+      for (int j = j0 + warp - 2; j < j1; j += 8) {
+        const int n = j + 4 < j1 ? 2 : 1;
+        float4 got[2][kProductMaxSplit];
 #pragma unroll
-        for (int k = 0; k < kProductMaxSplit; ++k)
-          got[k] = k < split ? ld_cluster_f32(from[k] + j * (kProductBM * 4)) : 0.f;
-        float v = 0.f;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int k = 0; k < kProductMaxSplit; ++k) v += got[k];
-        if (live) finish_value<MODE, T>(p, row0 + rank * share + j, feat, b, v);
+          for (int k = 0; k < kProductMaxSplit; ++k)
+            if (i < n && k < split) got[i][k] = ld_cluster_f32x4(from[k] + (j + 4 * i) * (kProductBM * 4));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= n) break;
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < kProductMaxSplit; ++k)
+            if (k < split) {
+              v[0] += got[i][k].x;
+              v[1] += got[i][k].y;
+              v[2] += got[i][k].z;
+              v[3] += got[i][k].w;
+            }
+          finish_row4<MODE, T>(p, row0 + j + 4 * i, t.f0 + lane * 4, t.g, v);
+        }
       }
       break;
     }
