@@ -252,51 +252,84 @@ int check_ws(const void* ws, size_t have, size_t need) {
   return ws == nullptr || !aligned(ws, kWsAlign) || have < need ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
-// Tile, split and order of a product: `blocks64` slots of 64 contraction
-// steps, `groups` groups of `mean` rows (dw: output rows) each.
+// Tile, split and order of a product.
 struct Choice {
   bool pair;
   int bn, split, chunk;
 };
 
-// Cycles of a CTA pair per 16 contraction steps of a tile of bn rows: with one
-// accumulator the MMAs follow each other every ~165 cycles whatever their
-// rows; with two, 128 cycles of work for the first 256 rows and at least ~88
-// for the second MMA (4096 x 4096 -> 1280, one wave: 53.7 us at 512 rows, 45.9
-// at 384, 45.4 at 320 and 304; two waves of 256 rows 59.8).
-int pair_step_cost(int bn) { return bn <= 256 ? 165 : 128 + std::max(88, (bn - 256) / 2); }
+// What the choice goes by: features, `groups` groups of `mean` rows (dw:
+// output rows) each, of differing sizes if ragged, and blocks64 slots of 64
+// contraction steps per tile.
+struct Shape {
+  int64_t feats, groups, mean, blocks64;
+  bool ragged, dw, act;
+};
 
-Choice choose(int64_t feats, int64_t groups, int64_t mean, int64_t blocks64, int num_sms) {
-  Choice best{true, 0, 1, 1};
-  if (mean > kProductMaxBN) {
-    const int64_t f_tiles = (feats + 2 * kProductBM - 1) / (2 * kProductBM);
-    const int64_t pairs = num_sms / 2;
-    int64_t best_cost = 0, tiles = 0;
-    for (int bn = kProductPairMaxBN; bn >= 128; bn -= 16) {
-      const int64_t n = groups * f_tiles * ((mean + bn - 1) / bn);
-      const int64_t cost = (n + pairs - 1) / pairs * pair_step_cost(bn);
-      if (best.bn == 0 || cost < best_cost) {
-        best.bn = bn;
-        best_cost = cost;
-        tiles = n;
-      }
+// Row blocks of bn rows over all groups; a ragged group fills half of its last
+// one on average.
+int64_t row_blocks(const Shape& q, int64_t bn) {
+  if (!q.ragged) return q.groups * ((q.mean + bn - 1) / bn);
+  return (q.groups * q.mean + bn - 1) / bn + q.groups / 2;
+}
+
+// Nanoseconds of one slot of 64 contraction steps, and of what a tile's
+// epilogue leaves uncovered, as measured on one B200 with weights from L2.
+// One CTA, 128 features x bn rows: 4096 -> 1280 (64 slots) takes 15.1, 15.6,
+// 17.0, 21.2 us at bn = 16, 32, 64, 128; 1280 -> 4096 (20 slots) 7.8 to 11.2.
+// A CTA pair, 256 features: with one accumulator 23 us per wave of 64 slots at
+// 256 rows, 21 at 224 and 19.8 at 208 and below; with two 43 us at 512 rows,
+// 31 at 320, and 4.6 us more per tile, since its epilogue overlaps the next
+// tile less (1280 -> 4096 at 4096 rows: 33 us with one, 42 with two; 4096 ->
+// 1280, where two accumulators make one wave of what else is two: 37 and 45 us
+// for dw, 36 and 38.5 for dx).
+int one_cta_slot_ns(int bn) { return bn <= 16 ? 166 : bn <= 32 ? 173 : bn <= 64 ? 195 : 260; }
+int pair_slot_ns(int bn) {
+  if (bn <= 256) return bn >= 240 ? 360 : bn >= 224 ? 330 : 310;
+  return 490 + std::max(0, bn - 320) * 190 / 192;
+}
+constexpr int kPairTileNs = 500, kPairTwoTileNs = 4600;
+// Joining a split tile: 2 us and 45 ns per row (one token 4096 -> 1280: 15.1 us
+// unsplit, 11.6, 9.7, 9.0 in 2, 4, 8 parts; 128 tokens 21.2, 23.7, 17.2, 14.0).
+constexpr int kJoinNs = 2000, kJoinRowNs = 45;
+
+Choice choose(const Shape& q, int num_sms) {
+  Choice best{false, 0, 1, 1};
+  int64_t best_ns = 0;
+  auto offer = [&](bool pair, int bn, int split, int64_t ns) {
+    if (best.bn == 0 || ns < best_ns) {
+      best = {pair, bn, split, 1};
+      best_ns = ns;
     }
-    if (2 * tiles < pairs) best.bn = 0;
+  };
+  const int64_t f1 = (q.feats + kProductBM - 1) / kProductBM;
+  for (int bn = 16; bn <= kProductMaxBN; bn *= 2) {
+    if (bn > 16 && bn >= 2 * q.mean) break;
+    const int64_t tiles = f1 * row_blocks(q, bn);
+    for (int split = 1; split <= kProductMaxSplit; split *= 2) {
+      if (split > 1 && (tiles * split > num_sms || split > q.blocks64)) break;
+      const int64_t waves = (tiles + num_sms - 1) / num_sms;
+      const int64_t slots = (q.blocks64 + split - 1) / split;
+      offer(false, bn, split,
+            waves * slots * one_cta_slot_ns(bn) +
+                (split > 1 ? kJoinNs + kJoinRowNs * std::min<int64_t>(bn, q.mean) : 0));
+    }
   }
-  if (best.bn == 0) {
-    best.pair = false;
-    best.bn = 16;
-    while (best.bn < kProductMaxBN && best.bn < mean) best.bn *= 2;
-    const int64_t f_tiles = (feats + kProductBM - 1) / kProductBM;
-    const int64_t tiles = f_tiles * groups * ((mean + best.bn - 1) / best.bn);
-    while (best.split < kProductMaxSplit && tiles * best.split * 2 <= num_sms &&
-           blocks64 >= 4 * best.split)
-      best.split *= 2;
+  const int64_t f2 = (q.feats + 2 * kProductBM - 1) / (2 * kProductBM);
+  // (dw reads both operands MN-major, where halves that are no multiple of 16
+  // rows are slow: 58 us at 208 rows, 45 at 192.  An activation costs a second
+  // accumulator's poorer overlap more: gelu 4096 -> 11264 361 us, 291 without.)
+  const int step = q.dw ? 32 : 16;
+  for (int bn = q.act ? 256 : kProductPairMaxBN; bn >= 128 && q.mean > 64; bn -= step) {
+    const int64_t tiles = f2 * row_blocks(q, bn);
+    const int64_t waves = (tiles + num_sms / 2 - 1) / (num_sms / 2);
+    offer(true, bn, 1,
+          waves * (q.blocks64 * pair_slot_ns(bn) + (bn <= 256 ? kPairTileNs : kPairTwoTileNs)));
   }
   // a chunk's rows stay in L2 across its weight tiles: up to 32 MB of them
   // (4096 x 4096 -> 11264: 259 us with 8 blocks, 274 with 4; its dx, with rows
   // of 22 KB, 254 with 2 and 272 with 8)
-  const int64_t block_bytes = static_cast<int64_t>(best.bn) * blocks64 * 128;
+  const int64_t block_bytes = static_cast<int64_t>(best.bn) * q.blocks64 * 128;
   best.chunk = static_cast<int>(std::min<int64_t>(16, std::max<int64_t>(1, (32 << 20) / block_bytes)));
   return best;
 }
@@ -374,7 +407,8 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.depth = c->in_features;
   int64_t n_groups, mean;
   filled(a->offsets, G, R, &n_groups, &mean);
-  const Choice ch = choose(N, n_groups, mean, (K + 63) / 64, sms);
+  const Choice ch = choose({N, n_groups, mean, (K + 63) / 64, n_groups > 1, false,
+                            c->activation != MOE_ACT_NONE}, sms);
   p.bn = ch.bn;
   p.chunk = ch.chunk;
   p.split = ch.split;
@@ -464,7 +498,8 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.vec_out = vec_rows(a->dx, a->ld_dx, K);
     int64_t n_groups, mean;
     filled(a->offsets, G, R, &n_groups, &mean);
-    const Choice ch = choose(K, n_groups, mean, (N + 63) / 64, sms);
+    const Choice ch =
+        choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false}, sms);
     p.bn = ch.bn;
   p.chunk = ch.chunk;
     p.split = ch.split;
@@ -480,7 +515,8 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.out = a->dw;
     p.ld_out = N;
     p.vec_out = vec_rows(a->dw, N, N);
-    const Choice ch = choose(N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), sms);
+    const Choice ch =
+        choose({N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), false, true, false}, sms);
     p.bn = ch.bn;
   p.chunk = ch.chunk;
     p.split = ch.split;
