@@ -158,8 +158,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int i = 0; i < subs; ++i, sa += sub_bytes, c += 64) {
             const uint32_t sb = sa + kABytes;
             if (MODE == kProductForward) {
-              tma_load_3d(sa, &tmA, bar, t.f0, c, t.g, pol);
-              tma_load_3d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, t.g, pol);
+              if (p.wide_a) {
+                tma_load_4d(sa, &tmA, bar, 0, c, t.f0 >> 6, t.g, pol);
+              } else {
+                tma_load_3d(sa, &tmA, bar, t.f0, c, t.g, pol);
+                tma_load_3d(sa + kSubBytes, &tmA, bar, t.f0 + 64, c, t.g, pol);
+              }
             } else if (MODE == kProductDx) {
               tma_load_3d(sa, &tmA, bar, c, t.f0, t.g, pol);
             } else {

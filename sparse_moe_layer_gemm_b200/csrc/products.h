@@ -37,6 +37,10 @@ struct ProductParams {
   int bn;              // rows per tile, a multiple of 16
   int chunk;           // row blocks per ordering chunk
   int stages;          // pipeline slots
+  // forward: the weights' map walks 64-element chunks in a dimension of its own,
+  // so that one load brings both chunks of a CTA's 128 features (else one each;
+  // 4096 x 4096 -> 11264 248 us against 258; dw gained nothing from it)
+  bool wide_a;
   int split;           // CTAs of a cluster sharing one tile's contraction
   void* out;
   int64_t ld_out;      // elements between output rows
@@ -67,9 +71,20 @@ cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const
                                 int num_sms, cudaStream_t st);
 
 // Row kernels (product_rows.cu).
-// Copies groups x rows x cols 2-byte elements into rows of ld_dst elements.
-cudaError_t launch_pack_rows(const void* src, int64_t ld, int64_t group_stride, int groups,
-                             int64_t rows, int cols, void* dst, int64_t ld_dst, cudaStream_t st);
+// Copies of operands with rows of ld_dst elements, all in one launch (groups 0:
+// no operand).
+struct PackOperand {
+  const void* src;
+  int64_t ld, group_stride;
+  int64_t groups, rows;
+  int cols;
+  void* dst;
+  int64_t ld_dst;
+};
+struct PackParams {
+  PackOperand op[3];
+};
+cudaError_t launch_pack_rows(const PackParams& p, cudaStream_t st);
 
 struct RowGradParams {
   const void* dout;
@@ -81,14 +96,20 @@ struct RowGradParams {
   const int* offsets;
   int groups, rows, cols;
   int act;
-  float* partial;      // [chunks, cols] column sums of 128-row chunks, or nullptr
   void* db;            // [groups, cols] or nullptr
+  // db of few rows: a CTA sums all rows of a group, in the one launch; else each
+  // CTA sums a 64-row chunk into partial [chunks, cols] and a second launch
+  // adds the chunks
+  bool direct;
+  float* partial;
 };
-constexpr int kRowChunk = 128;
+constexpr int kRowChunk = 64;
+// Up to here a CTA walks its group's rows alone: 16 rows per warp at most.
+constexpr int kRowDirect = 128;
 inline size_t row_grad_chunks(int rows, int groups) {
   return static_cast<size_t>(rows) / kRowChunk + static_cast<size_t>(groups);
 }
-// dz = dout * act'(preact), and db from dz in fp32 (two launches when db is asked for)
+// dz = dout * act'(preact), and db from dz in fp32
 cudaError_t launch_row_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st);
 
 // SwiGLU (swiglu.cu)

@@ -69,22 +69,32 @@ int device_of(int* sms, int** status) {
   return MOE_OK;
 }
 
-// A 16-bit tensor as (cols, rows, groups) with its strides, box 64 columns
-// (128 bytes) x box_rows, 128-byte swizzle; out-of-range elements read as zero.
+// A 16-bit operand [groups][rows][cols] with its strides, 128-byte swizzle,
+// out-of-range elements read as zero.
+//  wide = false: (cols, rows, groups), box 64 columns (128 bytes) x box_rows;
+//  wide = true:  (64, rows, cols / 64, groups), box 64 x box_rows x 2 chunks,
+//                cols a multiple of 64 (so every element lies in the tensor).
+// Without groups (group_stride 0) that dimension is left out.
 bool encode(CUtensorMap* m, bool bf16, const void* base, int64_t cols, int64_t rows,
-            int64_t groups, int64_t ld, int64_t group_stride, int dims, int box_rows) {
+            int64_t groups, int64_t ld, int64_t group_stride, int box_rows, bool wide) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return false;
-  cuuint64_t dim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                       static_cast<cuuint64_t>(groups)};
-  cuuint64_t stride[2] = {static_cast<cuuint64_t>(ld) * 2,
-                          static_cast<cuuint64_t>(group_stride) * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-             static_cast<cuuint32_t>(dims), const_cast<void*>(base), dim, stride, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  cuuint64_t dim[4], stride[3];
+  cuuint32_t box[4], n = 0;
+  auto add = [&](int64_t d, int b, int64_t s) {  // s: bytes from one index to the next
+    dim[n] = static_cast<cuuint64_t>(d);
+    box[n] = static_cast<cuuint32_t>(b);
+    if (n > 0) stride[n - 1] = static_cast<cuuint64_t>(s);
+    ++n;
+  };
+  add(wide ? 64 : cols, 64, 2);
+  add(rows, box_rows, ld * 2);
+  if (wide) add(cols / 64, 2, 128);
+  if (group_stride > 0) add(groups, 1, group_stride * 2);
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, n,
+             const_cast<void*>(base), dim, stride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -242,7 +252,7 @@ BackwardWs backward_ws(const moe_linear_config_t* c, const moe_linear_grads_t* a
   w.dz = w.total;
   if (w.make_dz || w.copy_dout) w.total += copy_bytes(c->rows, c->out_features);
   w.partial = w.total;
-  if (a->dbias != nullptr)
+  if (a->dbias != nullptr && c->rows > kRowDirect)
     w.total += ws_round(row_grad_chunks(c->rows, G) * static_cast<size_t>(c->out_features) * 4);
   return w;
 }
@@ -351,6 +361,14 @@ struct Operand {
   int64_t ld, gs;
 };
 
+// Turns *o into its copy at dst with 16-byte aligned rows.
+PackOperand aligned_copy(Operand* o, int64_t groups, int64_t rows, int64_t cols, void* dst) {
+  const int64_t ld = padded(cols);
+  const PackOperand c{o->p, o->ld, o->gs, groups, rows, static_cast<int>(cols), dst, ld};
+  *o = {dst, ld, groups > 1 || o->gs > 0 ? ld * rows : 0};
+  return c;
+}
+
 }  // namespace
 
 extern "C" {
@@ -391,14 +409,10 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   const int G = std::max(1, c->groups);
   const bool bf16 = c->dtype == MOE_BF16;
   Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
-  if (ws.copy_x) {
-    MOE_CUDA(launch_pack_rows(x.p, x.ld, 0, 1, R, static_cast<int>(K), base + ws.x, padded(K), st));
-    x = {base + ws.x, padded(K), 0};
-  }
-  if (ws.copy_w) {
-    MOE_CUDA(launch_pack_rows(w.p, w.ld, w.gs, G, K, static_cast<int>(N), base + ws.w, padded(N), st));
-    w = {base + ws.w, padded(N), padded(N) * K};
-  }
+  PackParams pack{};
+  if (ws.copy_x) pack.op[0] = aligned_copy(&x, 1, R, K, base + ws.x);
+  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w);
+  MOE_CUDA(launch_pack_rows(pack, st));
   ProductParams p{};
   p.offsets = a->offsets;
   p.groups = G;
@@ -425,8 +439,9 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.vec_preact = vec_rows(a->preact, a->ld_preact, N);
   p.status = status;
   ProductMaps m;
-  if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, 64) ||
-      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, ch.pair ? product_pair_box(p.bn) : p.bn))
+  p.wide_a = N % 64 == 0;
+  if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 64, p.wide_a) ||
+      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, ch.pair ? product_pair_box(p.bn) : p.bn, false))
     return MOE_ERR_CUDA;
   MOE_CUDA(launch_any(ch, kProductForward, bf16, m, p, sms, st));
   return MOE_OK;
@@ -467,23 +482,17 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     q.rows = c->rows;
     q.cols = c->out_features;
     q.act = c->activation;
-    q.partial = a->dbias != nullptr ? reinterpret_cast<float*>(base + ws.partial) : nullptr;
     q.db = a->dbias;
+    q.direct = a->dbias != nullptr && c->rows <= kRowDirect;
+    q.partial = reinterpret_cast<float*>(base + ws.partial);
     if (products || a->dbias != nullptr) MOE_CUDA(launch_row_grad(bf16, q, sms, st));
     if (ws.make_dz) dz = {base + ws.dz, padded(N), 0};
   }
-  if (ws.copy_dout) {
-    MOE_CUDA(launch_pack_rows(dz.p, dz.ld, 0, 1, R, static_cast<int>(N), base + ws.dz, padded(N), st));
-    dz = {base + ws.dz, padded(N), 0};
-  }
-  if (ws.copy_w) {
-    MOE_CUDA(launch_pack_rows(w.p, w.ld, w.gs, G, K, static_cast<int>(N), base + ws.w, padded(N), st));
-    w = {base + ws.w, padded(N), padded(N) * K};
-  }
-  if (ws.copy_x) {
-    MOE_CUDA(launch_pack_rows(x.p, x.ld, 0, 1, R, static_cast<int>(K), base + ws.x, padded(K), st));
-    x = {base + ws.x, padded(K), 0};
-  }
+  PackParams pack{};
+  if (ws.copy_dout) pack.op[0] = aligned_copy(&dz, 1, R, N, base + ws.dz);
+  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w);
+  if (ws.copy_x) pack.op[2] = aligned_copy(&x, 1, R, K, base + ws.x);
+  MOE_CUDA(launch_pack_rows(pack, st));
   ProductParams p{};
   p.offsets = a->offsets;
   p.groups = G;
@@ -503,8 +512,9 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.bn = ch.bn;
   p.chunk = ch.chunk;
     p.split = ch.split;
-    if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 3, kProductBM) ||
-        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, 2, ch.pair ? product_pair_box(p.bn) : p.bn))
+    if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, kProductBM, false) ||
+        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, ch.pair ? product_pair_box(p.bn) : p.bn,
+                false))
       return MOE_ERR_CUDA;
     MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
   }
@@ -520,8 +530,8 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.bn = ch.bn;
   p.chunk = ch.chunk;
     p.split = ch.split;
-    if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 2, 64) ||
-        !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 2, 64))
+    if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 64, false) ||
+        !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 64, false))
       return MOE_ERR_CUDA;
     MOE_CUDA(launch_any(ch, kProductDw, bf16, m, p, sms, st));
   }

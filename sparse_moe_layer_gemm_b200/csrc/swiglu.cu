@@ -5,9 +5,15 @@
 //   dup   = dout * s * silu(a) where |up| <= L, else 0
 //   ds    = sum over the row of dout * silu(a) * v
 // with s the row's gate weight (1 without).  6 bytes per element forward, 10
-// backward at 16 bits: bound by memory.  One CTA per row at a time, 16 bytes
-// per thread and access where the rows allow it; the row's sum is added per
-// thread, over the warp, then over the warps in order, in fp32.
+// backward at 16 bits: bound by memory.
+//
+// A team of one or eight warps takes a row at a time, 16 bytes per lane and
+// access where every row starts at a 16-byte boundary, and keeps several
+// accesses of each tensor under way before it uses the first: one warp per
+// row from kManyRows rows on (32768 x 1280 bf16, one CTA per row: 58 us
+// forward, 95 backward), a whole CTA per row below, where the row's length is
+// what takes time.  The row's sum is added per lane, over the warp, then over
+// the warps in order, in fp32: the same on every run.
 #include <algorithm>
 
 #include "moe_internal.h"
@@ -19,7 +25,9 @@ namespace {
 
 using namespace product;
 
-constexpr int kMaxThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kManyRows = 1024;
 
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Pack {
@@ -31,51 +39,80 @@ __device__ __forceinline__ float exp_of(float x) { return __expf(x); }
 template <>
 __device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
 
+// a / b: approximate where the result is rounded to 16 bits
+template <typename T>
+__device__ __forceinline__ float divide(float a, float b) { return __fdividef(a, b); }
+template <>
+__device__ __forceinline__ float divide<float>(float a, float b) { return a / b; }
+
 // NaN passes both clamps, as it passes the plain formula.
 __device__ __forceinline__ float clamp_gate(float g, float L) { return L > 0.f && g > L ? L : g; }
 __device__ __forceinline__ float clamp_up(float u, float L) {
   return L > 0.f ? (u > L ? L : (u < -L ? -L : u)) : u;
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kMaxThreads) swiglu_kernel(const SwigluParams p) {
-  pdl_wait();
-  int r0 = 0, r1 = p.rows;
+__device__ __forceinline__ void row_range(const SwigluParams& p, int* r0, int* r1) {
+  *r0 = 0;
+  *r1 = p.rows;
   if (p.offsets != nullptr) {
-    r0 = min(max(p.offsets[0], 0), p.rows);
-    r1 = min(max(p.offsets[p.groups], 0), p.rows);
+    *r0 = min(max(p.offsets[0], 0), p.rows);
+    *r1 = min(max(p.offsets[p.groups], 0), p.rows);
   }
-  for (int64_t row = static_cast<int64_t>(r0) + blockIdx.x; row < r1; row += gridDim.x) {
+}
+
+// TEAM: warps per row.  U accesses of each tensor under way per lane.
+template <typename T, int V, int TEAM, int U>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) {
+  pdl_wait();
+  int r0, r1;
+  row_range(p, &r0, &r1);
+  constexpr int kStep = 32 * TEAM * V;  // columns per access of the team
+  const int team = static_cast<int>(threadIdx.x) / (32 * TEAM);
+  const int lane = static_cast<int>(threadIdx.x) % (32 * TEAM);
+  constexpr int kTeams = kWarps / TEAM;
+  for (int64_t row = r0 + static_cast<int64_t>(blockIdx.x) * kTeams + team; row < r1;
+       row += static_cast<int64_t>(gridDim.x) * kTeams) {
     const T* gate = static_cast<const T*>(p.gate) + row * p.ld_gate;
     const T* up = static_cast<const T*>(p.up) + row * p.ld_up;
     T* out = static_cast<T*>(p.out) + row * p.ld_out;
     const float s = p.scale != nullptr ? p.scale[row] : 1.f;
-    for (int c = threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
-      const Pack<T, V> g = *reinterpret_cast<const Pack<T, V>*>(gate + c);
-      const Pack<T, V> u = *reinterpret_cast<const Pack<T, V>*>(up + c);
-      Pack<T, V> o;
+    for (int c0 = lane * V; c0 < p.cols; c0 += U * kStep) {
+      Pack<T, V> g[U], u[U];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float a = clamp_gate(to_f32<T>(g.v[i]), p.limit);
-        const float b = clamp_up(to_f32<T>(u.v[i]), p.limit);
-        o.v[i] = from_f32<T>(s * (a / (1.0f + exp_of<T>(-a))) * b);
-      }
-      *reinterpret_cast<Pack<T, V>*>(out + c) = o;
+      for (int k = 0; k < U; ++k)
+        if (c0 + k * kStep < p.cols) {
+          g[k] = *reinterpret_cast<const Pack<T, V>*>(gate + c0 + k * kStep);
+          u[k] = *reinterpret_cast<const Pack<T, V>*>(up + c0 + k * kStep);
+        }
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (c0 + k * kStep < p.cols) {
+          Pack<T, V> o;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float a = clamp_gate(to_f32<T>(g[k].v[i]), p.limit);
+            const float b = clamp_up(to_f32<T>(u[k].v[i]), p.limit);
+            o.v[i] = from_f32<T>(s * divide<T>(a, 1.0f + exp_of<T>(-a)) * b);
+          }
+          *reinterpret_cast<Pack<T, V>*>(out + c0 + k * kStep) = o;
+        }
     }
   }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kMaxThreads) swiglu_backward_kernel(const SwigluParams p) {
-  __shared__ float sums[kMaxThreads / 32];
+template <typename T, int V, int TEAM, int U>
+__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluParams p) {
+  __shared__ float sums[kWarps];
   pdl_wait();
-  int r0 = 0, r1 = p.rows;
-  if (p.offsets != nullptr) {
-    r0 = min(max(p.offsets[0], 0), p.rows);
-    r1 = min(max(p.offsets[p.groups], 0), p.rows);
-  }
+  int r0, r1;
+  row_range(p, &r0, &r1);
   const float L = p.limit;
-  for (int64_t row = static_cast<int64_t>(r0) + blockIdx.x; row < r1; row += gridDim.x) {
+  constexpr int kStep = 32 * TEAM * V;
+  const int team = static_cast<int>(threadIdx.x) / (32 * TEAM);
+  const int lane = static_cast<int>(threadIdx.x) % (32 * TEAM);
+  constexpr int kTeams = kWarps / TEAM;
+  for (int64_t row = r0 + static_cast<int64_t>(blockIdx.x) * kTeams + team; row < r1;
+       row += static_cast<int64_t>(gridDim.x) * kTeams) {
     const T* gate = static_cast<const T*>(p.gate) + row * p.ld_gate;
     const T* up = static_cast<const T*>(p.up) + row * p.ld_up;
     const T* dout = static_cast<const T*>(p.dout) + row * p.ld_dout;
@@ -83,37 +120,53 @@ __global__ void __launch_bounds__(kMaxThreads) swiglu_backward_kernel(const Swig
     T* dup = static_cast<T*>(p.dup) + row * p.ld_dup;
     const float s = p.scale != nullptr ? p.scale[row] : 1.f;
     float acc = 0.f;
-    for (int c = threadIdx.x * V; c < p.cols; c += blockDim.x * V) {
-      const Pack<T, V> g = *reinterpret_cast<const Pack<T, V>*>(gate + c);
-      const Pack<T, V> u = *reinterpret_cast<const Pack<T, V>*>(up + c);
-      const Pack<T, V> d = *reinterpret_cast<const Pack<T, V>*>(dout + c);
-      Pack<T, V> dg, du;
+    for (int c0 = lane * V; c0 < p.cols; c0 += U * kStep) {
+      Pack<T, V> g[U], u[U], d[U];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float gf = to_f32<T>(g.v[i]), uf = to_f32<T>(u.v[i]), df = to_f32<T>(d.v[i]);
-        const float a = clamp_gate(gf, L), b = clamp_up(uf, L);
-        const float sg = 1.0f / (1.0f + exp_of<T>(-a));
-        const float silu = a * sg;
-        acc += df * silu * b;
-        const float dgv = df * s * b * sg * (1.0f + a * (1.0f - sg));
-        const float duv = df * s * silu;
-        dg.v[i] = from_f32<T>(L > 0.f && gf > L ? 0.f : dgv);
-        du.v[i] = from_f32<T>(L > 0.f && fabsf(uf) > L ? 0.f : duv);
-      }
-      *reinterpret_cast<Pack<T, V>*>(dgate + c) = dg;
-      *reinterpret_cast<Pack<T, V>*>(dup + c) = du;
+      for (int k = 0; k < U; ++k)
+        if (c0 + k * kStep < p.cols) {
+          g[k] = *reinterpret_cast<const Pack<T, V>*>(gate + c0 + k * kStep);
+          u[k] = *reinterpret_cast<const Pack<T, V>*>(up + c0 + k * kStep);
+          d[k] = *reinterpret_cast<const Pack<T, V>*>(dout + c0 + k * kStep);
+        }
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (c0 + k * kStep < p.cols) {
+          Pack<T, V> dg, du;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float gf = to_f32<T>(g[k].v[i]), uf = to_f32<T>(u[k].v[i]);
+            const float df = to_f32<T>(d[k].v[i]);
+            const float a = clamp_gate(gf, L), b = clamp_up(uf, L);
+            const float sg = divide<T>(1.0f, 1.0f + exp_of<T>(-a));
+            const float silu = a * sg;
+            acc += df * silu * b;
+            const float dgv = df * s * b * sg * (1.0f + a * (1.0f - sg));
+            const float duv = df * s * silu;
+            dg.v[i] = from_f32<T>(L > 0.f && gf > L ? 0.f : dgv);
+            du.v[i] = from_f32<T>(L > 0.f && fabsf(uf) > L ? 0.f : duv);
+          }
+          *reinterpret_cast<Pack<T, V>*>(dgate + c0 + k * kStep) = dg;
+          *reinterpret_cast<Pack<T, V>*>(dup + c0 + k * kStep) = du;
+        }
     }
     if (p.dscale != nullptr) {
+      __syncwarp();
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
-      if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = acc;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        float v = 0.f;
-        for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v += sums[i];
-        p.dscale[row] = v;
+      for (int m = 16; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+      if (TEAM == 1) {
+        if (lane == 0) p.dscale[row] = acc;
+      } else {
+        if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = acc;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          float v = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) v += sums[i];
+          p.dscale[row] = v;
+        }
+        __syncthreads();
       }
-      __syncthreads();
     }
   }
 }
@@ -131,18 +184,24 @@ bool vec_ok(const SwigluParams& p, bool backward) {
   return ok(p.dout, p.ld_dout) && ok(p.dgate, p.ld_dgate) && ok(p.dup, p.ld_dup);
 }
 
+template <typename T, int V, int TEAM>
+cudaError_t launch(const SwigluParams& p, bool backward, cudaStream_t st) {
+  // about 100 bytes per lane under way
+  constexpr int U = V == 1 ? 8 : (TEAM == 1 ? 2 : 1);
+  constexpr int kTeams = kWarps / TEAM;
+  const dim3 grid(static_cast<unsigned>(std::min((p.rows + kTeams - 1) / kTeams, 1 << 20)));
+  return backward
+             ? launch_pdl(swiglu_backward_kernel<T, V, TEAM, U>, grid, dim3(kThreads), 0, st, p)
+             : launch_pdl(swiglu_kernel<T, V, TEAM, U>, grid, dim3(kThreads), 0, st, p);
+}
+
 template <typename T>
 cudaError_t run(const SwigluParams& p, bool backward, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  const bool vec = vec_ok<T>(p, backward);
-  const int pieces = (p.cols + (vec ? V : 1) - 1) / (vec ? V : 1);
-  const int threads = std::min(kMaxThreads, (pieces + 31) / 32 * 32);
-  const dim3 grid(static_cast<unsigned>(std::min(p.rows, 1 << 20)));
-  if (backward)
-    return vec ? launch_pdl(swiglu_backward_kernel<T, V>, grid, dim3(threads), 0, st, p)
-               : launch_pdl(swiglu_backward_kernel<T, 1>, grid, dim3(threads), 0, st, p);
-  return vec ? launch_pdl(swiglu_kernel<T, V>, grid, dim3(threads), 0, st, p)
-             : launch_pdl(swiglu_kernel<T, 1>, grid, dim3(threads), 0, st, p);
+  const bool many = p.rows >= kManyRows;
+  if (vec_ok<T>(p, backward))
+    return many ? launch<T, V, 1>(p, backward, st) : launch<T, V, kWarps>(p, backward, st);
+  return many ? launch<T, 1, 1>(p, backward, st) : launch<T, 1, kWarps>(p, backward, st);
 }
 
 cudaError_t dispatch(int dtype, const SwigluParams& p, bool backward, cudaStream_t st) {
