@@ -48,9 +48,23 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
 
-__device__ __forceinline__ float reciprocal(float v) { return __fdividef(1.0f, v); }
+// one special-function instruction each, to a few units of 2^-23
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float sigmoid(float z) { return reciprocal(1.0f + __expf(-z)); }
+// 1 / (1 + exp(-z)); an exponential of infinity gives 0
+__device__ __forceinline__ float sigmoid(float z) {
+  return reciprocal(1.0f + exp2_fast(-kLog2e * z));
+}
 
 // Phi(z), and exp(-z^2 / 2)
 __device__ __forceinline__ float normal_cdf(float z, float* e) {
@@ -64,7 +78,7 @@ __device__ __forceinline__ float normal_cdf(float z, float* e) {
   q = fmaf(q, t, 0.2916032075881958f);
   q = fmaf(q, t, 0.3372488021850586f);
   q = fmaf(q, t, 0.3385601043701172f);
-  *e = __expf(-0.5f * z * z);
+  *e = exp2_fast(-0.5f * kLog2e * z * z);
   const float half_erfc = 0.5f * t * q * *e;
   return z < 0.f ? half_erfc : 1.0f - half_erfc;
 }
@@ -74,7 +88,7 @@ __device__ __forceinline__ float activate(float z, int act) {
     case MOE_ACT_RELU:
       return z < 0.f ? 0.f : z;  // NaN stays NaN
     case MOE_ACT_SILU:
-      return __fdividef(z, 1.0f + __expf(-z));
+      return z * sigmoid(z);
     case MOE_ACT_GELU: {
       float e;
       return z * normal_cdf(z, &e);

@@ -8,12 +8,14 @@
 // backward at 16 bits: bound by memory.
 //
 // A team of one or eight warps takes a row at a time, 16 bytes per lane and
-// access where every row starts at a 16-byte boundary, and keeps several
-// accesses of each tensor under way before it uses the first: one warp per
-// row from kManyRows rows on (32768 x 1280 bf16, one CTA per row: 58 us
-// forward, 95 backward), a whole CTA per row below, where the row's length is
-// what takes time.  The row's sum is added per lane, over the warp, then over
-// the warps in order, in fp32: the same on every run.
+// access where every row starts at a 16-byte boundary: one warp per row from
+// kManyRows rows on (32768 x 1280 bf16 with clamp and scale: 41 us forward, 66
+// backward, 6.2 and 6.35 TB/s; one CTA per row took 58 and 95), a whole CTA
+// per row below, where the row's length is what takes time.  The instructions
+// count too: the sigmoid is one ex2, one rcp and two more, the clamps min and
+// max with NaN (with the library's expf and division 49 and 86 us).  The row's
+// sum is added per lane, over the warp, then over the warps in order, in fp32:
+// the same on every run.
 #include <algorithm>
 
 #include "moe_internal.h"
@@ -34,21 +36,22 @@ struct alignas(sizeof(T) * V) Pack {
   T v[V];
 };
 
+// fp32 rows take the exact division and exponential.
 template <typename T>
-__device__ __forceinline__ float exp_of(float x) { return __expf(x); }
+__device__ __forceinline__ float sigmoid_of(float x) { return sigmoid(x); }
 template <>
-__device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
+__device__ __forceinline__ float sigmoid_of<float>(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// a / b: approximate where the result is rounded to 16 bits
-template <typename T>
-__device__ __forceinline__ float divide(float a, float b) { return __fdividef(a, b); }
-template <>
-__device__ __forceinline__ float divide<float>(float a, float b) { return a / b; }
-
-// NaN passes both clamps, as it passes the plain formula.
-__device__ __forceinline__ float clamp_gate(float g, float L) { return L > 0.f && g > L ? L : g; }
-__device__ __forceinline__ float clamp_up(float u, float L) {
-  return L > 0.f ? (u > L ? L : (u < -L ? -L : u)) : u;
+// NaN passes the clamps, as it passes the plain formula.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 __device__ __forceinline__ void row_range(const SwigluParams& p, int* r0, int* r1) {
@@ -61,11 +64,12 @@ __device__ __forceinline__ void row_range(const SwigluParams& p, int* r0, int* r
 }
 
 // TEAM: warps per row.  U accesses of each tensor under way per lane.
-template <typename T, int V, int TEAM, int U>
-__global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) {
+template <typename T, int V, int TEAM, int U, bool CLAMP>
+__global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 6) swiglu_kernel(const SwigluParams p) {
   pdl_wait();
   int r0, r1;
   row_range(p, &r0, &r1);
+  const float L = p.limit;
   constexpr int kStep = 32 * TEAM * V;  // columns per access of the team
   const int team = static_cast<int>(threadIdx.x) / (32 * TEAM);
   const int lane = static_cast<int>(threadIdx.x) % (32 * TEAM);
@@ -90,9 +94,12 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) 
           Pack<T, V> o;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const float a = clamp_gate(to_f32<T>(g[k].v[i]), p.limit);
-            const float b = clamp_up(to_f32<T>(u[k].v[i]), p.limit);
-            o.v[i] = from_f32<T>(s * divide<T>(a, 1.0f + exp_of<T>(-a)) * b);
+            float a = to_f32<T>(g[k].v[i]), b = to_f32<T>(u[k].v[i]);
+            if (CLAMP) {
+              a = min_nan(a, L);
+              b = max_nan(min_nan(b, L), -L);
+            }
+            o.v[i] = from_f32<T>(s * b * (a * sigmoid_of<T>(a)));
           }
           *reinterpret_cast<Pack<T, V>*>(out + c0 + k * kStep) = o;
         }
@@ -100,8 +107,8 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) 
   }
 }
 
-template <typename T, int V, int TEAM, int U>
-__global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluParams p) {
+template <typename T, int V, int TEAM, int U, bool CLAMP>
+__global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 6) swiglu_backward_kernel(const SwigluParams p) {
   __shared__ float sums[kWarps];
   pdl_wait();
   int r0, r1;
@@ -137,14 +144,23 @@ __global__ void __launch_bounds__(kThreads) swiglu_backward_kernel(const SwigluP
           for (int i = 0; i < V; ++i) {
             const float gf = to_f32<T>(g[k].v[i]), uf = to_f32<T>(u[k].v[i]);
             const float df = to_f32<T>(d[k].v[i]);
-            const float a = clamp_gate(gf, L), b = clamp_up(uf, L);
-            const float sg = divide<T>(1.0f, 1.0f + exp_of<T>(-a));
+            float a = gf, b = uf;
+            if (CLAMP) {
+              a = min_nan(gf, L);
+              b = max_nan(min_nan(uf, L), -L);
+            }
+            const float sg = sigmoid_of<T>(a);
             const float silu = a * sg;
-            acc += df * silu * b;
-            const float dgv = df * s * b * sg * (1.0f + a * (1.0f - sg));
-            const float duv = df * s * silu;
-            dg.v[i] = from_f32<T>(L > 0.f && gf > L ? 0.f : dgv);
-            du.v[i] = from_f32<T>(L > 0.f && fabsf(uf) > L ? 0.f : duv);
+            const float ds = df * s, db = df * b;
+            acc = fmaf(db, silu, acc);
+            float dgv = ds * b * sg * fmaf(a, 1.0f - sg, 1.0f);
+            float duv = ds * silu;
+            if (CLAMP) {
+              dgv = gf > L ? 0.f : dgv;
+              duv = fabsf(uf) > L ? 0.f : duv;
+            }
+            dg.v[i] = from_f32<T>(dgv);
+            du.v[i] = from_f32<T>(duv);
           }
           *reinterpret_cast<Pack<T, V>*>(dgate + c0 + k * kStep) = dg;
           *reinterpret_cast<Pack<T, V>*>(dup + c0 + k * kStep) = du;
@@ -184,15 +200,23 @@ bool vec_ok(const SwigluParams& p, bool backward) {
   return ok(p.dout, p.ld_dout) && ok(p.dgate, p.ld_dgate) && ok(p.dup, p.ld_dup);
 }
 
-template <typename T, int V, int TEAM>
-cudaError_t launch(const SwigluParams& p, bool backward, cudaStream_t st) {
-  // about 100 bytes per lane under way
-  constexpr int U = V == 1 ? 8 : (TEAM == 1 ? 2 : 1);
+template <typename T, int V, int TEAM, bool CLAMP>
+cudaError_t launch_clamp(const SwigluParams& p, bool backward, cudaStream_t st) {
+  // of 16-byte accesses one per tensor is under way in a lane, and registers are
+  // held to 6 CTAs per SM (32768 x 1280 with clamp and scale: backward 66 us so,
+  // 78 at 3 CTAs, 109 with two accesses per tensor); of one element, 8
+  constexpr int U = V == 1 ? 8 : 1;
   constexpr int kTeams = kWarps / TEAM;
   const dim3 grid(static_cast<unsigned>(std::min((p.rows + kTeams - 1) / kTeams, 1 << 20)));
-  return backward
-             ? launch_pdl(swiglu_backward_kernel<T, V, TEAM, U>, grid, dim3(kThreads), 0, st, p)
-             : launch_pdl(swiglu_kernel<T, V, TEAM, U>, grid, dim3(kThreads), 0, st, p);
+  return backward ? launch_pdl(swiglu_backward_kernel<T, V, TEAM, U, CLAMP>, grid, dim3(kThreads),
+                               0, st, p)
+                  : launch_pdl(swiglu_kernel<T, V, TEAM, U, CLAMP>, grid, dim3(kThreads), 0, st, p);
+}
+
+template <typename T, int V, int TEAM>
+cudaError_t launch(const SwigluParams& p, bool backward, cudaStream_t st) {
+  return p.limit > 0.f ? launch_clamp<T, V, TEAM, true>(p, backward, st)
+                       : launch_clamp<T, V, TEAM, false>(p, backward, st);
 }
 
 template <typename T>
