@@ -62,6 +62,14 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   return v;
 }
 
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // This CTA's sub-slots [kb0, kb1) of a contraction shared by `split` CTAs.
 __device__ __forceinline__ void my_slots(int depth, int rank, int split, int* kb0, int* kb1) {
   const int nkb = (depth + 63) >> 6;
@@ -130,7 +138,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, p.bn);
   tc_fence_before();
   __syncthreads();
-  if (split > 1) cluster_sync_all();  // every CTA's barriers are ready before remote use
+  // this CTA's barriers are ready; the peers' are needed only where the partials
+  // meet, so the loads do not wait for them
+  if (split > 1) cluster_arrive();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int f_tiles = (p.feats + kProductBM - 1) / kProductBM;
@@ -138,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         ? p.groups * f_tiles * ((p.cols + p.bn - 1) / p.bn)
                         : tab.block_start[p.groups] * f_tiles;
 
+  bool peers_ready = false;  // this warp has passed the cluster barrier above
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const uint64_t pol = l2_policy_evict_normal();
@@ -324,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (c + i < t.n_valid) part[(c + i) * kProductBM] = __uint_as_float(r[i]);
       }
       __syncwarp();
+      cluster_wait();
+      peers_ready = true;
       if (lane < split) mbar_arrive_cluster(mapa_shared(xfull, lane));
       int go = 1;
       if (lane == 0) go = mbar_wait_cluster(xfull, 0, abort_flag, p.status) ? 1 : 0;
@@ -364,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   tc_fence_before();
+  if (split > 1 && !peers_ready) cluster_wait();
   __syncthreads();
   if (split > 1) cluster_sync_all();  // no CTA leaves while its peers may still reach it
   if (warp == 1) {

@@ -15,128 +15,121 @@ using namespace product;
 
 constexpr int kPackThreads = 256;
 
-// One CTA per row of any of the operands.
+// One warp per row of any of the operands.
 __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParams p) {
   pdl_wait();
-  int64_t row = blockIdx.x;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * (kPackThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   int i = 0;
-  while (row >= p.op[i].groups * p.op[i].rows) row -= p.op[i].groups * p.op[i].rows, ++i;
+  while (i < 3 && row >= p.op[i].groups * p.op[i].rows) {
+    row -= p.op[i].groups * p.op[i].rows;
+    ++i;
+  }
+  if (i == 3) return;
   const PackOperand& o = p.op[i];
   const int64_t g = row / o.rows;
   const uint16_t* s = static_cast<const uint16_t*>(o.src) + g * o.group_stride + (row - g * o.rows) * o.ld;
   uint16_t* d = static_cast<uint16_t*>(o.dst) + row * o.ld_dst;
-  constexpr int U = 4;  // loads under way per thread
-  for (int c = threadIdx.x; c < o.cols; c += U * kPackThreads) {
+  constexpr int U = 8;  // loads under way per lane
+  for (int c = lane; c < o.cols; c += U * 32) {
     uint16_t v[U];
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if (c + k * kPackThreads < o.cols) v[k] = s[c + k * kPackThreads];
+      if (c + k * 32 < o.cols) v[k] = s[c + k * 32];
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if (c + k * kPackThreads < o.cols) d[c + k * kPackThreads] = v[k];
+      if (c + k * 32 < o.cols) d[c + k * 32] = v[k];
   }
 }
 
 constexpr int kGradThreads = 256;          // 8 warps: rows of a chunk are dealt to them
 constexpr int kGradWarps = kGradThreads / 32;
 constexpr int kVec = 8;                    // elements per 16-byte access
-constexpr int kGradCols = 32 * kVec;       // columns per CTA
+// elements of a row per lane: one 16-byte piece, or two single ones 32 apart
+template <bool VEC>
+constexpr int kLaneCols = VEC ? kVec : 2;
 
 template <typename T>
 struct alignas(16) Vec {
   T v[kVec];
 };
 
-// One CTA: 64 rows of one group x 256 columns, or with `direct` all rows of
-// the group.  The column sums are added in fp32, per warp over its rows, then
-// over the warps in order; direct: they are the group's and go to db at once.
-// VEC: every row starts at a 16-byte boundary and cols % 8 == 0.  Each lane
-// keeps U rows' loads under way.
+// One CTA: 32 rows of one group x 256 columns (64 where the rows are not
+// aligned), or with `direct` all rows of the group.  The column sums are added
+// in fp32, per warp over its rows, then over the warps in order; direct: they
+// are the group's and go to db at once.  VEC: every row starts at a 16-byte
+// boundary and cols % 8 == 0.  Each lane keeps U rows' loads under way.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kGradThreads) row_grad_kernel(const RowGradParams p) {
+__global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGradParams p) {
+  constexpr int E = kLaneCols<VEC>;
+  constexpr int U = VEC ? 2 : 8;
+  constexpr int kCols = 32 * E;
   extern __shared__ int tab_mem[];
-  __shared__ float sums[kGradWarps][kGradCols];
+  __shared__ float sums[kGradWarps][kCols];
   pdl_wait();
   const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, kRowChunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col_blocks = (p.cols + kGradCols - 1) / kGradCols;
+  const int col_blocks = (p.cols + kCols - 1) / kCols;
   const int total = (p.direct ? p.groups : tab.block_start[p.groups]) * col_blocks;
   const T* dout = static_cast<const T*>(p.dout);
   const T* preact = static_cast<const T*>(p.preact);
   T* dz = static_cast<T*>(p.dz);
-  constexpr int U = VEC ? 4 : 2;
   for (int w = blockIdx.x; w < total; w += gridDim.x) {
     const int chunk = w / col_blocks;  // (direct: the group)
-    const int c0 = (w - chunk * col_blocks) * kGradCols;
+    const int c0 = (w - chunk * col_blocks) * kCols;
     const int g = p.direct ? chunk : group_of_block(tab, p.groups, chunk);
     const int first = p.direct ? 0 : (chunk - tab.block_start[g]) * kRowChunk;
     const int n = p.direct ? tab.count(g) : min(kRowChunk, tab.count(g) - first);
     const int64_t row0 = static_cast<int64_t>(tab.row0[g]) + first;
-    float acc[kVec] = {};
-    // column of element i of this lane: contiguous pieces, or 32 apart
+    float acc[E] = {};
     const int col = VEC ? c0 + lane * kVec : c0 + lane;
     if (col < p.cols) {
       for (int r = warp; r < n; r += U * kGradWarps) {
-        if (VEC) {
-          Vec<T> d[U], z[U];
+        // the rows' values, loaded before the first is used
+        Vec<T> dv[U], zv[U];
 #pragma unroll
-          for (int k = 0; k < U; ++k)
-            if (r + k * kGradWarps < n) {
-              const int64_t row = row0 + r + k * kGradWarps;
-              d[k] = *reinterpret_cast<const Vec<T>*>(dout + row * p.ld_dout + col);
-              if (preact != nullptr)
-                z[k] = *reinterpret_cast<const Vec<T>*>(preact + row * p.ld_preact + col);
-            }
+        for (int k = 0; k < U; ++k) {
+          if (r + k * kGradWarps >= n) break;
+          const int64_t row = row0 + r + k * kGradWarps;
+          const T* d = dout + row * p.ld_dout + col;
+          const T* z = preact + row * p.ld_preact + col;
+          if (VEC) {
+            dv[k] = *reinterpret_cast<const Vec<T>*>(d);
+            if (preact != nullptr) zv[k] = *reinterpret_cast<const Vec<T>*>(z);
+          } else {
 #pragma unroll
-          for (int k = 0; k < U; ++k)
-            if (r + k * kGradWarps < n) {
+            for (int i = 0; i < E; ++i)
+              if (col + 32 * i < p.cols) {
+                dv[k].v[i] = d[32 * i];
+                if (preact != nullptr) zv[k].v[i] = z[32 * i];
+              }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          if (r + k * kGradWarps >= n) break;
+          T* out = dz + (row0 + r + k * kGradWarps) * p.ld_dz + col;
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (VEC || col + 32 * i < p.cols) {
+              float v = to_f32<T>(dv[k].v[i]);
               if (preact != nullptr) {
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                  const float v =
-                      to_f32<T>(d[k].v[i]) * activation_slope(to_f32<T>(z[k].v[i]), p.act);
-                  acc[i] += v;
-                  d[k].v[i] = from_f32<T>(v);
-                }
-                *reinterpret_cast<Vec<T>*>(dz + (row0 + r + k * kGradWarps) * p.ld_dz + col) = d[k];
-              } else {
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) acc[i] += to_f32<T>(d[k].v[i]);
+                v *= activation_slope(to_f32<T>(zv[k].v[i]), p.act);
+                dv[k].v[i] = from_f32<T>(v);
+                if (!VEC) out[32 * i] = dv[k].v[i];
               }
+              acc[i] += v;
             }
-        } else {
-          T d[U][kVec], z[U][kVec];
-#pragma unroll
-          for (int k = 0; k < U; ++k)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i)
-              if (r + k * kGradWarps < n && col + 32 * i < p.cols) {
-                const int64_t row = row0 + r + k * kGradWarps;
-                d[k][i] = dout[row * p.ld_dout + col + 32 * i];
-                if (preact != nullptr) z[k][i] = preact[row * p.ld_preact + col + 32 * i];
-              }
-#pragma unroll
-          for (int k = 0; k < U; ++k)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i)
-              if (r + k * kGradWarps < n && col + 32 * i < p.cols) {
-                const int64_t row = row0 + r + k * kGradWarps;
-                float v = to_f32<T>(d[k][i]);
-                if (preact != nullptr) {
-                  v *= activation_slope(to_f32<T>(z[k][i]), p.act);
-                  dz[row * p.ld_dz + col + 32 * i] = from_f32<T>(v);
-                }
-                acc[i] += v;
-              }
+          if (VEC && preact != nullptr) *reinterpret_cast<Vec<T>*>(out) = dv[k];
         }
       }
     }
     if (p.db != nullptr) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) sums[warp][VEC ? lane * kVec + i : lane + 32 * i] = acc[i];
+      for (int i = 0; i < E; ++i) sums[warp][VEC ? lane * kVec + i : lane + 32 * i] = acc[i];
       __syncthreads();
       const int c = c0 + threadIdx.x;
-      if (c < p.cols) {
+      if (threadIdx.x < kCols && c < p.cols) {
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < kGradWarps; ++i) v += sums[i][threadIdx.x];
@@ -194,8 +187,8 @@ cudaError_t row_grad(const RowGradParams& p, int num_sms, cudaStream_t st) {
                     (rows_aligned(p.preact, p.ld_preact) && rows_aligned(p.dz, p.ld_dz)));
   const int64_t items = static_cast<int64_t>(p.direct ? p.groups
                                                       : row_grad_chunks(p.rows, p.groups) + 1) *
-                        ((p.cols + kGradCols - 1) / kGradCols);
-  const int grid = static_cast<int>(std::min<int64_t>(items, 6 * num_sms));
+                        ((p.cols + (vec ? 32 * kVec : 64) - 1) / (vec ? 32 * kVec : 64));
+  const int grid = static_cast<int>(std::min<int64_t>(items, 8 * num_sms));
   cudaError_t e;
   if (vec)
     e = launch_pdl(row_grad_kernel<T, true>, dim3(grid), dim3(kGradThreads), tab, st, p);
@@ -213,9 +206,10 @@ cudaError_t launch_pack_rows(const PackParams& p, cudaStream_t st) {
   int64_t rows = 0;
   for (const PackOperand& o : p.op) rows += o.groups * o.rows;
   if (rows == 0) return cudaSuccess;
+  constexpr int kPer = kPackThreads / 32;
   if (rows > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(pack_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(kPackThreads), 0, st,
-                    p);
+  return launch_pdl(pack_rows_kernel, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),
+                    dim3(kPackThreads), 0, st, p);
 }
 
 cudaError_t launch_row_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st) {

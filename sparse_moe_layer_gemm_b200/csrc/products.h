@@ -98,12 +98,12 @@ struct RowGradParams {
   int act;
   void* db;            // [groups, cols] or nullptr
   // db of few rows: a CTA sums all rows of a group, in the one launch; else each
-  // CTA sums a 64-row chunk into partial [chunks, cols] and a second launch
+  // CTA sums a 32-row chunk into partial [chunks, cols] and a second launch
   // adds the chunks
   bool direct;
   float* partial;
 };
-constexpr int kRowChunk = 64;
+constexpr int kRowChunk = 32;
 // Up to here a CTA walks its group's rows alone: 16 rows per warp at most.
 constexpr int kRowDirect = 128;
 inline size_t row_grad_chunks(int rows, int groups) {
