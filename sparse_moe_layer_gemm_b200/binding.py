@@ -722,44 +722,40 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # mo
 _OP_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 
 
-class _Launch:
-    """Makes a tensor's device (and the caller's stream, if given) current, so
-    that what a call allocates belongs to the stream that it runs on; enters
-    as the raw stream."""
-
-    __slots__ = ("_ctx", "_raw")
+class _Elsewhere:
+    """Makes a tensor's device and the caller's stream (if given) current, so
+    that what a call allocates belongs to the stream that it runs on."""
 
     def __init__(self, t: torch.Tensor, stream):
         dev = t.device
-        if dev.type != "cuda":
-            raise ValueError(f"want tensors on a CUDA device, got {dev}")
-        if stream is None and dev.index == torch.cuda.current_device():
-            self._ctx = ()
-            self._raw = torch._C._cuda_getCurrentRawStream(dev.index)
-            return
         s = torch.cuda.current_stream(dev) if stream is None else \
             stream if isinstance(stream, torch.cuda.Stream) else \
             torch.cuda.ExternalStream(int(stream), device=dev)
         if s.device != dev:
             raise ValueError(f"stream on {s.device}, tensors on {dev}")
         self._ctx = (torch.cuda.device(dev), torch.cuda.stream(s))
-        self._raw = s.cuda_stream
 
     def __enter__(self):
         for c in self._ctx:
             c.__enter__()
-        return self._raw
 
     def __exit__(self, *exc):
         for c in reversed(self._ctx):
             c.__exit__(*exc)
 
 
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on t has to change the current device or stream first."""
+    if not t.is_cuda:
+        raise ValueError(f"want tensors on a CUDA device, got {t.device}")
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
 def _need_rows(t: torch.Tensor, name: str, like: torch.Tensor, rows: int, cols: int) -> int:
     """Checks a [rows, cols] tensor of like's type and device with contiguous
     rows; returns its row stride."""
-    if t is not like and (t.shape != (rows, cols) or t.dtype != like.dtype
-                          or t.device != like.device):
+    if t is not like and (t.shape != (rows, cols) or t.dtype is not like.dtype
+                          or t.get_device() != like.get_device()):
         raise ValueError(f"{name}: want {like.dtype} {(rows, cols)} on {like.device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     ld, step = t.stride()
@@ -774,7 +770,7 @@ def _need_rows(t: torch.Tensor, name: str, like: torch.Tensor, rows: int, cols: 
 
 def _need_vec(t: torch.Tensor, name: str, like: torch.Tensor, shape, dtype=None):
     dtype = like.dtype if dtype is None else dtype
-    if t.shape != shape or t.dtype != dtype or t.device != like.device or \
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device() or \
             not t.is_contiguous():
         raise ValueError(f"{name}: want contiguous {dtype} {tuple(shape)} on {like.device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -788,7 +784,8 @@ def _product_setup(t, w, offsets, cols_dim, activation, name):
     shape, ws = t.shape, w.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: want [rows, features], got {tuple(shape)}")
-    if len(ws) != (2 if offsets is None else 3) or w.dtype != t.dtype or w.device != t.device:
+    if len(ws) != (2 if offsets is None else 3) or w.dtype is not t.dtype or \
+            w.get_device() != t.get_device():
         raise ValueError(f"w: want {t.dtype} {'[K, N]' if offsets is None else '[G, K, N]'} on "
                          f"{t.device}, got {w.dtype} {tuple(ws)} on {w.device}")
     K, N = ws[-2], ws[-1]
@@ -819,7 +816,6 @@ def _workspace(n: int, device) -> Optional[torch.Tensor]:
 
 
 def _linear(x, offsets, w, bias, residual, activation, out, preact, stream):
-    lib = load_library()
     cfg, K, N, G, ld_w, gs = _product_setup(x, w, offsets, 0, activation, "x")
     R = x.shape[0]
     ld_x = _need_rows(x, "x", x, R, K)
@@ -827,20 +823,27 @@ def _linear(x, offsets, w, bias, residual, activation, out, preact, stream):
         _need_vec(bias, "bias", x, (G, N) if G else (N,))
     ld_res = _need_rows(residual, "residual", x, R, N) if residual is not None else 0
     ld_pre = _need_rows(preact, "preact", x, R, N) if preact is not None else 0
-    with _Launch(x, stream) as st:
-        if out is None:
-            out = x.new_empty((R, N))
-        ld_out = _need_rows(out, "out", x, R, N)
-        args = moe_linear_args_t(x.data_ptr(), ld_x, _ptr(offsets), w.data_ptr(), ld_w, gs,
-                                 _ptr(bias), _ptr(residual), ld_res, out.data_ptr(), ld_out,
-                                 _ptr(preact), ld_pre)
-        status = lib.moe_linear(cfg, args, None, 0, st)
-        if status == MOE_ERR_WORKSPACE:  # misaligned operands are copied first
-            n = ctypes.c_size_t()
-            _check(lib.moe_linear_workspace_size(cfg, args, n), "moe_linear")
-            ws = _workspace(n.value, x.device)
-            status = lib.moe_linear(cfg, args, ws.data_ptr(), n.value, st)
-        _check(status, "moe_linear")
+    if _elsewhere(x, stream):
+        with _Elsewhere(x, stream):
+            return _linear(x, offsets, w, bias, residual, activation, out, preact, None)
+    st = torch._C._cuda_getCurrentRawStream(x.get_device())
+    if out is None:
+        out = x.new_empty((R, N))
+    ld_out = _need_rows(out, "out", x, R, N)
+    args = moe_linear_args_t(x.data_ptr(), ld_x, None if offsets is None else offsets.data_ptr(),
+                             w.data_ptr(), ld_w, gs, None if bias is None else bias.data_ptr(),
+                             None if residual is None else residual.data_ptr(), ld_res,
+                             out.data_ptr(), ld_out, None if preact is None else preact.data_ptr(),
+                             ld_pre)
+    lib = load_library()
+    status = lib.moe_linear(cfg, args, None, 0, st)
+    if status == MOE_ERR_WORKSPACE:  # misaligned operands are copied first
+        n = ctypes.c_size_t()
+        _check(lib.moe_linear_workspace_size(cfg, args, n), "moe_linear")
+        ws = _workspace(n.value, x.device)
+        status = lib.moe_linear(cfg, args, ws.data_ptr(), n.value, st)
+    if status:
+        raise MoeError(status, "moe_linear")
     return out
 
 
@@ -870,7 +873,6 @@ def grouped_linear(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
 
 
 def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream):
-    lib = load_library()
     cfg, K, N, G, ld_w, gs = _product_setup(dout, w, offsets, 1, activation, "dout")
     R = dout.shape[0]
     ld_dout = _need_rows(dout, "dout", dout, R, N)
@@ -884,26 +886,30 @@ def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream
         raise ValueError("preact: wanted exactly when there is an activation")
     ld_pre = _need_rows(preact, "preact", dout, R, N) if preact is not None else 0
     dx, dw, db = into
-    with _Launch(dout, stream) as st:
-        if need[0] and dx is None:
-            dx = dout.new_empty((R, K))
-        if need[1] and dw is None:
-            dw = dout.new_empty(w.shape)
-        if need[2] and db is None:
-            db = dout.new_empty((G, N) if G else (N,))
-        dx, dw, db = (t if n else None for t, n in zip((dx, dw, db), need))
-        ld_dx = _need_rows(dx, "dx", dout, R, K) if dx is not None else 0
-        if dw is not None:
-            _need_vec(dw, "dw", dout, w.shape)
-        if db is not None:
-            _need_vec(db, "db", dout, (G, N) if G else (N,))
-        grads = moe_linear_grads_t(dout.data_ptr(), ld_dout, _ptr(x) if need[1] else None, ld_x,
-                                   _ptr(offsets), w.data_ptr() if need[0] else None, ld_w, gs,
-                                   _ptr(preact), ld_pre, _ptr(dx), ld_dx, _ptr(dw), _ptr(db))
-        n = ctypes.c_size_t()
-        _check(lib.moe_linear_backward_workspace_size(cfg, grads, n), "moe_linear_backward")
-        ws = _workspace(n.value, dout.device)
-        _check(lib.moe_linear_backward(cfg, grads, _ptr(ws), n.value, st), "moe_linear_backward")
+    if _elsewhere(dout, stream):
+        with _Elsewhere(dout, stream):
+            return _linear_backward(dout, x, offsets, w, preact, activation, need, into, None)
+    st = torch._C._cuda_getCurrentRawStream(dout.get_device())
+    if need[0] and dx is None:
+        dx = dout.new_empty((R, K))
+    if need[1] and dw is None:
+        dw = dout.new_empty(w.shape)
+    if need[2] and db is None:
+        db = dout.new_empty((G, N) if G else (N,))
+    dx, dw, db = (t if n else None for t, n in zip((dx, dw, db), need))
+    ld_dx = _need_rows(dx, "dx", dout, R, K) if dx is not None else 0
+    if dw is not None:
+        _need_vec(dw, "dw", dout, w.shape)
+    if db is not None:
+        _need_vec(db, "db", dout, (G, N) if G else (N,))
+    grads = moe_linear_grads_t(dout.data_ptr(), ld_dout, _ptr(x) if need[1] else None, ld_x,
+                               _ptr(offsets), w.data_ptr() if need[0] else None, ld_w, gs,
+                               _ptr(preact), ld_pre, _ptr(dx), ld_dx, _ptr(dw), _ptr(db))
+    lib = load_library()
+    n = ctypes.c_size_t()
+    _check(lib.moe_linear_backward_workspace_size(cfg, grads, n), "moe_linear_backward")
+    ws = _workspace(n.value, dout.device)
+    _check(lib.moe_linear_backward(cfg, grads, _ptr(ws), n.value, st), "moe_linear_backward")
     return dx, dw, db
 
 
@@ -944,10 +950,11 @@ def linear_device_error(device=None) -> int:
 
 
 def _swiglu_setup(gate, up, scale, limit, offsets):
-    if gate.dim() != 2 or gate.dtype not in _OP_DTYPES:
+    dtype, shape = _OP_DTYPES.get(gate.dtype), gate.shape
+    if dtype is None or len(shape) != 2:
         raise ValueError(f"gate: want [rows, width] in fp32, bf16 or fp16, got {gate.dtype} "
-                         f"{tuple(gate.shape)}")
-    R, W = gate.shape
+                         f"{tuple(shape)}")
+    R, W = shape
     lds = _need_rows(gate, "gate", gate, R, W), _need_rows(up, "up", gate, R, W)
     if scale is not None:
         _need_vec(scale, "scale", gate, (R,), torch.float32)
@@ -957,7 +964,7 @@ def _swiglu_setup(gate, up, scale, limit, offsets):
             raise ValueError(f"offsets: want [G + 1], got {tuple(offsets.shape)}")
         G = offsets.numel() - 1
         _need_vec(offsets, "offsets", gate, (G + 1,), torch.int32)
-    return moe_swiglu_config_t(R, W, G, _OP_DTYPES[gate.dtype], float(limit)), R, W, lds
+    return moe_swiglu_config_t(R, W, G, dtype, limit), R, W, lds
 
 
 def swiglu(gate: torch.Tensor, up: torch.Tensor, scale: Optional[torch.Tensor] = None, *,
@@ -967,14 +974,20 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, scale: Optional[torch.Tensor] =
     limit 0: no clamp): gate, up, out [R, W] with any row stride (the halves of
     one [R, 2W] tensor, say), fp32, bf16 or fp16; scale [R] fp32.  offsets:
     rows outside [offsets[0], offsets[-1]) are not written."""
-    lib = load_library()
     cfg, R, W, (ldg, ldu) = _swiglu_setup(gate, up, scale, limit, offsets)
-    with _Launch(gate, stream) as st:
-        if out is None:
-            out = gate.new_empty((R, W))
-        ldo = _need_rows(out, "out", gate, R, W)
-        _check(lib.moe_swiglu(cfg, gate.data_ptr(), ldg, up.data_ptr(), ldu,
-                              _ptr(scale), _ptr(offsets), out.data_ptr(), ldo, st), "moe_swiglu")
+    if _elsewhere(gate, stream):
+        with _Elsewhere(gate, stream):
+            return swiglu(gate, up, scale, limit=limit, offsets=offsets, out=out)
+    if out is None:
+        out = gate.new_empty((R, W))
+    ldo = _need_rows(out, "out", gate, R, W)
+    status = load_library().moe_swiglu(
+        cfg, gate.data_ptr(), ldg, up.data_ptr(), ldu,
+        None if scale is None else scale.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), out.data_ptr(), ldo,
+        torch._C._cuda_getCurrentRawStream(gate.get_device()))
+    if status:
+        raise MoeError(status, "moe_swiglu")
     return out
 
 
@@ -985,23 +998,25 @@ def swiglu_backward(dout: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
                     stream=None):
     """(dgate, dup, dscale) of swiglu (moe_swiglu_backward); dscale [R] fp32 is
     None without scale.  dgate and dup may be gate, up or dout themselves."""
-    lib = load_library()
     cfg, R, W, (ldg, ldu) = _swiglu_setup(gate, up, scale, limit, offsets)
     ldd = _need_rows(dout, "dout", gate, R, W)
     if dscale is not None and scale is None:
         raise ValueError("dscale: there is no scale")
-    with _Launch(gate, stream) as st:
-        if dgate is None:
-            dgate = gate.new_empty((R, W))
-        if dup is None:
-            dup = gate.new_empty((R, W))
-        if dscale is None and scale is not None:
-            dscale = torch.empty(R, dtype=torch.float32, device=gate.device)
-        if dscale is not None:
-            _need_vec(dscale, "dscale", gate, (R,), torch.float32)
-        ldg2, ldu2 = _need_rows(dgate, "dgate", gate, R, W), _need_rows(dup, "dup", gate, R, W)
-        _check(lib.moe_swiglu_backward(cfg, dout.data_ptr(), ldd, gate.data_ptr(),
-                                       ldg, up.data_ptr(), ldu, _ptr(scale), _ptr(offsets),
-                                       dgate.data_ptr(), ldg2, dup.data_ptr(), ldu2, _ptr(dscale),
-                                       st), "moe_swiglu_backward")
+    if _elsewhere(gate, stream):
+        with _Elsewhere(gate, stream):
+            return swiglu_backward(dout, gate, up, scale, limit=limit, offsets=offsets,
+                                   dgate=dgate, dup=dup, dscale=dscale)
+    if dgate is None:
+        dgate = gate.new_empty((R, W))
+    if dup is None:
+        dup = gate.new_empty((R, W))
+    if dscale is None and scale is not None:
+        dscale = scale.new_empty((R,))
+    if dscale is not None:
+        _need_vec(dscale, "dscale", gate, (R,), torch.float32)
+    ldg2, ldu2 = _need_rows(dgate, "dgate", gate, R, W), _need_rows(dup, "dup", gate, R, W)
+    _check(load_library().moe_swiglu_backward(
+        cfg, dout.data_ptr(), ldd, gate.data_ptr(), ldg, up.data_ptr(), ldu, _ptr(scale),
+        _ptr(offsets), dgate.data_ptr(), ldg2, dup.data_ptr(), ldu2, _ptr(dscale),
+        torch._C._cuda_getCurrentRawStream(gate.get_device())), "moe_swiglu_backward")
     return dgate, dup, dscale

@@ -389,9 +389,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <int MODE, typename T>
 cudaError_t launch(const ProductMaps& m, const ProductParams& p, size_t smem, int grid,
                    cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(product_kernel<MODE, T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
@@ -410,6 +407,21 @@ cudaError_t launch(const ProductMaps& m, const ProductParams& p, size_t smem, in
 }
 
 }  // namespace
+
+cudaError_t product_configure_device() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  };
+  set(product_kernel<kProductForward, __nv_bfloat16>);
+  set(product_kernel<kProductDx, __nv_bfloat16>);
+  set(product_kernel<kProductDw, __nv_bfloat16>);
+  set(product_kernel<kProductForward, __half>);
+  set(product_kernel<kProductDx, __half>);
+  set(product_kernel<kProductDw, __half>);
+  return e;
+}
 
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p0,
                            int num_sms, cudaStream_t st) {

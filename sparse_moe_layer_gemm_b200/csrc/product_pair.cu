@@ -414,9 +414,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
 
 template <int MODE, int HALVES, typename T>
 cudaError_t launch(const ProductMaps& m, const ProductParams& p, int grid, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(product_pair_kernel<MODE, HALVES, T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (e != cudaSuccess) return e;
   return launch_pdl(product_pair_kernel<MODE, HALVES, T>, dim3(static_cast<unsigned>(grid)),
                     dim3(threads_of(MODE)), PairShape<HALVES>::kSmem + group_table_bytes(p.groups), st, m.a,
                     m.b, p);
@@ -433,6 +430,27 @@ cudaError_t launch_mode(bool bf16, const ProductMaps& m, const ProductParams& p,
 }
 
 }  // namespace
+
+cudaError_t product_pair_configure_device() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  };
+  set(product_pair_kernel<kProductForward, 1, __nv_bfloat16>);
+  set(product_pair_kernel<kProductForward, 2, __nv_bfloat16>);
+  set(product_pair_kernel<kProductDx, 1, __nv_bfloat16>);
+  set(product_pair_kernel<kProductDx, 2, __nv_bfloat16>);
+  set(product_pair_kernel<kProductDw, 1, __nv_bfloat16>);
+  set(product_pair_kernel<kProductDw, 2, __nv_bfloat16>);
+  set(product_pair_kernel<kProductForward, 1, __half>);
+  set(product_pair_kernel<kProductForward, 2, __half>);
+  set(product_pair_kernel<kProductDx, 1, __half>);
+  set(product_pair_kernel<kProductDx, 2, __half>);
+  set(product_pair_kernel<kProductDw, 1, __half>);
+  set(product_pair_kernel<kProductDw, 2, __half>);
+  return e;
+}
 
 cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                                 int num_sms, cudaStream_t st) {

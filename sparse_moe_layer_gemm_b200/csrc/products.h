@@ -70,6 +70,10 @@ constexpr int product_pair_box(int bn) { return bn <= 256 ? bn / 2 : 128; }
 cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                                 int num_sms, cudaStream_t st);
 
+// one-time per-device kernel attributes (dynamic shared memory limits)
+cudaError_t product_configure_device();
+cudaError_t product_pair_configure_device();
+
 // Row kernels (product_rows.cu).
 // Copies of operands with rows of ld_dst elements, all in one launch (groups 0:
 // no operand).

@@ -27,8 +27,9 @@ size_t ws_round(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 // The kernels' status word of each device (set by a bounded wait that gave up).
 __device__ int g_product_status;
 
-// The current device's status word and SM count, looked up once per device
-// (and again if a device reset gave the device another context).
+// The current device's status word and SM count, looked up once per device and
+// host thread (and again if a device reset gave the device another context),
+// with the kernels' attributes set.
 int device_of(int* sms, int** status) {
   struct Entry {
     unsigned long long ctx = 0;
@@ -59,6 +60,8 @@ int device_of(int* sms, int** status) {
     void* p = nullptr;
     MOE_CUDA(cudaGetSymbolAddress(&p, g_product_status));
     MOE_CUDA(cudaDeviceGetAttribute(&e.sms, cudaDevAttrMultiProcessorCount, dev));
+    MOE_CUDA(product_configure_device());
+    MOE_CUDA(product_pair_configure_device());
     e.status = static_cast<int*>(p);
     if (get_ctx(&ctx) != CUDA_SUCCESS || ctx == nullptr || get_id(ctx, &id) != CUDA_SUCCESS)
       return MOE_ERR_CUDA;

@@ -804,7 +804,9 @@ def test_linear_backward_workspace(lib):
     assert size(_cfg(), _grads(w=None, dx=None, dbias=None)) == 0
     with_dz = size(_cfg(activation=2), _grads(preact=OFF, ld_preact=72, dbias=None))
     assert with_dz >= 4 * 72 * 2
-    c, a = _cfg(), _grads()
+    # the column sums of many rows meet in the workspace
+    c, a = _cfg(rows=200), _grads()
+    assert size(c, a) >= 200 // 32 * 72 * 4
     assert lib.moe_linear_backward(ctypes.byref(c), ctypes.byref(a), None, 0, None) == \
         B.MOE_ERR_WORKSPACE
 
