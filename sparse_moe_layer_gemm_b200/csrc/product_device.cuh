@@ -338,7 +338,8 @@ __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable&
 // ---------------------------------------------------------------- epilogue
 // An accumulator holds features on its lanes and output rows on its columns;
 // the output is row-major with features contiguous.  A warp takes 32 features
-// x 16 rows at a time as two 16x256b tensor-memory loads: the values then lie
+// x 32 rows at a time (16 with a residual or pre-activation) as two 16x256b
+// tensor-memory loads per 16 rows: the values then lie
 // in the registers as 8 x 8 matrices (feature lane / 4, rows 2 (lane % 4) and
 // + 1), so after packing two rows into 32 bits one transposing stmatrix per 8
 // rows lays [row][32 features] into shared memory, from where 16-byte pieces
@@ -347,7 +348,7 @@ __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable&
 // output went from 95 to 16 us at a contraction of 64.
 constexpr int kEpiPitch = 80;                  // bytes per staged row: 64 + 16 against bank conflicts
 constexpr int kEpiChunk = 16 * kEpiPitch;      // one staged chunk
-constexpr int kEpiWarpBytes = 2 * kEpiChunk;   // out, and residual / preact
+constexpr int kEpiWarpBytes = 2 * kEpiChunk;   // 32 rows, or 16 and the residual's 16
 
 __device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
@@ -394,20 +395,23 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// 16 staged rows x 32 features <-> global memory at `base` (the chunk's first
+// ROWS staged rows x 32 features <-> global memory at `base` (the chunk's first
 // row and this warp's first feature); n rows and nf features exist.  vec: 16
 // byte pieces (aligned rows, nf a multiple of 8).
-template <typename T>
-__device__ __forceinline__ void copy_out(uint8_t* stg, T* base, int64_t ld, int n, int nf, bool vec,
-                                         int lane) {
+template <typename T, int ROWS>
+__device__ __forceinline__ void copy_out(const uint8_t* stg, T* base, int64_t ld, int n, int nf,
+                                         bool vec, int lane) {
   if (vec) {
-    const int piece = lane & 3;
+    const int piece = lane & 3, row = lane >> 2;
+    uint4 v[ROWS / 8];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = 8 * k + (lane >> 2);
-      if (row < n && piece * 8 < nf)
-        *reinterpret_cast<uint4*>(base + row * ld + piece * 8) =
-            *reinterpret_cast<const uint4*>(stg + row * kEpiPitch + piece * 16);
+    for (int k = 0; k < ROWS / 8; ++k)
+      v[k] = *reinterpret_cast<const uint4*>(stg + (8 * k + row) * kEpiPitch + piece * 16);
+    T* at = base + row * ld + piece * 8;
+    if (piece * 8 < nf) {
+#pragma unroll
+      for (int k = 0; k < ROWS / 8; ++k)
+        if (8 * k + row < n) *reinterpret_cast<uint4*>(at + 8 * k * ld) = v[k];
     }
   } else if (lane < nf) {
     for (int row = 0; row < n; ++row)
@@ -457,13 +461,15 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
 }
 
 // One warp's part of a tile: lanes [32 q, 32 q + 32) of the accumulator at
-// taddr (quadrant and buffer included), 16-row chunks c0, c0 + step, ... below
-// n_valid; row0 the tile's first output row, f0 the warp's first feature.
-// zeros: the contraction was empty.
-template <int MODE, typename T>
-__device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t taddr, int c0, int step,
-                                           int n_valid, int64_t row0, int f0, int g, bool zeros,
-                                           uint8_t* stg, int lane) {
+// taddr (quadrant and buffer included), in chunks of ROWS rows: `part`,
+// part + parts, ... below n_valid; row0 the tile's first output row, f0 the
+// warp's first feature.  zeros: the contraction was empty.  EXTRA: with a
+// residual or the pre-activation, whose staging takes the second 16 rows'.
+template <int MODE, typename T, int ROWS, bool EXTRA>
+__device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t taddr, int part,
+                                             int parts, int n_valid, int64_t row0, int f0, int g,
+                                             bool zeros, uint8_t* stg, int lane) {
+  static_assert(!EXTRA || ROWS == 16, "staging");
   const int nf = p.feats - f0;
   if (nf <= 0) return;
   // matrix m: features 8 m + lane / 4
@@ -477,75 +483,83 @@ __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t tadd
   // stmatrix / ldmatrix: lane 8 m + j addresses row j of matrix m
   const uint32_t mat = smem_u32(stg) + (lane & 7) * kEpiPitch + (lane >> 3) * 16;
   T* out = static_cast<T*>(p.out) + row0 * p.ld_out + f0;
-  uint32_t r[2][8];
+  constexpr int kB = ROWS / 16;  // 16-row loads per chunk
+  uint32_t r[2 * kB][8];
+  auto load = [&](int c) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i >> 3][i & 7] = 0;
-  if (!zeros && c0 < n_valid) {
-    tmem_ld_16x256b_x2(taddr + c0, r[0]);
-    tmem_ld_16x256b_x2(taddr + (16u << 16) + c0, r[1]);
-  }
-  for (int c = c0; c < n_valid; c += step) {
-    const int n = min(16, n_valid - c);
-    if (MODE == kProductForward && p.residual != nullptr)
+    for (int b = 0; b < kB; ++b) {
+      if (c + 16 * b >= n_valid) break;
+      tmem_ld_16x256b_x2(taddr + c + 16 * b, r[2 * b]);
+      tmem_ld_16x256b_x2(taddr + (16u << 16) + c + 16 * b, r[2 * b + 1]);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < 16 * kB; ++i) r[i >> 3][i & 7] = 0;
+  if (!zeros) load(part * ROWS);
+  for (int c = part * ROWS; c < n_valid; c += parts * ROWS) {
+    const int n = min(ROWS, n_valid - c);
+    if (EXTRA && p.residual != nullptr)
       copy_in<T>(stg + kEpiChunk,
                  static_cast<const T*>(p.residual) + (row0 + c) * p.ld_residual + f0,
                  p.ld_residual, n, nf, p.vec_residual, lane);
     if (!zeros) tmem_ld_wait();
     // v[8 k + 2 m + e]: rows 8 k + 2 (lane % 4) + e of matrix m
-    float v[16];
+    float v[16 * kB];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2 * kB; ++k)
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          v[8 * k + 2 * m + e] = __uint_as_float(r[m >> 1][4 * k + 2 * (m & 1) + e]) + bias[m];
+          v[8 * k + 2 * m + e] =
+              __uint_as_float(r[2 * (k >> 1) + (m >> 1)][4 * (k & 1) + 2 * (m & 1) + e]) + bias[m];
     // the next chunk's load runs below this one's arithmetic and stores
-    if (!zeros && c + step < n_valid) {
-      tmem_ld_16x256b_x2(taddr + c + step, r[0]);
-      tmem_ld_16x256b_x2(taddr + (16u << 16) + c + step, r[1]);
-    }
-    if (MODE == kProductForward) {
-      if (p.preact != nullptr) {
+    if (!zeros && c + parts * ROWS < n_valid) load(c + parts * ROWS);
+    auto stage = [&]() {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t w[4] = {pack2<T>(v[8 * k], v[8 * k + 1]), pack2<T>(v[8 * k + 2], v[8 * k + 3]),
-                                 pack2<T>(v[8 * k + 4], v[8 * k + 5]),
-                                 pack2<T>(v[8 * k + 6], v[8 * k + 7])};
-          stmatrix_x4_trans(mat + k * 8 * kEpiPitch, w);
-        }
-        __syncwarp();
-        copy_out<T>(stg, static_cast<T*>(p.preact) + (row0 + c) * p.ld_preact + f0, p.ld_preact, n,
-                    nf, p.vec_preact, lane);
-        __syncwarp();
+      for (int k = 0; k < 2 * kB; ++k) {
+        const uint32_t w[4] = {pack2<T>(v[8 * k], v[8 * k + 1]), pack2<T>(v[8 * k + 2], v[8 * k + 3]),
+                               pack2<T>(v[8 * k + 4], v[8 * k + 5]),
+                               pack2<T>(v[8 * k + 6], v[8 * k + 7])};
+        stmatrix_x4_trans(mat + k * 8 * kEpiPitch, w);
       }
-      activate_all(v, p.act);
-      if (p.residual != nullptr) {
-        __syncwarp();
+      __syncwarp();
+    };
+    if (EXTRA && p.preact != nullptr) {
+      stage();
+      copy_out<T, ROWS>(stg, static_cast<T*>(p.preact) + (row0 + c) * p.ld_preact + f0, p.ld_preact,
+                        n, nf, p.vec_preact, lane);
+      __syncwarp();
+    }
+    if (MODE == kProductForward) activate_all(v, p.act);
+    if (EXTRA && p.residual != nullptr) {
+      __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t w[4];
-          ldmatrix_x4_trans(mat + kEpiChunk + k * 8 * kEpiPitch, w);
+      for (int k = 0; k < 2; ++k) {
+        uint32_t w[4];
+        ldmatrix_x4_trans(mat + kEpiChunk + k * 8 * kEpiPitch, w);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float2 f = unpack2<T>(w[m]);
-            v[8 * k + 2 * m] += f.x;
-            v[8 * k + 2 * m + 1] += f.y;
-          }
+        for (int m = 0; m < 4; ++m) {
+          const float2 f = unpack2<T>(w[m]);
+          v[8 * k + 2 * m] += f.x;
+          v[8 * k + 2 * m + 1] += f.y;
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t w[4] = {pack2<T>(v[8 * k], v[8 * k + 1]), pack2<T>(v[8 * k + 2], v[8 * k + 3]),
-                             pack2<T>(v[8 * k + 4], v[8 * k + 5]),
-                             pack2<T>(v[8 * k + 6], v[8 * k + 7])};
-      stmatrix_x4_trans(mat + k * 8 * kEpiPitch, w);
-    }
-    __syncwarp();
-    copy_out<T>(stg, out + c * p.ld_out, p.ld_out, n, nf, p.vec_out, lane);
+    stage();
+    copy_out<T, ROWS>(stg, out + c * p.ld_out, p.ld_out, n, nf, p.vec_out, lane);
     __syncwarp();
   }
+}
+
+template <int MODE, typename T>
+__device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t taddr, int part,
+                                           int parts, int n_valid, int64_t row0, int f0, int g,
+                                           bool zeros, uint8_t* stg, int lane) {
+  if (MODE == kProductForward && (p.preact != nullptr || p.residual != nullptr))
+    store_chunks<MODE, T, 16, true>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
+  else
+    store_chunks<MODE, T, 32, false>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
 }
 
 // Four neighbouring features of a row of the split form.

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
       if (split == 1) {
-        store_tile<MODE, T>(p, taddr, 0, 16, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
+        store_tile<MODE, T>(p, taddr, 0, 1, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
         if (!empty) {
           tc_fence_before();
           __syncwarp();

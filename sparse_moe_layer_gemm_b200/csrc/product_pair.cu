@@ -21,7 +21,7 @@
 // Roles per CTA (10 warps): warp 0 TMA producer (own halves; every load
 // completes on the leader's full barrier), warp 1 tensor memory and (leader)
 // MMA issue, warps 2-9 epilogue, two per accumulator lane quadrant on
-// alternate 16-row chunks.  Accumulators are taken in turn, one per half, so
+// alternate chunks of rows.  Accumulators are taken in turn, one per half, so
 // tiles of one half still double-buffer.  Every wait is bounded.  No TMA
 // multicast.
 //
@@ -387,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
           tc_fence_after();
         }
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
-        store_tile<MODE, T>(p, taddr, 16 * part, 32, min(hn, t.n_valid - h * hn), row0 + h * hn,
+        store_tile<MODE, T>(p, taddr, part, 2, min(hn, t.n_valid - h * hn), row0 + h * hn,
                             t.f0 + static_cast<int>(rank) * kProductBM + q * 32, t.g, empty, stg,
                             lane);
         if (!empty) {
