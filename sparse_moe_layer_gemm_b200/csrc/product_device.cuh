@@ -296,30 +296,33 @@ struct Tile {
 // Tile w.  Inside a group, chunks of p.chunk row blocks run feature-major: a
 // weight tile's readers follow one another, and the chunk's rows stay in L2
 // across its weight tiles.
+__device__ __forceinline__ int divide(int n, const FastDiv& f) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(n), f.mul) + static_cast<uint32_t>(n)) >>
+                          f.shift);
+}
+
 template <int MODE, int BM>
 __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable& t, int w) {
   Tile r;
-  const int f_tiles = (p.feats + BM - 1) / BM;
-  int local, blocks, in_chunk_first;
+  int local, blocks;
+  const int b = divide(w, p.by_group);  // dw: the group, else the row block over all groups
   if (MODE == kProductDw) {
-    blocks = (p.cols + p.bn - 1) / p.bn;
-    const int per_group = f_tiles * blocks;
-    r.g = w / per_group;
-    local = w - r.g * per_group;
+    blocks = p.dw_blocks;
+    r.g = b;
+    local = w - b * static_cast<int>(p.by_group.d);
   } else {
-    // tiles before group g: block_start[g] * f_tiles
-    const int b = w / f_tiles;
     r.g = group_of_block(t, p.groups, b);
-    local = w - t.block_start[r.g] * f_tiles;
+    local = w - t.block_start[r.g] * p.f_tiles;
     blocks = t.block_start[r.g + 1] - t.block_start[r.g];
   }
-  const int per_chunk = f_tiles * p.chunk;
-  const int c = local / per_chunk;
-  const int rem = local - c * per_chunk;
-  in_chunk_first = c * p.chunk;
-  const int in_chunk = min(p.chunk, blocks - in_chunk_first);
-  const int ft = rem / in_chunk;
-  const int nb = in_chunk_first + (rem - ft * in_chunk);
+  const int c = divide(local, p.by_chunk);
+  const int rem = local - c * static_cast<int>(p.by_chunk.d);
+  const int first = c * p.chunk;
+  const int in_chunk = min(p.chunk, blocks - first);
+  // rem < 2^13, in_chunk <= 16: the rounded quotient of rem + 1/2 truncates right
+  const int ft = static_cast<int>((static_cast<float>(rem) + 0.5f) *
+                                  reciprocal(static_cast<float>(in_chunk)));
+  const int nb = first + (rem - ft * in_chunk);
   r.f0 = ft * BM;
   if (MODE == kProductDw) {
     r.j0 = nb * p.bn;

@@ -143,10 +143,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (split > 1) cluster_arrive();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int f_tiles = (p.feats + kProductBM - 1) / kProductBM;
-  const int total = MODE == kProductDw
-                        ? p.groups * f_tiles * ((p.cols + p.bn - 1) / p.bn)
-                        : tab.block_start[p.groups] * f_tiles;
+  const int total = p.f_tiles * (MODE == kProductDw ? p.groups * p.dw_blocks
+                                                    : tab.block_start[p.groups]);
 
   bool peers_ready = false;  // this warp has passed the cluster barrier above
   if (warp == 0) {
@@ -429,17 +427,7 @@ cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const Prod
   const size_t fixed = 1024 + kEpiBytes + kBarBytes +
                        static_cast<size_t>(group_table_bytes(p.groups));
   const size_t slot = kSubs * (kABytes + static_cast<size_t>(b_bytes(mode, p.bn)));
-  const int64_t f_tiles = (p.feats + kProductBM - 1) / kProductBM;
-  // the most tiles the launch can have (a ragged problem's count is known on the device only)
-  int64_t tiles;
-  if (mode == kProductDw) {
-    tiles = p.groups * f_tiles * ((p.cols + p.bn - 1) / p.bn);
-  } else {
-    const int64_t blocks = p.offsets == nullptr
-                               ? (p.rows + p.bn - 1) / p.bn
-                               : std::min<int64_t>(p.rows, p.rows / p.bn + p.groups);
-    tiles = blocks * f_tiles;
-  }
+  const int64_t tiles = product_tile_order(mode, kProductBM, &p);
   if (tiles <= 0) return cudaSuccess;
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
   p.stages = static_cast<int>(

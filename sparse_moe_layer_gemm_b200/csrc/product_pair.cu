@@ -131,10 +131,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   cluster_sync_all();  // both CTAs' barriers are ready before remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int f_tiles = (p.feats + kPairBM - 1) / kPairBM;
-  const int total = MODE == kProductDw
-                        ? p.groups * f_tiles * ((p.cols + p.bn - 1) / p.bn)
-                        : tab.block_start[p.groups] * f_tiles;
+  const int total = p.f_tiles * (MODE == kProductDw ? p.groups * p.dw_blocks
+                                                    : tab.block_start[p.groups]);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -219,9 +217,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
       const uint64_t bd0 = kBMn ? sdesc_mn_sw128(sa + kOperand) : sdesc_k_sw<128>(sa + kOperand);
       uint32_t s = 0, ph = 0, tc = 0;
       bool any = false, ok = true;
+      // the next tile is decoded below the current one's first MMAs
+      Tile next{};
+      if (pair < total) next = decode<MODE, kPairBM>(p, tab, pair);
       for (int w = pair; w < total && ok; w += n_pairs) {
-        const Tile t = decode<MODE, kPairBM>(p, tab, w);
+        const Tile t = next;
+        auto look_ahead = [&]() {
+          if (w + n_pairs < total) next = decode<MODE, kPairBM>(p, tab, w + n_pairs);
+        };
         const int nkb = (t.depth + 63) >> 6;
+        if (nkb == 0) look_ahead();
         if (nkb == 0) continue;  // an empty group's gradient: the epilogue takes zeros
         any = true;
         uint32_t idesc[HALVES], d[HALVES];
@@ -294,6 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
             if (!(ok = wait_slot(0))) break;
             issue(0, 0, left);
             release();
+            if (left == t.depth) look_ahead();
           }
           if (!ok) break;
           finish(0);
@@ -303,6 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
           const int lead = min(kLead, nkb);
           for (int k = 0; k < lead && ok; ++k)
             if ((ok = wait_slot(k))) issue(0, k, left - 64 * k);
+          look_ahead();
           if (ok && nkb <= kLead) finish(0);
           if (!ok || !(ok = acquire(1))) break;
           for (int k = 0; k < lead; ++k, left -= 64) {
@@ -452,16 +459,10 @@ cudaError_t product_pair_configure_device() {
   return e;
 }
 
-cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
+cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p0,
                                 int num_sms, cudaStream_t st) {
-  const int64_t f_tiles = (p.feats + kPairBM - 1) / kPairBM;
-  int64_t tiles;
-  if (mode == kProductDw)
-    tiles = p.groups * f_tiles * ((p.cols + p.bn - 1) / p.bn);
-  else if (p.offsets == nullptr)
-    tiles = f_tiles * ((p.rows + p.bn - 1) / p.bn);
-  else
-    tiles = f_tiles * std::min<int64_t>(p.rows, p.rows / p.bn + p.groups);
+  ProductParams p = p0;
+  const int64_t tiles = product_tile_order(mode, kPairBM, &p);
   if (tiles <= 0) return cudaSuccess;
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(std::min<int64_t>(2 * tiles, num_sms & ~1));

@@ -27,6 +27,16 @@ constexpr int kProductBM = 128;     // features per CTA tile
 constexpr int kProductMaxBN = 128;  // rows per one-CTA tile (a multiple of 16)
 constexpr int kProductMaxSplit = 8;
 
+// Division of 0 <= n < 2^31 by a divisor known on the host.
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return {static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1), s, d};
+}
+
 struct ProductParams {
   const int* offsets;  // [groups + 1] first row of each group; nullptr: one group of all rows
   int groups;          // >= 1
@@ -42,6 +52,11 @@ struct ProductParams {
   // 4096 x 4096 -> 11264 248 us against 258; dw gained nothing from it)
   bool wide_a;
   int split;           // CTAs of a cluster sharing one tile's contraction
+  // of the tile order, filled in at launch: feature tiles, row blocks per group
+  // (dw), and divisions by the tiles of a group (dw) or of a row block, and by
+  // those of an ordering chunk
+  int f_tiles, dw_blocks;
+  FastDiv by_group, by_chunk;
   void* out;
   int64_t ld_out;      // elements between output rows
   const void* bias;    // [groups, feats] or nullptr
@@ -54,6 +69,23 @@ struct ProductParams {
   bool vec_out, vec_residual, vec_preact;
   int* status;         // device status word
 };
+
+// Fills in the tile order for tiles of bm features; returns the most tiles the
+// launch can have (a ragged problem's count is known on the device only).
+inline int64_t product_tile_order(int mode, int bm, ProductParams* p) {
+  p->f_tiles = (p->feats + bm - 1) / bm;
+  p->dw_blocks = mode == kProductDw ? (p->cols + p->bn - 1) / p->bn : 0;
+  p->by_group = fast_div(static_cast<uint32_t>(p->f_tiles * (mode == kProductDw ? p->dw_blocks : 1)));
+  p->by_chunk = fast_div(static_cast<uint32_t>(p->f_tiles * p->chunk));
+  int64_t blocks;
+  if (mode == kProductDw)
+    blocks = static_cast<int64_t>(p->groups) * p->dw_blocks;
+  else if (p->offsets == nullptr)
+    blocks = (p->rows + p->bn - 1) / p->bn;
+  else
+    blocks = p->rows / p->bn + p->groups < p->rows ? p->rows / p->bn + p->groups : p->rows;
+  return blocks * p->f_tiles;
+}
 
 struct ProductMaps {
   CUtensorMap a, b;
