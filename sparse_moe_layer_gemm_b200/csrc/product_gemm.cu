@@ -77,8 +77,40 @@ __device__ __forceinline__ void my_slots(int depth, int rank, int split, int* kb
   *kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
 }
 
+// Rows j, j + 4, ... below j1 of a tile whose SPLIT partials lie at `mine` in
+// the cluster's CTAs: a lane adds 4 features of a row in rank order, with 16
+// of a thread's loads under way at once.
+template <int SPLIT, typename Store>
+__device__ __forceinline__ void join_rows(uint32_t mine, int j, int j1, Store store) {
+  constexpr int kRows = 16 / SPLIT;
+  uint32_t from[SPLIT];
+#pragma unroll
+  for (int k = 0; k < SPLIT; ++k) from[k] = mapa_shared(mine, k);
+  for (; j < j1; j += 4 * kRows) {
+    float4 got[kRows][SPLIT];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int k = 0; k < SPLIT; ++k)
+        if (j + 4 * i < j1) got[i][k] = ld_cluster_f32x4(from[k] + (j + 4 * i) * (kProductBM * 4));
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (j + 4 * i >= j1) break;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < SPLIT; ++k) {
+        v[0] += got[i][k].x;
+        v[1] += got[i][k].y;
+        v[2] += got[i][k].z;
+        v[3] += got[i][k].w;
+      }
+      store(j + 4 * i, v);
+    }
+  }
+}
+
 template <int MODE, typename T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const ProductParams p) {
   constexpr bool kAMn = MODE != kProductDx;
@@ -88,6 +120,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int stages = p.stages;
   const int sub_bytes = kABytes + b_bytes(MODE, p.bn);
+  // what a sub-slot's loads bring: of a problem with fewer rows than the tile
+  // only those (what lies behind them in shared memory reaches no kept result)
+  const int load_bytes = kABytes + (kBMn ? b_bytes(MODE, p.bn) : p.box_rows * 128);
   const int slot_bytes = kSubs * sub_bytes;
   uint8_t* epi = smem + stages * slot_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi + kEpiBytes);
@@ -161,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int subs = min(kSubs, kb1 - kb);
         if (elect_one()) {
           const uint32_t bar = full0 + 8 * s;
-          mbar_arrive_expect_tx(bar, subs * sub_bytes);
+          mbar_arrive_expect_tx(bar, subs * load_bytes);
           uint32_t sa = smem_u32(smem) + s * slot_bytes;
           int c = t.c0 + kb * 64;
           for (int i = 0; i < subs; ++i, sa += sub_bytes, c += 64) {
@@ -319,18 +354,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       // one tile per cluster in this form (the launch has a cluster per tile):
       // the partial goes where the slots were, [row][128 features]
       float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
-      for (int c = 0; c < t.n_valid; c += 16) {
-        uint32_t r[16];
-        if (empty) {
+      for (int c = 0; c < t.n_valid; c += 32) {
+        uint32_t r[2][16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = 0;
-        } else {
-          tmem_ld_x16(taddr + c, r);
+        for (int i = 0; i < 32; ++i) r[i >> 4][i & 15] = 0;
+        if (!empty) {
+          tmem_ld_x16(taddr + c, r[0]);
+          if (c + 16 < t.n_valid) tmem_ld_x16(taddr + c + 16, r[1]);
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < t.n_valid) part[(c + i) * kProductBM] = __uint_as_float(r[i]);
+        for (int i = 0; i < 32; ++i)
+          if (c + i < t.n_valid) part[(c + i) * kProductBM] = __uint_as_float(r[i >> 4][i & 15]);
       }
       __syncwarp();
       cluster_wait();
@@ -339,37 +374,18 @@ __global__ void __launch_bounds__(kThreads, 2)
       int go = 1;
       if (lane == 0) go = mbar_wait_cluster(xfull, 0, abort_flag, p.status) ? 1 : 0;
       if (!__shfl_sync(0xffffffffu, go, 0)) break;
-      // this CTA's rows, dealt to its warps; a lane joins 4 features of a row, with
-      // two rows' loads under way at once
       const int share = (t.n_valid + split - 1) / split;
       const int j0 = rank * share, j1 = min(j0 + share, t.n_valid);
       const uint32_t mine = smem_u32(smem) + lane * 16;
-      uint32_t from[kProductMaxSplit];
-#pragma unroll
-      for (int k = 0; k < kProductMaxSplit; ++k) from[k] = mapa_shared(mine, min(k, split - 1));
-      for (int j = j0 + warp - 2; j < j1; j += 8) {
-        const int n = j + 4 < j1 ? 2 : 1;
-        float4 got[2][kProductMaxSplit];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int k = 0; k < kProductMaxSplit; ++k)
-            if (i < n && k < split) got[i][k] = ld_cluster_f32x4(from[k] + (j + 4 * i) * (kProductBM * 4));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i >= n) break;
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < kProductMaxSplit; ++k)
-            if (k < split) {
-              v[0] += got[i][k].x;
-              v[1] += got[i][k].y;
-              v[2] += got[i][k].z;
-              v[3] += got[i][k].w;
-            }
-          finish_row4<MODE, T>(p, row0 + j + 4 * i, t.f0 + lane * 4, t.g, v);
-        }
-      }
+      auto store = [&](int j, float (&v)[4]) {
+        finish_row4<MODE, T>(p, row0 + j, t.f0 + lane * 4, t.g, v);
+      };
+      if (split == 2)
+        join_rows<2>(mine, j0 + warp - 2, j1, store);
+      else if (split == 4)
+        join_rows<4>(mine, j0 + warp - 2, j1, store);
+      else
+        join_rows<8>(mine, j0 + warp - 2, j1, store);
       break;
     }
   }

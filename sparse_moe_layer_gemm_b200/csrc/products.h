@@ -45,6 +45,7 @@ struct ProductParams {
   int cols;            // dw: J, the output's rows per group; else unused
   int depth;           // contraction length (forward K, dx N; dw: unused)
   int bn;              // rows per tile, a multiple of 16
+  int box_rows;        // rows of map b's box (forward, dx)
   int chunk;           // row blocks per ordering chunk
   int stages;          // pipeline slots
   // forward: the weights' map walks 64-element chunks in a dimension of its own,

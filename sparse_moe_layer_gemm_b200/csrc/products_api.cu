@@ -302,9 +302,9 @@ int pair_slot_ns(int bn) {
   return 490 + std::max(0, bn - 320) * 190 / 192;
 }
 constexpr int kPairTileNs = 500, kPairTwoTileNs = 4600;
-// Joining a split tile: 2 us and 45 ns per row (one token 4096 -> 1280: 15.1 us
-// unsplit, 11.6, 9.7, 9.0 in 2, 4, 8 parts; 128 tokens 21.2, 23.7, 17.2, 14.0).
-constexpr int kJoinNs = 2000, kJoinRowNs = 45;
+// Joining a split tile: 1.6 us and 30 ns per row (one token 4096 -> 1280: 15.0
+// us unsplit, 11.4, 8.8, 7.9 in 2, 4, 8 parts; 128 tokens 20.0, 18.3, 13.7, 12.1).
+constexpr int kJoinNs = 1600, kJoinRowNs = 30;
 
 Choice choose(const Shape& q, int num_sms) {
   Choice best{false, 0, 1, 1};
@@ -351,6 +351,10 @@ Choice choose(const Shape& q, int num_sms) {
 void filled(const int32_t* offsets, int64_t groups, int64_t rows, int64_t* n, int64_t* mean) {
   *n = offsets == nullptr ? 1 : std::min(groups, rows);
   *mean = (rows + *n - 1) / *n;
+}
+
+int box_rows(const Choice& ch, int rows) {
+  return ch.pair ? product_pair_box(ch.bn) : std::min(ch.bn, rows);
 }
 
 cudaError_t launch_any(const Choice& ch, int mode, bool bf16, const ProductMaps& m,
@@ -427,6 +431,7 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   const Choice ch = choose({N, n_groups, mean, (K + 63) / 64, n_groups > 1, false,
                             c->activation != MOE_ACT_NONE}, sms);
   p.bn = ch.bn;
+  p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
   p.split = ch.split;
   p.out = a->out;
@@ -444,7 +449,7 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   ProductMaps m;
   p.wide_a = N % 64 == 0;
   if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 64, p.wide_a) ||
-      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, ch.pair ? product_pair_box(p.bn) : p.bn, false))
+      !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, p.box_rows, false))
     return MOE_ERR_CUDA;
   MOE_CUDA(launch_any(ch, kProductForward, bf16, m, p, sms, st));
   return MOE_OK;
@@ -513,10 +518,11 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     const Choice ch =
         choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false}, sms);
     p.bn = ch.bn;
+  p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
     p.split = ch.split;
     if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, kProductBM, false) ||
-        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, ch.pair ? product_pair_box(p.bn) : p.bn,
+        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, p.box_rows,
                 false))
       return MOE_ERR_CUDA;
     MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
@@ -531,6 +537,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     const Choice ch =
         choose({N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), false, true, false}, sms);
     p.bn = ch.bn;
+  p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
     p.split = ch.split;
     if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 64, false) ||
