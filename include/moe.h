@@ -500,7 +500,7 @@ void moe_dense_destroy(moe_dense_t* layer);
  * overlap on the GPU. */
 typedef enum {
   MOE_ACT_NONE = 0,
-  MOE_ACT_RELU = 1,
+  MOE_ACT_RELU = 1,     /* slope 0 at 0 */
   MOE_ACT_SILU = 2,     /* z sigmoid(z) */
   MOE_ACT_GELU = 3,     /* z Phi(z), Phi the normal distribution function */
   MOE_ACT_GELU_TANH = 4 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */

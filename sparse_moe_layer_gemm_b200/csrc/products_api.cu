@@ -110,16 +110,32 @@ bool vec_rows(const void* p, int64_t ld, int64_t cols) {
   return aligned(p, 16) && ld % 8 == 0 && cols % 8 == 0;
 }
 
-// [first, last) bytes of a strided 2-byte tensor
-struct Range {
-  uintptr_t a, b;
+// A matrix in memory: rows of `cols` bytes, `ld` bytes apart.
+struct Block {
+  const void* p;
+  int64_t rows, cols, ld;
 };
-Range range(const void* p, int64_t rows, int64_t cols, int64_t ld, int el = 2) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  if (p == nullptr || rows <= 0) return {0, 0};
-  return {a, a + static_cast<uintptr_t>(((rows - 1) * ld + cols) * el)};
+Block block(const void* p, int64_t rows, int64_t cols, int64_t ld, int el = 2) {
+  return {p, rows, cols * el, ld * el};
 }
-bool overlap(Range x, Range y) { return x.a < y.b && y.a < x.b; }
+Block flat(const void* p, int64_t n, int el = 2) { return {p, 1, n * el, n * el}; }
+
+// Whether two matrices share bytes: their extents meet, and they are not
+// columns apart in rows of the same stride (slices of one tensor).
+bool overlap(const Block& x, const Block& y) {
+  if (x.p == nullptr || y.p == nullptr || x.rows <= 0 || y.rows <= 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  const uintptr_t a1 = a + static_cast<uintptr_t>((x.rows - 1) * x.ld + x.cols);
+  const uintptr_t b1 = b + static_cast<uintptr_t>((y.rows - 1) * y.ld + y.cols);
+  if (a >= b1 || b >= a1) return false;
+  // a single row lies in rows of any stride (it may cross two of them)
+  const int64_t ld = x.rows > 1 ? x.ld : y.ld;
+  if ((x.rows > 1 && y.rows > 1 && x.ld != y.ld) || x.cols > ld || y.cols > ld) return true;
+  // y starts d bytes into a row of x's
+  int64_t d = static_cast<int64_t>(b - a) % ld;
+  if (d < 0) d += ld;
+  return !(d >= x.cols && ld - d >= y.cols);
+}
 
 bool stride_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxStride; }
 
@@ -136,16 +152,17 @@ int check_config(const moe_linear_config_t* c) {
 }
 
 // W's own checks: strides, and the elements it spans
-int check_w(const moe_linear_config_t* c, const void* w, int64_t ld, int64_t gs, Range* r) {
+int check_w(const moe_linear_config_t* c, const void* w, int64_t ld, int64_t gs, Block* r) {
   if (w == nullptr || !aligned(w, 2) || !stride_ok(ld, c->out_features)) return MOE_ERR_INVALID_ARG;
   const int64_t K = c->in_features, G = c->groups;
-  int64_t span = (K - 1) * ld + c->out_features;
+  *r = block(w, K, c->out_features, ld);
   if (G > 1) {
-    if (gs < span) return MOE_ERR_INVALID_ARG;
+    if (gs < (K - 1) * ld + c->out_features) return MOE_ERR_INVALID_ARG;
     if (gs > (1LL << 38)) return MOE_ERR_UNSUPPORTED;
-    span += (G - 1) * gs;
+    // groups whole rows apart are more rows; else everything from first to last
+    *r = gs % ld == 0 ? block(w, (G - 1) * (gs / ld) + K, c->out_features, ld)
+                      : flat(w, (G - 1) * gs + (K - 1) * ld + c->out_features);
   }
-  *r = range(w, 1, span, span);
   return MOE_OK;
 }
 
@@ -155,7 +172,7 @@ int check_forward(const moe_linear_config_t* c, const moe_linear_args_t* a) {
   if (a == nullptr) return MOE_ERR_INVALID_ARG;
   if (c->rows == 0) return MOE_OK;
   const int64_t R = c->rows, K = c->in_features, N = c->out_features;
-  Range w;
+  Block w{};
   if (a->x == nullptr || a->out == nullptr || (c->groups > 0) != (a->offsets != nullptr) ||
       !stride_ok(a->ld_x, K) || !stride_ok(a->ld_out, N) ||
       (a->residual != nullptr && !stride_ok(a->ld_residual, N)) ||
@@ -165,12 +182,12 @@ int check_forward(const moe_linear_config_t* c, const moe_linear_args_t* a) {
       !aligned(a->residual, 2) || !aligned(a->preact, 2) || !aligned(a->offsets, 4))
     return MOE_ERR_INVALID_ARG;
   if ((r = check_w(c, a->w, a->ld_w, a->group_stride_w, &w)) != MOE_OK) return r;
-  const Range x = range(a->x, R, K, a->ld_x), out = range(a->out, R, N, a->ld_out);
-  const Range pre = range(a->preact, R, N, a->ld_preact);
-  const Range res = range(a->residual, R, N, a->ld_residual);
-  const Range bias = range(a->bias, 1, std::max(1, c->groups) * N, 0);
+  const Block x = block(a->x, R, K, a->ld_x), out = block(a->out, R, N, a->ld_out);
+  const Block pre = block(a->preact, R, N, a->ld_preact);
+  const Block res = block(a->residual, R, N, a->ld_residual);
+  const Block bias = flat(a->bias, std::max(1, c->groups) * N);
   const bool in_place = a->residual == a->out && a->ld_residual == a->ld_out;
-  for (const Range& o : {out, pre})
+  for (const Block& o : {out, pre})
     if (overlap(o, x) || overlap(o, w) || overlap(o, bias)) return MOE_ERR_INVALID_ARG;
   if (overlap(out, pre) || overlap(pre, res) || (overlap(out, res) && !in_place))
     return MOE_ERR_INVALID_ARG;
@@ -192,14 +209,14 @@ int check_backward(const moe_linear_config_t* c, const moe_linear_grads_t* a) {
       (a->dx != nullptr && !stride_ok(a->ld_dx, K)) ||
       (a->dw != nullptr && (a->x == nullptr || !aligned(a->x, 2) || !stride_ok(a->ld_x, K))))
     return MOE_ERR_INVALID_ARG;
-  Range w{0, 0};
+  Block w{};
   if (a->dx != nullptr && (r = check_w(c, a->w, a->ld_w, a->group_stride_w, &w)) != MOE_OK) return r;
-  const Range in[4] = {range(a->dout, R, N, a->ld_dout), w, range(a->preact, R, N, a->ld_preact),
-                       a->dw != nullptr ? range(a->x, R, K, a->ld_x) : Range{0, 0}};
-  const Range out[3] = {range(a->dx, R, K, a->ld_dx), range(a->dw, 1, G * K * N, 0),
-                        range(a->dbias, 1, G * N, 0)};
+  const Block in[4] = {block(a->dout, R, N, a->ld_dout), w, block(a->preact, R, N, a->ld_preact),
+                       block(a->dw != nullptr ? a->x : nullptr, R, K, a->ld_x)};
+  const Block out[3] = {block(a->dx, R, K, a->ld_dx), flat(a->dw, G * K * N),
+                        flat(a->dbias, G * N)};
   for (int i = 0; i < 3; ++i) {
-    for (const Range& v : in)
+    for (const Block& v : in)
       if (overlap(out[i], v)) return MOE_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (overlap(out[i], out[j])) return MOE_ERR_INVALID_ARG;
@@ -577,17 +594,8 @@ int check_swiglu(const moe_swiglu_config_t* c) {
 
 // an output may be one of the inputs (the same rows, read before written by
 // the thread that writes them) or apart from it
-bool apart_or_same(const void* o, int64_t ld_o, const void* i, int64_t ld_i, int64_t rows,
-                   int64_t cols, int el) {
-  if (o == i && ld_o == ld_i) return true;
-  // interleaved halves of one tensor: the same stride, columns apart
-  if (ld_o == ld_i) {
-    const intptr_t row = static_cast<intptr_t>(ld_o) * el;
-    intptr_t d = (reinterpret_cast<intptr_t>(i) - reinterpret_cast<intptr_t>(o)) % row;
-    if (d < 0) d += row;
-    if (d >= cols * el && row - d >= cols * el) return true;
-  }
-  return !overlap(range(o, rows, cols, ld_o, el), range(i, rows, cols, ld_i, el));
+bool apart_or_same(const Block& o, const Block& i) {
+  return (o.p == i.p && o.ld == i.ld) || !overlap(o, i);
 }
 
 }  // namespace
@@ -606,9 +614,9 @@ int moe_swiglu(const moe_swiglu_config_t* c, const void* gate, int64_t ld_gate, 
       !aligned(up, el) || !aligned(out, el) || !aligned(scale, 4) || !aligned(offsets, 4) ||
       !stride_ok(ld_gate, W) || !stride_ok(ld_up, W) || !stride_ok(ld_out, W) ||
       (c->groups > 0) != (offsets != nullptr) ||
-      !apart_or_same(out, ld_out, gate, ld_gate, R, W, el) ||
-      !apart_or_same(out, ld_out, up, ld_up, R, W, el) ||
-      overlap(range(out, R, W, ld_out, el), range(scale, 1, R, 0, 4)))
+      !apart_or_same(block(out, R, W, ld_out, el), block(gate, R, W, ld_gate, el)) ||
+      !apart_or_same(block(out, R, W, ld_out, el), block(up, R, W, ld_up, el)) ||
+      overlap(block(out, R, W, ld_out, el), flat(scale, R, 4)))
     return MOE_ERR_INVALID_ARG;
   SwigluParams p{};
   p.gate = gate;
@@ -642,23 +650,18 @@ int moe_swiglu_backward(const moe_swiglu_config_t* c, const void* dout, int64_t 
       !stride_ok(ld_dout, W) || !stride_ok(ld_gate, W) || !stride_ok(ld_up, W) ||
       !stride_ok(ld_dgate, W) || !stride_ok(ld_dup, W) || (c->groups > 0) != (offsets != nullptr))
     return MOE_ERR_INVALID_ARG;
-  struct {
-    const void* p;
-    int64_t ld;
-  } in[3] = {{dout, ld_dout}, {gate, ld_gate}, {up, ld_up}}, outs[2] = {{dgate, ld_dgate}, {dup, ld_dup}};
-  for (const auto& o : outs) {
-    for (const auto& i : in)
-      if (!apart_or_same(o.p, o.ld, i.p, i.ld, R, W, el)) return MOE_ERR_INVALID_ARG;
-    if (overlap(range(o.p, R, W, o.ld, el), range(scale, 1, R, 0, 4)) ||
-        overlap(range(o.p, R, W, o.ld, el), range(dscale, 1, R, 0, 4)))
-      return MOE_ERR_INVALID_ARG;
+  const Block in[3] = {block(dout, R, W, ld_dout, el), block(gate, R, W, ld_gate, el),
+                       block(up, R, W, ld_up, el)};
+  const Block outs[2] = {block(dgate, R, W, ld_dgate, el), block(dup, R, W, ld_dup, el)};
+  const Block sc = flat(scale, R, 4), ds = flat(dscale, R, 4);
+  for (const Block& o : outs) {
+    for (const Block& i : in)
+      if (!apart_or_same(o, i)) return MOE_ERR_INVALID_ARG;
+    if (overlap(o, sc) || overlap(o, ds)) return MOE_ERR_INVALID_ARG;
   }
-  if (dgate == dup || !apart_or_same(dgate, ld_dgate, dup, ld_dup, R, W, el))
-    return MOE_ERR_INVALID_ARG;
-  for (const auto& i : in)
-    if (overlap(range(i.p, R, W, i.ld, el), range(dscale, 1, R, 0, 4))) return MOE_ERR_INVALID_ARG;
-  if (dscale != nullptr && overlap(range(dscale, 1, R, 0, 4), range(scale, 1, R, 0, 4)))
-    return MOE_ERR_INVALID_ARG;
+  for (const Block& i : in)
+    if (overlap(i, ds)) return MOE_ERR_INVALID_ARG;
+  if (overlap(outs[0], outs[1]) || overlap(ds, sc)) return MOE_ERR_INVALID_ARG;
   SwigluParams p{};
   p.gate = gate;
   p.ld_gate = ld_gate;

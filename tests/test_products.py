@@ -30,7 +30,7 @@ def half_step(dtype):
 
 def act64(z, name):
     if name == "relu":
-        return z.clamp(min=0)
+        return torch.relu(z)  # slope 0 at 0 (clamp's is 1)
     if name == "silu":
         return z * torch.sigmoid(z)
     if name == "gelu":
@@ -195,6 +195,45 @@ def test_linear_backward_parts(act):
         part = B.linear_backward(dout, x if i == 1 else None, w, preact=pre, activation=act, **need)
         assert [p is None for p in part] == [j != i for j in range(3)]
         assert torch.equal(part[i], whole[i])
+
+
+@gpu
+def test_slopes_at_zero_and_far_out():
+    """relu's slope at 0 is 0; far from 0 every slope is 0 or 1, without NaN."""
+    z = torch.tensor([[0.0, -0.0, 300.0, -300.0, 6e4, -6e4, 1e30, -1e30]],
+                     dtype=torch.bfloat16, device="cuda")
+    one, eye = torch.ones_like(z), torch.eye(8, dtype=z.dtype, device="cuda")
+    for act, at0 in (("relu", 0.0), ("silu", 0.5), ("gelu", 0.5), ("gelu_tanh", 0.5)):
+        dx, _, db = B.linear_backward(one, None, eye, preact=z, activation=act, need_dw=False)
+        want = [at0, at0, 1.0, 0.0, 1.0, 0.0, 1.0, 0.0]
+        assert dx[0].tolist() == want and db.tolist() == want, act
+        x = torch.zeros(1, 8, dtype=z.dtype, device="cuda")
+        out = B.linear(x, eye, z[0].contiguous(), activation=act)
+        keep = torch.where(z > 0, z, torch.zeros_like(z))
+        assert torch.equal(out, keep), act
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """Row strides that take the last rows more than 2^32 elements away."""
+    gen = torch.Generator().manual_seed(9)
+    rows, K, N, ld = 2100, 64, 72, (1 << 21) + 64
+    big = torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda")  # 8.8 GB
+    x, res, dout = big[:, :K], big[:, 128:128 + N], big[:, 256:256 + N]
+    out, dx = big[:, 512:512 + N], big[:, 1024:1024 + K]
+    x.copy_(normal(gen, torch.bfloat16, rows, K))
+    res.copy_(normal(gen, torch.bfloat16, rows, N))
+    dout.copy_(normal(gen, torch.bfloat16, rows, N))
+    w = normal(gen, torch.bfloat16, K, N, std=0.1)
+    for lo, hi in ((0, rows), (rows - 3, rows)):  # CTA pairs or not, split or not
+        B.linear(x[lo:hi], w, residual=res[lo:hi], activation="silu", out=out[lo:hi])
+        check_rows(out[lo:hi], x[lo:hi], w, None, res[lo:hi], "silu")
+        _, dw, db = B.linear_backward(dout[lo:hi], x[lo:hi], w, preact=res[lo:hi],
+                                      activation="silu", dx=dx[lo:hi])
+        check_grads(dx[lo:hi], dw, db, dout[lo:hi], x[lo:hi], w, res[lo:hi], "silu")
+    h = big[:, 2048:2048 + N]
+    B.swiglu(res, dout, out=h)
+    assert torch.equal(h, B.swiglu(res.contiguous(), dout.contiguous()))
 
 
 @gpu
@@ -735,6 +774,7 @@ def _args(**kw):
     ({}, dict(ld_w=71)), ({}, dict(ld_out=71)), ({}, dict(x=X + 1)), ({}, dict(offsets=OFF)),
     ({}, dict(out=X)), ({}, dict(out=W + 16)), ({}, dict(ld_out=1 << 32)),
     ({}, dict(residual=RES, ld_residual=10)), ({}, dict(preact=PRE, ld_preact=10)),
+    ({}, dict(out=X + 100, ld_x=256, ld_out=256)), ({}, dict(out=X + 256, ld_out=80)),
     ({}, dict(preact=OUT, ld_preact=72)), ({}, dict(residual=OUT + 16, ld_residual=72)),
     (dict(groups=2), dict()), (dict(groups=2), dict(offsets=OFF, group_stride_w=100)),
     (dict(groups=2), dict(offsets=OFF + 2, group_stride_w=64 * 72)),
@@ -745,6 +785,24 @@ def test_linear_refuses(lib, cfg, kw):
     assert lib.moe_linear_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)) == \
         B.MOE_ERR_INVALID_ARG
     assert lib.moe_linear(ctypes.byref(c), ctypes.byref(a), None, 0, None) == B.MOE_ERR_INVALID_ARG
+
+
+def test_slices_of_one_tensor_are_apart(lib):
+    """Columns of the same rows do not overlap, whatever their extents."""
+    import ctypes
+    n = ctypes.c_size_t()
+    for kw in (dict(ld_x=256, out=X + 2 * 128, ld_out=256),          # x | out in rows of 256
+               dict(x=X + 2 * 160, ld_x=256, out=X + 2 * 16, ld_out=256),
+               dict(w=X + 2 * 64, ld_w=256, ld_x=256, out=X + 2 * 176, ld_out=256,
+                    residual=X + 2 * 256 * 64, ld_residual=256)):
+        c, a = _cfg(), _args(**kw)
+        assert lib.moe_linear_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)) \
+            == B.MOE_OK, kw
+    c = _cfg(rows=1)
+    for at, want in ((128, B.MOE_OK), (126, B.MOE_ERR_INVALID_ARG)):  # one row of 64, then out
+        a = _args(out=X + at)
+        assert lib.moe_linear_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)) \
+            == want
 
 
 def test_linear_workspace(lib):
