@@ -41,8 +41,7 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 // exp(x^2) erfc(x) / t over 0 <= x <= 10 by reweighted least squares (relative
 // error 3.0e-7; evaluated in fp32 1.7e-6 for |z| < 6, from the exponent's
 // rounding).  The tail keeps its relative accuracy, where 1 + erf cancels.
-// (erfcf in its place: 4096 x 4096 -> 11264 377 us against 291 without an
-// activation.)  gelu_tanh is 0.5 (1 + tanh u) = sigmoid(2 u), for the same
+// (4096 x 4096 -> 11264: 12 us over no activation; erfcf in its place 87 us.)  gelu_tanh is 0.5 (1 + tanh u) = sigmoid(2 u), for the same
 // reason.
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 0.79788456080286536f;  // sqrt(2 / pi)
@@ -134,20 +133,25 @@ __device__ __forceinline__ float activation_slope(float z, int act) {
 struct GroupTable {
   int* block_start;  // [groups + 1]
   int* row0;         // [groups + 1]
+  int* block_rows;   // [groups]
   __device__ __forceinline__ int count(int g) const { return row0[g + 1] - row0[g]; }
 };
 
-constexpr int group_table_bytes(int groups) { return 2 * (groups + 1) * 4; }
+constexpr int group_table_bytes(int groups) { return 3 * (groups + 1) * 4; }
+
+__host__ __device__ constexpr int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
 __device__ __forceinline__ GroupTable build_group_table(int* mem, const int* offsets, int groups,
                                                         int rows, int unit) {
-  GroupTable t{mem, mem + groups + 1};
+  GroupTable t{mem, mem + groups + 1, mem + 2 * (groups + 1)};
   if (offsets == nullptr) {
     if (threadIdx.x == 0) {
       t.row0[0] = 0;
       t.row0[1] = rows;
+      const int blocks = (rows + unit - 1) / unit;
       t.block_start[0] = 0;
-      t.block_start[1] = (rows + unit - 1) / unit;
+      t.block_start[1] = blocks;
+      t.block_rows[0] = min(unit, round_up((rows + blocks - 1) / max(blocks, 1), 16));
     }
     __syncthreads();
     return t;
@@ -184,6 +188,11 @@ __device__ __forceinline__ GroupTable build_group_table(int* mem, const int* off
     }
   }
   __syncthreads();
+  for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+    const int blocks = max(t.block_start[g + 1] - t.block_start[g], 1);
+    t.block_rows[g] = min(unit, round_up((t.count(g) + blocks - 1) / blocks, 16));
+  }
+  __syncthreads();
   return t;
 }
 
@@ -203,8 +212,8 @@ __device__ __forceinline__ int group_of_block(const GroupTable& t, int groups, i
 
 // One lane of the (converged) warp, the same at every call.  The tcgen05 and
 // TMA instructions take warp-uniform registers: issued inside a loop that the
-// whole warp walks, under this predicate, their operands stay there; a loop
-// walked by one lane alone cost ~590 cycles per slot on top of its MMAs.
+// whole warp walks, under this predicate, their operands stay there (a loop
+// walked by one lane alone cost half as much again: see product_gemm.cu).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -325,13 +334,14 @@ __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable&
   const int nb = first + (rem - ft * in_chunk);
   r.f0 = ft * BM;
   if (MODE == kProductDw) {
-    r.j0 = nb * p.bn;
-    r.n_valid = min(p.bn, p.cols - r.j0);
+    r.j0 = nb * p.dw_rows;
+    r.n_valid = min(p.dw_rows, p.cols - r.j0);
     r.c0 = t.row0[r.g];
     r.depth = t.count(r.g);
   } else {
-    r.j0 = t.row0[r.g] + nb * p.bn;
-    r.n_valid = min(p.bn, t.count(r.g) - nb * p.bn);
+    const int size = t.block_rows[r.g];
+    r.j0 = t.row0[r.g] + nb * size;
+    r.n_valid = min(size, t.count(r.g) - nb * size);
     r.c0 = 0;
     r.depth = p.depth;
   }
@@ -347,8 +357,8 @@ __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable&
 // + 1), so after packing two rows into 32 bits one transposing stmatrix per 8
 // rows lays [row][32 features] into shared memory, from where 16-byte pieces
 // go out, 64 contiguous bytes per row.  The residual comes in the same way
-// backwards.  Measured against one 2-byte store per value: a 4096 x 4096
-// output went from 95 to 16 us at a contraction of 64.
+// backwards.  Against one 2-byte store per value, 4096 rows 64 -> 4096 went
+// from 95 to 20 us (33.5 MB written).
 constexpr int kEpiPitch = 80;                  // bytes per staged row: 64 + 16 against bank conflicts
 constexpr int kEpiChunk = 16 * kEpiPitch;      // one staged chunk
 constexpr int kEpiWarpBytes = 2 * kEpiChunk;   // 32 rows, or 16 and the residual's 16

@@ -21,10 +21,11 @@
 // issue, warps 2-5 epilogue (one accumulator lane quadrant each).  Persistent
 // over tiles w = cluster, cluster + clusters, ...; the accumulator is
 // double-buffered.  A slot holds two sub-slots of 64 steps: with few rows the
-// weights stream no faster than the issuing warps turn slots over (16-row
-// tile, 64 x 64 steps: 35.6 us with one-lane loops, 22.5 with whole-warp loops
-// and elect, and two sub-slots per turn on top).  Every wait is bounded
-// (moe_ptx.cuh).
+// weights stream no faster than the issuing warps turn slots over (one tile of
+// 16 rows, 4096 steps: 30.4 us with one-lane loops, 22.5 with whole-warp loops
+// and elect, 15.0 with two sub-slots per turn).  With enough tiles HBM is the
+// bound: 512 rows over 288 groups, 4096 -> 1280, read their weights at 6.6 TB/s.
+// Every wait is bounded (moe_ptx.cuh).
 //
 // Weight gradient: the contraction runs over the group's rows, which end
 // inside a slot; the rows behind the last one belong to the next group.  The

@@ -6,17 +6,17 @@
 // of the tile and half of its rows, and holds its features x all rows of the
 // accumulator.
 //
-// Why two accumulators per tile (HALVES = 2, rows 0-255 and 256-511): MMAs
-// into one accumulator follow one another every ~165 cycles whatever their N
-// (4096^3: 25.6 us per wave of tiles at N = 128 and at N = 256), above the 128
-// cycles of work of an N = 256 instruction; alternating between two
-// accumulators hides that latency.  A tile of twice the rows also loads a
-// quarter less per flop, which matters at the 64 bytes per cycle that an SM
-// draws from L2.  The two accumulators fill tensor memory, so the epilogue
-// overlaps the next tile by skewing them: a tile's first kLead slots go to
-// the first accumulator before the second (which still drains), its last
-// kLead slots too (the first drains while the second finishes).
-// HALVES = 1 keeps 256-row tiles for problems of few tiles.
+// HALVES = 1: tiles of up to 256 rows, the accumulator double-buffered, so the
+// epilogue runs below the next tile's mainloop.  At 256 rows an SM's share of a
+// slot is 32 KB to load and 512 cycles of MMAs: what it draws from L2, 64 bytes
+// per cycle, and the tensor cores bound it alike (4096^3: 94 to 98 us, 23 us
+// per wave of tiles; the library's product 91 to 93).
+// HALVES = 2: tiles of up to 512 rows in two even accumulators that share the
+// features' loads, a quarter less per flop.  They fill tensor memory, so the
+// epilogue overlaps the next tile only by skewing them: a tile's first kLead
+// slots go to the first accumulator before the second (which still drains),
+// its last kLead slots too (the first drains while the second finishes).
+// Worth it where it saves a wave of tiles (the choice is in products_api.cu).
 //
 // Roles per CTA (10 warps): warp 0 TMA producer (own halves; every load
 // completes on the leader's full barrier), warp 1 tensor memory and (leader)
@@ -79,9 +79,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   constexpr int kSlot = PairShape<HALVES>::kSlot;
   constexpr int kStages = PairShape<HALVES>::kStages;
   constexpr int kBarBytes = PairShape<HALVES>::kBarBytes;
-  // rows per accumulator, and this CTA's bytes of one half's rows in a slot
-  const int hn = HALVES == 1 ? p.bn : kAccCols;
-  const uint32_t half_bytes = kBMn ? (hn / 2 + 63) / 64 * kSubBytes : hn / 2 * 128;
+  // an accumulator's rows are rounded up to kUnit for the MMA, so that each CTA
+  // supplies a multiple of 8 (MN-major: of 16; a half of 8 rows more is slow to
+  // read, 58 us against 45 for 4096 x 1280 gradients)
+  constexpr int kUnit = kBMn ? 32 : 16;
+  // most rows per accumulator, and this CTA's bytes of one half's rows in a slot
+  const int hn_max = product_pair_half(p.bn, kUnit);
+  const uint32_t half_bytes = kBMn ? (hn_max / 2 + 63) / 64 * kSubBytes : hn_max / 2 * 128;
+  // rows per accumulator of a tile: all in one if they fit, else two even halves
+  auto half_rows = [&](int n_valid) {
+    return HALVES == 1 || n_valid <= hn_max ? n_valid : round_up((n_valid + 1) / 2, kUnit);
+  };
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -145,11 +153,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
       const int f = t.f0 + static_cast<int>(rank) * kProductBM;
       // this CTA's first row in each half's MMA
       int j[HALVES], halves = 0;
+      const int hn = half_rows(t.n_valid);
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
         const int n = min(hn, t.n_valid - h * hn);
         if (n > 0) ++halves;
-        j[h] = t.j0 + h * hn + static_cast<int>(rank) * (((n + 15) & ~15) >> 1);
+        j[h] = t.j0 + h * hn + static_cast<int>(rank) * (round_up(n, kUnit) / 2);
       }
       const uint32_t box_bytes = kOperand + halves * half_bytes;
       for (int left = t.depth, c = t.c0; left > 0; left -= 64, c += 64) {
@@ -183,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
             if (h >= halves) break;
             if (kBMn) {
               tma_load_2d_pair(sb + h * kOperand, &tmB, bar, j[h], c, pol);
-              if (hn > 128)
+              if (hn_max > 128)
                 tma_load_2d_pair(sb + h * kOperand + kSubBytes, &tmB, bar, j[h] + 64, c, pol);
             } else {
               tma_load_2d_pair(sb + h * kOperand, &tmB, bar, c, j[h], pol);
@@ -231,11 +240,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
         any = true;
         uint32_t idesc[HALVES], d[HALVES];
         int halves = 0;
+        const int hn = half_rows(t.n_valid);
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
           const int n = min(hn, t.n_valid - h * hn);
           if (n > 0) ++halves;
-          idesc[h] = product_idesc(is_bf16<T>(), kAMn, kBMn, kPairBM, (n + 15) & ~15);
+          idesc[h] = product_idesc(is_bf16<T>(), kAMn, kBMn, kPairBM, round_up(n, kUnit));
           d[h] = tmem_base + ((tc + h) & 1u) * kAccCols;
         }
         // half h's accumulator is drained
@@ -384,6 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
                                ? static_cast<int64_t>(t.g) * p.cols + t.j0
                                : static_cast<int64_t>(t.j0);
       bool ok = true;
+      const int hn = half_rows(t.n_valid);
       for (int h = 0; h * hn < t.n_valid; ++h) {
         const uint32_t buf = tc & 1u;
         if (!empty) {

@@ -54,9 +54,9 @@ struct ProductParams {
   bool wide_a;
   int split;           // CTAs of a cluster sharing one tile's contraction
   // of the tile order, filled in at launch: feature tiles, row blocks per group
-  // (dw), and divisions by the tiles of a group (dw) or of a row block, and by
+  // and their rows (dw: even parts rounded up to 32), and divisions by the tiles of a group (dw) or of a row block, and by
   // those of an ordering chunk
-  int f_tiles, dw_blocks;
+  int f_tiles, dw_blocks, dw_rows;
   FastDiv by_group, by_chunk;
   void* out;
   int64_t ld_out;      // elements between output rows
@@ -76,6 +76,10 @@ struct ProductParams {
 inline int64_t product_tile_order(int mode, int bm, ProductParams* p) {
   p->f_tiles = (p->feats + bm - 1) / bm;
   p->dw_blocks = mode == kProductDw ? (p->cols + p->bn - 1) / p->bn : 0;
+  if (mode == kProductDw) {
+    const int even = ((p->cols + p->dw_blocks - 1) / p->dw_blocks + 31) / 32 * 32;
+    p->dw_rows = even < p->bn ? even : p->bn;
+  }
   p->by_group = fast_div(static_cast<uint32_t>(p->f_tiles * (mode == kProductDw ? p->dw_blocks : 1)));
   p->by_chunk = fast_div(static_cast<uint32_t>(p->f_tiles * p->chunk));
   int64_t blocks;
@@ -96,10 +100,12 @@ cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const Prod
                            int num_sms, cudaStream_t st);
 
 // The same on CTA pairs (product_pair.cu): tiles of 256 features x bn rows, up
-// to 256 with one accumulator per tile, up to 512 with two; map b's box has
-// product_pair_box(bn) rows (dw: 64 steps, as for one CTA).
+// to 256 with one accumulator per tile, up to 512 with two of half the rows;
+// map b's box has half of an accumulator's rows (dw: 64 steps, as for one CTA).
 constexpr int kProductPairMaxBN = 512;
-constexpr int product_pair_box(int bn) { return bn <= 256 ? bn / 2 : 128; }
+constexpr int product_pair_half(int bn, int unit) {
+  return bn <= 256 ? bn : (bn / 2 + unit - 1) / unit * unit;
+}
 cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                                 int num_sms, cudaStream_t st);
 

@@ -308,15 +308,15 @@ int64_t row_blocks(const Shape& q, int64_t bn) {
 // One CTA, 128 features x bn rows: 4096 -> 1280 (64 slots) takes 15.1, 15.6,
 // 17.0, 21.2 us at bn = 16, 32, 64, 128; 1280 -> 4096 (20 slots) 7.8 to 11.2.
 // A CTA pair, 256 features: with one accumulator 23 us per wave of 64 slots at
-// 256 rows, 21 at 224 and 19.8 at 208 and below; with two 43 us at 512 rows,
-// 31 at 320, and 4.6 us more per tile, since its epilogue overlaps the next
-// tile less (1280 -> 4096 at 4096 rows: 33 us with one, 42 with two; 4096 ->
-// 1280, where two accumulators make one wave of what else is two: 37 and 45 us
-// for dw, 36 and 38.5 for dx).
+// 256 rows, 21 at 224, 20 at 208 and below; with two of half the rows 43 us at
+// 512 rows, 28 at 320, and 4.6 us more per tile, since its epilogue overlaps
+// the next tile less (1280 -> 4096 at 4096 rows: 33 us with one, 42 with two;
+// 4096 -> 1280, where two accumulators make one wave of what else is two: 36 us
+// and 40 forward, 33 and 39 for dx, 35 and 44 for dw).
 int one_cta_slot_ns(int bn) { return bn <= 16 ? 166 : bn <= 32 ? 173 : bn <= 64 ? 195 : 260; }
 int pair_slot_ns(int bn) {
   if (bn <= 256) return bn >= 240 ? 360 : bn >= 224 ? 330 : 310;
-  return 490 + std::max(0, bn - 320) * 190 / 192;
+  return 440 + std::max(0, bn - 320) * 240 / 192;
 }
 constexpr int kPairTileNs = 500, kPairTwoTileNs = 4600;
 // Joining a split tile: 1.6 us and 30 ns per row (one token 4096 -> 1280: 15.0
@@ -346,9 +346,9 @@ Choice choose(const Shape& q, int num_sms) {
     }
   }
   const int64_t f2 = (q.feats + 2 * kProductBM - 1) / (2 * kProductBM);
-  // (dw reads both operands MN-major, where halves that are no multiple of 16
-  // rows are slow: 58 us at 208 rows, 45 at 192.  An activation costs a second
-  // accumulator's poorer overlap more: gelu 4096 -> 11264 361 us, 291 without.)
+  // (dw's rows per tile are multiples of 32, see product_pair.cu.  An activation
+  // costs two accumulators' poorer overlap more: gelu 4096 -> 11264 272 us with
+  // two, 254 with one; 251 and 242 without.)
   const int step = q.dw ? 32 : 16;
   for (int bn = q.act ? 256 : kProductPairMaxBN; bn >= 128 && q.mean > 64; bn -= step) {
     const int64_t tiles = f2 * row_blocks(q, bn);
@@ -371,7 +371,7 @@ void filled(const int32_t* offsets, int64_t groups, int64_t rows, int64_t* n, in
 }
 
 int box_rows(const Choice& ch, int rows) {
-  return ch.pair ? product_pair_box(ch.bn) : std::min(ch.bn, rows);
+  return ch.pair ? product_pair_half(ch.bn, 16) / 2 : std::min(ch.bn, rows);
 }
 
 cudaError_t launch_any(const Choice& ch, int mode, bool bf16, const ProductMaps& m,
