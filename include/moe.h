@@ -495,9 +495,13 @@ void moe_dense_destroy(moe_dense_t* layer);
  * groups.  bias, dW and dbias are contiguous.  16-byte aligned pointers and
  * row strides that are multiples of 8 elements are read in place; other x, W
  * and dout are first copied into the workspace (one more pass over them).
- * out, preact and dx must not overlap x, W or dout; residual may be out
- * itself (out += ...).  The workspace must not be shared by calls that may
- * overlap on the GPU. */
+ * out, preact and dx must not overlap x, W or dout (columns of the same rows,
+ * slices of one tensor, do not); residual may be out itself (out += ...).  The
+ * workspace must not be shared by calls that may overlap on the GPU.
+ *
+ * Calls need no handle.  A host thread's first call on a device looks up the
+ * library's status word and sets the kernels' attributes there; make it before
+ * any stream capture.  Later calls only enqueue work and may be captured. */
 typedef enum {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,     /* slope 0 at 0 */
