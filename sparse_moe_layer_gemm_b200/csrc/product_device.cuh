@@ -12,6 +12,15 @@
 namespace moe {
 namespace product {
 
+// Launch order of the kernels of one call (see LaunchOrder in products.h).
+__device__ __forceinline__ void begin_ordered(LaunchOrder o) {
+  if (!o.late_wait) pdl_wait();
+  if (o.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void end_ordered(LaunchOrder o) {
+  if (o.late_wait) pdl_wait();
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T v);
 template <>

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), tmem_cols);
     tmem_relinquish();
   }
-  pdl_wait();
+  begin_ordered(p.order);
   const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, p.bn);
   tc_fence_before();
   __syncthreads();
@@ -399,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, tmem_cols);
   }
+  end_ordered(p.order);
 }
 
 template <int MODE, typename T>

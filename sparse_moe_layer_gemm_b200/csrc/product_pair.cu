@@ -132,7 +132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
     tmem_alloc_pair(smem_u32(tmem_slot), 2 * kAccCols);
     tmem_relinquish_pair();
   }
-  pdl_wait();
+  begin_ordered(p.order);
   const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, p.bn);
   tc_fence_before();
   __syncthreads();
@@ -428,6 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * kAccCols);
   }
+  end_ordered(p.order);
 }
 
 template <int MODE, int HALVES, typename T>

@@ -17,7 +17,7 @@ constexpr int kPackThreads = 256;
 
 // One warp per row of any of the operands.
 __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParams p) {
-  pdl_wait();
+  begin_ordered(p.order);
   int64_t row = static_cast<int64_t>(blockIdx.x) * (kPackThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   int i = 0;
@@ -25,7 +25,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParam
     row -= p.op[i].groups * p.op[i].rows;
     ++i;
   }
-  if (i == 3) return;
+  if (i == 3) {
+    end_ordered(p.order);
+    return;
+  }
   const PackOperand& o = p.op[i];
   const int64_t g = row / o.rows;
   const uint16_t* s = static_cast<const uint16_t*>(o.src) + g * o.group_stride + (row - g * o.rows) * o.ld;
@@ -40,6 +43,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParam
     for (int k = 0; k < U; ++k)
       if (c + k * 32 < o.cols) d[c + k * 32] = v[k];
   }
+  end_ordered(p.order);
 }
 
 constexpr int kGradThreads = 256;          // 8 warps: rows of a chunk are dealt to them
@@ -66,7 +70,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
   constexpr int kCols = 32 * E;
   extern __shared__ int tab_mem[];
   __shared__ float sums[kGradWarps][kCols];
-  pdl_wait();
+  begin_ordered(p.order);
   const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, kRowChunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col_blocks = (p.cols + kCols - 1) / kCols;
@@ -141,6 +145,7 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
       __syncthreads();
     }
   }
+  end_ordered(p.order);
 }
 
 // db[g][c] for 32 columns per CTA: warp k adds chunks k, k + 8, ..., then the
@@ -149,7 +154,7 @@ template <typename T>
 __global__ void __launch_bounds__(kGradThreads) bias_grad_kernel(const RowGradParams p) {
   extern __shared__ int tab_mem[];
   __shared__ float sums[kGradWarps][32];
-  pdl_wait();
+  begin_ordered(p.order);
   const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, kRowChunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col_blocks = (p.cols + 31) / 32;
@@ -173,6 +178,7 @@ __global__ void __launch_bounds__(kGradThreads) bias_grad_kernel(const RowGradPa
     }
     __syncthreads();
   }
+  end_ordered(p.order);
 }
 
 bool rows_aligned(const void* p, int64_t ld) {
@@ -189,15 +195,15 @@ cudaError_t row_grad(const RowGradParams& p, int num_sms, cudaStream_t st) {
                                                       : row_grad_chunks(p.rows, p.groups) + 1) *
                         ((p.cols + (vec ? 32 * kVec : 64) - 1) / (vec ? 32 * kVec : 64));
   const int grid = static_cast<int>(std::min<int64_t>(items, 8 * num_sms));
-  cudaError_t e;
-  if (vec)
-    e = launch_pdl(row_grad_kernel<T, true>, dim3(grid), dim3(kGradThreads), tab, st, p);
-  else
-    e = launch_pdl(row_grad_kernel<T, false>, dim3(grid), dim3(kGradThreads), tab, st, p);
-  if (e != cudaSuccess || p.db == nullptr || p.direct) return e;
+  return vec ? launch_pdl(row_grad_kernel<T, true>, dim3(grid), dim3(kGradThreads), tab, st, p)
+             : launch_pdl(row_grad_kernel<T, false>, dim3(grid), dim3(kGradThreads), tab, st, p);
+}
+
+template <typename T>
+cudaError_t bias_grad(const RowGradParams& p, int num_sms, cudaStream_t st) {
   const int64_t outs = static_cast<int64_t>(p.groups) * ((p.cols + 31) / 32);
   return launch_pdl(bias_grad_kernel<T>, dim3(static_cast<int>(std::min<int64_t>(outs, 4 * num_sms))),
-                    dim3(kGradThreads), tab, st, p);
+                    dim3(kGradThreads), group_table_bytes(p.groups), st, p);
 }
 
 }  // namespace
@@ -214,6 +220,10 @@ cudaError_t launch_pack_rows(const PackParams& p, cudaStream_t st) {
 
 cudaError_t launch_row_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st) {
   return bf16 ? row_grad<__nv_bfloat16>(p, num_sms, st) : row_grad<__half>(p, num_sms, st);
+}
+
+cudaError_t launch_bias_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st) {
+  return bf16 ? bias_grad<__nv_bfloat16>(p, num_sms, st) : bias_grad<__half>(p, num_sms, st);
 }
 
 }  // namespace moe

@@ -37,7 +37,19 @@ inline FastDiv fast_div(uint32_t d) {
   return {static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1), s, d};
 }
 
+// The kernels of one backward call run one after another in the stream, but
+// some do not need the one before: dw runs beside dx, the bias gradient beside
+// both, and dz is made beside the copies.  Such a kernel (late_wait) starts
+// once every CTA of its predecessor runs, which the predecessor allows
+// (trigger) only after its own wait, so that all before the predecessor is
+// complete; and it waits for the predecessor before it ends, so that what
+// follows it in the stream follows both.
+struct LaunchOrder {
+  bool late_wait, trigger;
+};
+
 struct ProductParams {
+  LaunchOrder order;
   const int* offsets;  // [groups + 1] first row of each group; nullptr: one group of all rows
   int groups;          // >= 1
   int rows;            // rows of x / dz that exist
@@ -125,11 +137,13 @@ struct PackOperand {
   int64_t ld_dst;
 };
 struct PackParams {
+  LaunchOrder order;
   PackOperand op[3];
 };
 cudaError_t launch_pack_rows(const PackParams& p, cudaStream_t st);
 
 struct RowGradParams {
+  LaunchOrder order;
   const void* dout;
   int64_t ld_dout;
   const void* preact;  // nullptr: dz = dout, not written
@@ -152,8 +166,10 @@ constexpr int kRowDirect = 128;
 inline size_t row_grad_chunks(int rows, int groups) {
   return static_cast<size_t>(rows) / kRowChunk + static_cast<size_t>(groups);
 }
-// dz = dout * act'(preact), and db from dz in fp32
+// dz = dout * act'(preact), and db (direct) or its partial sums from dz in fp32
 cudaError_t launch_row_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st);
+// db from the partial sums
+cudaError_t launch_bias_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st);
 
 // SwiGLU (swiglu.cu)
 struct SwigluParams {

@@ -494,8 +494,19 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
   Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
   Operand dz{a->dout, a->ld_dout, 0};
   const bool products = a->dx != nullptr || a->dw != nullptr;
-  if (ws.make_dz || a->dbias != nullptr) {
-    RowGradParams q{};
+  const bool row_pass = (ws.make_dz && products) || a->dbias != nullptr;
+  const bool joins = a->dbias != nullptr && c->rows > kRowDirect;  // a launch of its own adds db
+  // copies, then dz beside them, then dx, then dw beside it, then db beside both
+  PackParams pack{};
+  if (ws.copy_dout) pack.op[0] = aligned_copy(&dz, 1, R, N, base + ws.dz);
+  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w);
+  if (ws.copy_x) pack.op[2] = aligned_copy(&x, 1, R, K, base + ws.x);
+  const bool packs = ws.copy_dout || ws.copy_w || ws.copy_x;
+  pack.order.trigger = row_pass;
+  MOE_CUDA(launch_pack_rows(pack, st));
+  RowGradParams q{};
+  if (row_pass) {
+    q.order.late_wait = packs;
     q.dout = a->dout;
     q.ld_dout = a->ld_dout;
     q.preact = a->preact;
@@ -508,16 +519,11 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     q.cols = c->out_features;
     q.act = c->activation;
     q.db = a->dbias;
-    q.direct = a->dbias != nullptr && c->rows <= kRowDirect;
+    q.direct = a->dbias != nullptr && !joins;
     q.partial = reinterpret_cast<float*>(base + ws.partial);
-    if (products || a->dbias != nullptr) MOE_CUDA(launch_row_grad(bf16, q, sms, st));
+    MOE_CUDA(launch_row_grad(bf16, q, sms, st));
     if (ws.make_dz) dz = {base + ws.dz, padded(N), 0};
   }
-  PackParams pack{};
-  if (ws.copy_dout) pack.op[0] = aligned_copy(&dz, 1, R, N, base + ws.dz);
-  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w);
-  if (ws.copy_x) pack.op[2] = aligned_copy(&x, 1, R, K, base + ws.x);
-  MOE_CUDA(launch_pack_rows(pack, st));
   ProductParams p{};
   p.offsets = a->offsets;
   p.groups = G;
@@ -542,6 +548,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
         !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, p.box_rows,
                 false))
       return MOE_ERR_CUDA;
+    p.order = {false, a->dw != nullptr || joins};
     MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
   }
   if (a->dw != nullptr) {
@@ -560,7 +567,12 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 64, false) ||
         !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 64, false))
       return MOE_ERR_CUDA;
+    p.order = {a->dx != nullptr, joins};
     MOE_CUDA(launch_any(ch, kProductDw, bf16, m, p, sms, st));
+  }
+  if (joins) {
+    q.order = {products, false};
+    MOE_CUDA(launch_bias_grad(bf16, q, sms, st));
   }
   return MOE_OK;
 }
