@@ -891,9 +891,9 @@ def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream
             return _linear_backward(dout, x, offsets, w, preact, activation, need, into, None)
     st = torch._C._cuda_getCurrentRawStream(dout.get_device())
     if need[0] and dx is None:
-        dx = dout.new_empty((R, K))
+        dx = dout.new_empty((R, K)) if x is None else torch.empty_like(x)
     if need[1] and dw is None:
-        dw = dout.new_empty(w.shape)
+        dw = torch.empty_like(w) if w.is_contiguous() else dout.new_empty(w.shape)
     if need[2] and db is None:
         db = dout.new_empty((G, N) if G else (N,))
     dx, dw, db = (t if n else None for t, n in zip((dx, dw, db), need))

@@ -15,20 +15,14 @@ using namespace product;
 
 constexpr int kPackThreads = 256;
 
-// One warp per row of any of the operands.
-__global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParams p) {
-  begin_ordered(p.order);
-  int64_t row = static_cast<int64_t>(blockIdx.x) * (kPackThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+// One row of any of the operands, by a warp.
+__device__ __forceinline__ void pack_row(const PackParams& p, int64_t row, int lane) {
   int i = 0;
   while (i < 3 && row >= p.op[i].groups * p.op[i].rows) {
     row -= p.op[i].groups * p.op[i].rows;
     ++i;
   }
-  if (i == 3) {
-    end_ordered(p.order);
-    return;
-  }
+  if (i == 3) return;
   const PackOperand& o = p.op[i];
   const int64_t g = row / o.rows;
   const uint16_t* s = static_cast<const uint16_t*>(o.src) + g * o.group_stride + (row - g * o.rows) * o.ld;
@@ -43,10 +37,23 @@ __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParam
     for (int k = 0; k < U; ++k)
       if (c + k * 32 < o.cols) d[c + k * 32] = v[k];
   }
-  end_ordered(p.order);
 }
 
-constexpr int kGradThreads = 256;          // 8 warps: rows of a chunk are dealt to them
+__global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParams p) {
+  pdl_wait();
+  pack_row(p, static_cast<int64_t>(blockIdx.x) * (kPackThreads / 32) + (threadIdx.x >> 5),
+           threadIdx.x & 31);
+}
+
+// CTAs for the copies (a warp per row), and whether that is too many
+int64_t pack_ctas(const PackParams& p) {
+  int64_t rows = 0;
+  for (const PackOperand& o : p.op) rows += o.groups * o.rows;
+  constexpr int kPer = kPackThreads / 32;
+  return (rows + kPer - 1) / kPer;
+}
+
+constexpr int kGradThreads = kPackThreads;  // 8 warps: rows of a chunk are dealt to them
 constexpr int kGradWarps = kGradThreads / 32;
 constexpr int kVec = 8;                    // elements per 16-byte access
 // elements of a row per lane: one 16-byte piece, or two single ones 32 apart
@@ -62,7 +69,8 @@ struct alignas(16) Vec {
 // aligned), or with `direct` all rows of the group.  The column sums are added
 // in fp32, per warp over its rows, then over the warps in order; direct: they
 // are the group's and go to db at once.  VEC: every row starts at a 16-byte
-// boundary and cols % 8 == 0.  Each lane keeps U rows' loads under way.
+// boundary and cols % 8 == 0.  Each lane keeps U rows' loads under way.  The
+// first copy_ctas CTAs copy misaligned operands instead.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGradParams p) {
   constexpr int E = kLaneCols<VEC>;
@@ -70,15 +78,19 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
   constexpr int kCols = 32 * E;
   extern __shared__ int tab_mem[];
   __shared__ float sums[kGradWarps][kCols];
-  begin_ordered(p.order);
-  const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, kRowChunk);
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x < p.copy_ctas) {
+    pack_row(p.copies, static_cast<int64_t>(blockIdx.x) * kGradWarps + warp, lane);
+    return;
+  }
+  const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, kRowChunk);
   const int col_blocks = (p.cols + kCols - 1) / kCols;
   const int total = (p.direct ? p.groups : tab.block_start[p.groups]) * col_blocks;
   const T* dout = static_cast<const T*>(p.dout);
   const T* preact = static_cast<const T*>(p.preact);
   T* dz = static_cast<T*>(p.dz);
-  for (int w = blockIdx.x; w < total; w += gridDim.x) {
+  for (int w = blockIdx.x - p.copy_ctas; w < total; w += gridDim.x - p.copy_ctas) {
     const int chunk = w / col_blocks;  // (direct: the group)
     const int c0 = (w - chunk * col_blocks) * kCols;
     const int g = p.direct ? chunk : group_of_block(tab, p.groups, chunk);
@@ -145,7 +157,6 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
       __syncthreads();
     }
   }
-  end_ordered(p.order);
 }
 
 // db[g][c] for 32 columns per CTA: warp k adds chunks k, k + 8, ..., then the
@@ -186,7 +197,11 @@ bool rows_aligned(const void* p, int64_t ld) {
 }
 
 template <typename T>
-cudaError_t row_grad(const RowGradParams& p, int num_sms, cudaStream_t st) {
+cudaError_t row_grad(const RowGradParams& p0, int num_sms, cudaStream_t st) {
+  RowGradParams p = p0;
+  const int64_t copies = pack_ctas(p.copies);
+  if (copies > INT32_MAX / 2) return cudaErrorInvalidValue;
+  p.copy_ctas = static_cast<unsigned>(copies);
   const size_t tab = group_table_bytes(p.groups);
   const bool vec = p.cols % kVec == 0 && rows_aligned(p.dout, p.ld_dout) &&
                    (p.preact == nullptr ||
@@ -194,7 +209,7 @@ cudaError_t row_grad(const RowGradParams& p, int num_sms, cudaStream_t st) {
   const int64_t items = static_cast<int64_t>(p.direct ? p.groups
                                                       : row_grad_chunks(p.rows, p.groups) + 1) *
                         ((p.cols + (vec ? 32 * kVec : 64) - 1) / (vec ? 32 * kVec : 64));
-  const int grid = static_cast<int>(std::min<int64_t>(items, 8 * num_sms));
+  const unsigned grid = p.copy_ctas + static_cast<unsigned>(std::min<int64_t>(items, 8 * num_sms));
   return vec ? launch_pdl(row_grad_kernel<T, true>, dim3(grid), dim3(kGradThreads), tab, st, p)
              : launch_pdl(row_grad_kernel<T, false>, dim3(grid), dim3(kGradThreads), tab, st, p);
 }
@@ -209,13 +224,11 @@ cudaError_t bias_grad(const RowGradParams& p, int num_sms, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_pack_rows(const PackParams& p, cudaStream_t st) {
-  int64_t rows = 0;
-  for (const PackOperand& o : p.op) rows += o.groups * o.rows;
-  if (rows == 0) return cudaSuccess;
-  constexpr int kPer = kPackThreads / 32;
-  if (rows > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(pack_rows_kernel, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),
-                    dim3(kPackThreads), 0, st, p);
+  const int64_t ctas = pack_ctas(p);
+  if (ctas == 0) return cudaSuccess;
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(pack_rows_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPackThreads), 0, st,
+                    p);
 }
 
 cudaError_t launch_row_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st) {

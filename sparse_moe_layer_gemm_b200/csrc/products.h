@@ -39,7 +39,7 @@ inline FastDiv fast_div(uint32_t d) {
 
 // The kernels of one backward call run one after another in the stream, but
 // some do not need the one before: dw runs beside dx, the bias gradient beside
-// both, and dz is made beside the copies.  Such a kernel (late_wait) starts
+// both.  Such a kernel (late_wait) starts
 // once every CTA of its predecessor runs, which the predecessor allows
 // (trigger) only after its own wait, so that all before the predecessor is
 // complete; and it waits for the predecessor before it ends, so that what
@@ -137,13 +137,14 @@ struct PackOperand {
   int64_t ld_dst;
 };
 struct PackParams {
-  LaunchOrder order;
   PackOperand op[3];
 };
 cudaError_t launch_pack_rows(const PackParams& p, cudaStream_t st);
 
 struct RowGradParams {
-  LaunchOrder order;
+  LaunchOrder order;   // of the bias gradient's launch
+  PackParams copies;   // made in the same launch as dz
+  unsigned copy_ctas;  // (filled in at launch)
   const void* dout;
   int64_t ld_dout;
   const void* preact;  // nullptr: dz = dout, not written

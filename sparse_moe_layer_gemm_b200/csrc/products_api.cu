@@ -496,17 +496,16 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
   const bool products = a->dx != nullptr || a->dw != nullptr;
   const bool row_pass = (ws.make_dz && products) || a->dbias != nullptr;
   const bool joins = a->dbias != nullptr && c->rows > kRowDirect;  // a launch of its own adds db
-  // copies, then dz beside them, then dx, then dw beside it, then db beside both
+  // copies and dz in one launch, then dx, then dw beside it, then db beside both
   PackParams pack{};
   if (ws.copy_dout) pack.op[0] = aligned_copy(&dz, 1, R, N, base + ws.dz);
   if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w);
   if (ws.copy_x) pack.op[2] = aligned_copy(&x, 1, R, K, base + ws.x);
-  const bool packs = ws.copy_dout || ws.copy_w || ws.copy_x;
-  pack.order.trigger = row_pass;
-  MOE_CUDA(launch_pack_rows(pack, st));
   RowGradParams q{};
-  if (row_pass) {
-    q.order.late_wait = packs;
+  if (!row_pass) {
+    MOE_CUDA(launch_pack_rows(pack, st));
+  } else {
+    q.copies = pack;
     q.dout = a->dout;
     q.ld_dout = a->ld_dout;
     q.preact = a->preact;
