@@ -418,44 +418,75 @@ __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
 }
 
 // ROWS staged rows x 32 features <-> global memory at `base` (the chunk's first
-// row and this warp's first feature); n rows and nf features exist.  vec: 16
-// byte pieces (aligned rows, nf a multiple of 8).
-template <typename T, int ROWS>
-__device__ __forceinline__ void copy_out(const uint8_t* stg, T* base, int64_t ld, int n, int nf,
-                                         bool vec, int lane) {
-  if (vec) {
-    const int piece = lane & 3, row = lane >> 2;
-    uint4 v[ROWS / 8];
+// row and this warp's first feature); n rows and nf features exist.  W
+// elements per access (8, 2 or 1, as the rows' alignment allows), 32 / W lanes
+// per row, eight accesses under way at once.
+template <int W>
+struct Access;
+template <>
+struct Access<8> {
+  using Type = uint4;
+};
+template <>
+struct Access<2> {
+  using Type = uint32_t;
+};
+template <>
+struct Access<1> {
+  using Type = uint16_t;
+};
+
+template <typename T, int ROWS, int W, bool OUT>
+__device__ __forceinline__ void copy_staged(uint8_t* stg, T* base, int64_t ld, int n, int nf,
+                                            int lane) {
+  using V = typename Access<W>::Type;
+  constexpr int kLanes = 32 / W, kPer = 32 / kLanes;  // lanes per row, rows per access
+  constexpr int kBatch = ROWS / kPer < 8 ? ROWS / kPer : 8;
+  const int col = (lane % kLanes) * W, row = lane / kLanes;
+  const bool whole = col + W <= nf;
+  uint8_t* s = stg + row * kEpiPitch + col * 2;
+  T* at = base + row * ld + col;
 #pragma unroll
-    for (int k = 0; k < ROWS / 8; ++k)
-      v[k] = *reinterpret_cast<const uint4*>(stg + (8 * k + row) * kEpiPitch + piece * 16);
-    T* at = base + row * ld + piece * 8;
-    if (piece * 8 < nf) {
+  for (int k0 = 0; k0 < ROWS / kPer; k0 += kBatch) {
+    V v[kBatch];
 #pragma unroll
-      for (int k = 0; k < ROWS / 8; ++k)
-        if (8 * k + row < n) *reinterpret_cast<uint4*>(at + 8 * k * ld) = v[k];
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = (k0 + k) * kPer;
+      if (OUT)
+        v[k] = *reinterpret_cast<const V*>(s + r * kEpiPitch);
+      else if (whole && r + row < n)
+        v[k] = *reinterpret_cast<const V*>(at + r * ld);
     }
-  } else if (lane < nf) {
-    for (int row = 0; row < n; ++row)
-      base[row * ld + lane] = *reinterpret_cast<const T*>(stg + row * kEpiPitch + lane * 2);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = (k0 + k) * kPer;
+      if (!whole || r + row >= n) continue;
+      if (OUT)
+        *reinterpret_cast<V*>(at + r * ld) = v[k];
+      else
+        *reinterpret_cast<V*>(s + r * kEpiPitch) = v[k];
+    }
+  }
+  if (W == 2 && col + 1 == nf) {  // the odd last feature
+    for (int r = 0; r + row < n; r += kPer) {
+      T* e = reinterpret_cast<T*>(s + r * kEpiPitch);
+      if (OUT)
+        at[r * ld] = *e;
+      else
+        *e = at[r * ld];
+    }
   }
 }
-template <typename T>
-__device__ __forceinline__ void copy_in(uint8_t* stg, const T* base, int64_t ld, int n, int nf,
-                                        bool vec, int lane) {
-  if (vec) {
-    const int piece = lane & 3;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int row = 8 * k + (lane >> 2);
-      if (row < n && piece * 8 < nf)
-        *reinterpret_cast<uint4*>(stg + row * kEpiPitch + piece * 16) =
-            *reinterpret_cast<const uint4*>(base + row * ld + piece * 8);
-    }
-  } else if (lane < nf) {
-    for (int row = 0; row < n; ++row)
-      *reinterpret_cast<T*>(stg + row * kEpiPitch + lane * 2) = base[row * ld + lane];
-  }
+
+template <typename T, int ROWS, bool OUT>
+__device__ __forceinline__ void copy_rows(uint8_t* stg, T* base, int64_t ld, int n, int nf, int width,
+                                          int lane) {
+  if (width == 8)
+    copy_staged<T, ROWS, 8, OUT>(stg, base, ld, n, nf, lane);
+  else if (width == 2)
+    copy_staged<T, ROWS, 2, OUT>(stg, base, ld, n, nf, lane);
+  else
+    copy_staged<T, ROWS, 1, OUT>(stg, base, ld, n, nf, lane);
 }
 
 template <int N>
@@ -521,9 +552,10 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
   for (int c = part * ROWS; c < n_valid; c += parts * ROWS) {
     const int n = min(ROWS, n_valid - c);
     if (EXTRA && p.residual != nullptr)
-      copy_in<T>(stg + kEpiChunk,
-                 static_cast<const T*>(p.residual) + (row0 + c) * p.ld_residual + f0,
-                 p.ld_residual, n, nf, p.vec_residual, lane);
+      copy_rows<T, 16, false>(
+          stg + kEpiChunk,
+          const_cast<T*>(static_cast<const T*>(p.residual)) + (row0 + c) * p.ld_residual + f0,
+          p.ld_residual, n, nf, p.width_residual, lane);
     if (!zeros) tmem_ld_wait();
     // v[8 k + 2 m + e]: rows 8 k + 2 (lane % 4) + e of matrix m
     float v[16 * kB];
@@ -549,8 +581,8 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
     };
     if (EXTRA && p.preact != nullptr) {
       stage();
-      copy_out<T, ROWS>(stg, static_cast<T*>(p.preact) + (row0 + c) * p.ld_preact + f0, p.ld_preact,
-                        n, nf, p.vec_preact, lane);
+      copy_rows<T, ROWS, true>(stg, static_cast<T*>(p.preact) + (row0 + c) * p.ld_preact + f0,
+                               p.ld_preact, n, nf, p.width_preact, lane);
       __syncwarp();
     }
     if (MODE == kProductForward) activate_all(v, p.act);
@@ -569,7 +601,7 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
       }
     }
     stage();
-    copy_out<T, ROWS>(stg, out + c * p.ld_out, p.ld_out, n, nf, p.vec_out, lane);
+    copy_rows<T, ROWS, true>(stg, out + c * p.ld_out, p.ld_out, n, nf, p.width_out, lane);
     __syncwarp();
   }
 }
@@ -609,7 +641,7 @@ __device__ __forceinline__ void finish_row4(const ProductParams& p, int64_t row,
         if (i < n) v[i] += to_f32<T>(b[i]);
     }
     if (p.preact != nullptr)
-      store4<T>(static_cast<T*>(p.preact) + row * p.ld_preact + feat, v, n, p.vec_preact);
+      store4<T>(static_cast<T*>(p.preact) + row * p.ld_preact + feat, v, n, p.width_preact == 8);
     activate_all(v, p.act);
     if (p.residual != nullptr) {
       const T* r = static_cast<const T*>(p.residual) + row * p.ld_residual + feat;
@@ -618,7 +650,7 @@ __device__ __forceinline__ void finish_row4(const ProductParams& p, int64_t row,
         if (i < n) v[i] += to_f32<T>(r[i]);
     }
   }
-  store4<T>(static_cast<T*>(p.out) + row * p.ld_out + feat, v, n, p.vec_out);
+  store4<T>(static_cast<T*>(p.out) + row * p.ld_out + feat, v, n, p.width_out == 8);
 }
 
 template <typename T>

@@ -78,8 +78,9 @@ struct ProductParams {
   void* preact;
   int64_t ld_preact;
   int act;             // moe_activation_t
-  // rows at 16-byte boundaries, feats a multiple of 8: 16-byte accesses
-  bool vec_out, vec_residual, vec_preact;
+  // elements per access that the rows' alignment allows: 8 (and feats a multiple
+  // of 8), 2 or 1
+  int width_out, width_residual, width_preact;
   int* status;         // device status word
 };
 

@@ -105,9 +105,10 @@ bool tma_ready(const void* p, int64_t ld, int64_t group_stride) {
   return aligned(p, 16) && ld % 8 == 0 && group_stride % 8 == 0;
 }
 
-// rows of 16-byte pieces
-bool vec_rows(const void* p, int64_t ld, int64_t cols) {
-  return aligned(p, 16) && ld % 8 == 0 && cols % 8 == 0;
+// Elements per access to the rows of a 16-bit matrix.
+int row_width(const void* p, int64_t ld, int64_t cols) {
+  if (aligned(p, 16) && ld % 8 == 0 && cols % 8 == 0) return 8;
+  return aligned(p, 4) && ld % 2 == 0 ? 2 : 1;
 }
 
 // A matrix in memory: rows of `cols` bytes, `ld` bytes apart.
@@ -459,9 +460,9 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.preact = a->preact;
   p.ld_preact = a->ld_preact;
   p.act = c->activation;
-  p.vec_out = vec_rows(a->out, a->ld_out, N);
-  p.vec_residual = vec_rows(a->residual, a->ld_residual, N);
-  p.vec_preact = vec_rows(a->preact, a->ld_preact, N);
+  p.width_out = row_width(a->out, a->ld_out, N);
+  p.width_residual = row_width(a->residual, a->ld_residual, N);
+  p.width_preact = row_width(a->preact, a->ld_preact, N);
   p.status = status;
   ProductMaps m;
   p.wide_a = N % 64 == 0;
@@ -534,7 +535,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.depth = c->out_features;
     p.out = a->dx;
     p.ld_out = a->ld_dx;
-    p.vec_out = vec_rows(a->dx, a->ld_dx, K);
+    p.width_out = row_width(a->dx, a->ld_dx, K);
     int64_t n_groups, mean;
     filled(a->offsets, G, R, &n_groups, &mean);
     const Choice ch =
@@ -556,7 +557,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.depth = 0;
     p.out = a->dw;
     p.ld_out = N;
-    p.vec_out = vec_rows(a->dw, N, N);
+    p.width_out = row_width(a->dw, N, N);
     const Choice ch =
         choose({N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), false, true, false}, sms);
     p.bn = ch.bn;
