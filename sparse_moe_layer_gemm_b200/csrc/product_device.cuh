@@ -549,13 +549,31 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
 #pragma unroll
   for (int i = 0; i < 16 * kB; ++i) r[i >> 3][i & 7] = 0;
   if (!zeros) load(part * ROWS);
+  // a chunk's residual of 16-byte pieces is fetched a chunk ahead
+  const T* residual = static_cast<const T*>(p.residual) + row0 * p.ld_residual + f0;
+  const bool ahead = EXTRA && p.residual != nullptr && p.width_residual == 8;
+  const int piece = lane & 3, piece_row = lane >> 2;
+  uint4 res[2];
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (piece * 8 < nf && c + 8 * k + piece_row < n_valid)
+        res[k] = *reinterpret_cast<const uint4*>(
+            residual + (c + 8 * k + piece_row) * p.ld_residual + piece * 8);
+  };
+  if (ahead && part * ROWS < n_valid) fetch(part * ROWS);
   for (int c = part * ROWS; c < n_valid; c += parts * ROWS) {
     const int n = min(ROWS, n_valid - c);
-    if (EXTRA && p.residual != nullptr)
-      copy_rows<T, 16, false>(
-          stg + kEpiChunk,
-          const_cast<T*>(static_cast<const T*>(p.residual)) + (row0 + c) * p.ld_residual + f0,
-          p.ld_residual, n, nf, p.width_residual, lane);
+    if (ahead) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<uint4*>(stg + kEpiChunk + (8 * k + piece_row) * kEpiPitch + piece * 16) =
+            res[k];
+      if (c + parts * ROWS < n_valid) fetch(c + parts * ROWS);
+    } else if (EXTRA && p.residual != nullptr) {
+      copy_rows<T, 16, false>(stg + kEpiChunk, const_cast<T*>(residual) + c * p.ld_residual,
+                              p.ld_residual, n, nf, p.width_residual, lane);
+    }
     if (!zeros) tmem_ld_wait();
     // v[8 k + 2 m + e]: rows 8 k + 2 (lane % 4) + e of matrix m
     float v[16 * kB];
@@ -606,14 +624,14 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
   }
 }
 
-template <int MODE, typename T>
+template <int MODE, typename T, int ROWS>
 __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t taddr, int part,
                                            int parts, int n_valid, int64_t row0, int f0, int g,
                                            bool zeros, uint8_t* stg, int lane) {
   if (MODE == kProductForward && (p.preact != nullptr || p.residual != nullptr))
     store_chunks<MODE, T, 16, true>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
   else
-    store_chunks<MODE, T, 32, false>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
+    store_chunks<MODE, T, ROWS, false>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
 }
 
 // Four neighbouring features of a row of the split form.

@@ -17,8 +17,8 @@
 // the cluster and add them in rank order: the same sum on every run, no
 // workspace, no counters.
 //
-// Roles per CTA (6 warps): warp 0 TMA producer, warp 1 tensor memory and MMA
-// issue, warps 2-5 epilogue (one accumulator lane quadrant each).  Persistent
+// Roles per CTA (10 warps): warp 0 TMA producer, warp 1 tensor memory and MMA
+// issue, warps 2-9 epilogue (two per accumulator lane quadrant).  Persistent
 // over tiles w = cluster, cluster + clusters, ...; the accumulator is
 // double-buffered.  A slot holds two sub-slots of 64 steps: with few rows the
 // weights stream no faster than the issuing warps turn slots over (one tile of
@@ -42,11 +42,17 @@ namespace {
 
 using namespace product;
 
-constexpr int kThreads = 32 * 6;
+constexpr int kEpiWarps = 8;  // two per accumulator lane quadrant, on alternate chunks of rows
+constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kABytes = 2 * kSubBytes;
 constexpr int kSubs = 2;  // sub-slots of 64 contraction steps per slot
 constexpr int kMaxStages = 6;
-constexpr int kEpiBytes = 4 * kEpiWarpBytes;
+
+// staging of the epilogue: 16 rows per warp, twice that with a residual or the
+// pre-activation
+__host__ __device__ __forceinline__ int epi_bytes(const ProductParams& p) {
+  return kEpiWarps * (p.residual != nullptr || p.preact != nullptr ? kEpiWarpBytes : kEpiChunk);
+}
 constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
 
 // bytes of the B operand of one slot
@@ -78,7 +84,7 @@ __device__ __forceinline__ void my_slots(int depth, int rank, int split, int* kb
   *kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
 }
 
-// Rows j, j + 4, ... below j1 of a tile whose SPLIT partials lie at `mine` in
+// Rows j, j + kEpiWarps, ... below j1 of a tile whose SPLIT partials lie at `mine` in
 // the cluster's CTAs: a lane adds 4 features of a row in rank order, with 16
 // of a thread's loads under way at once.
 template <int SPLIT, typename Store>
@@ -87,16 +93,17 @@ __device__ __forceinline__ void join_rows(uint32_t mine, int j, int j1, Store st
   uint32_t from[SPLIT];
 #pragma unroll
   for (int k = 0; k < SPLIT; ++k) from[k] = mapa_shared(mine, k);
-  for (; j < j1; j += 4 * kRows) {
+  for (; j < j1; j += kEpiWarps * kRows) {
     float4 got[kRows][SPLIT];
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int k = 0; k < SPLIT; ++k)
-        if (j + 4 * i < j1) got[i][k] = ld_cluster_f32x4(from[k] + (j + 4 * i) * (kProductBM * 4));
+        if (j + kEpiWarps * i < j1)
+          got[i][k] = ld_cluster_f32x4(from[k] + (j + kEpiWarps * i) * (kProductBM * 4));
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (j + 4 * i >= j1) break;
+      if (j + kEpiWarps * i >= j1) break;
       float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < SPLIT; ++k) {
@@ -105,7 +112,7 @@ __device__ __forceinline__ void join_rows(uint32_t mine, int j, int j1, Store st
         v[2] += got[i][k].z;
         v[3] += got[i][k].w;
       }
-      store(j + 4 * i, v);
+      store(j + kEpiWarps * i, v);
     }
   }
 }
@@ -126,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int load_bytes = kABytes + (kBMn ? b_bytes(MODE, p.bn) : p.box_rows * 128);
   const int slot_bytes = kSubs * sub_bytes;
   uint8_t* epi = smem + stages * slot_bytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + kEpiBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + epi_bytes(p));
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = full0 + 8 * kMaxStages;
   const uint32_t tfull0 = empty0 + 8 * kMaxStages;
@@ -155,10 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, 4);
+      mbar_init(tempty0 + 8 * b, kEpiWarps);
     }
     mbar_init(drain, 1);
-    mbar_init(xfull, 4 * split);
+    mbar_init(xfull, kEpiWarps * split);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -324,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // the TMEM lane quadrant this warp may read
     uint32_t tc = 0;
-    uint8_t* stg = epi + (warp - 2) * kEpiWarpBytes;
+    const int part = (warp - 2) >> 2;  // which of its quadrant's warps
+    uint8_t* stg = epi + (warp - 2) * (epi_bytes(p) / kEpiWarps);
     for (int w = cluster; w < total; w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
       int kb0, kb1;
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
       if (split == 1) {
-        store_tile<MODE, T>(p, taddr, 0, 1, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
+        store_tile<MODE, T, 16>(p, taddr, part, kEpiWarps / 4, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
         if (!empty) {
           tc_fence_before();
           __syncwarp();
@@ -354,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // one tile per cluster in this form (the launch has a cluster per tile):
       // the partial goes where the slots were, [row][128 features]
-      float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
-      for (int c = 0; c < t.n_valid; c += 32) {
+      float* partial = reinterpret_cast<float*>(smem) + q * 32 + lane;
+      for (int c = 32 * part; c < t.n_valid; c += 32 * (kEpiWarps / 4)) {
         uint32_t r[2][16];
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i >> 4][i & 15] = 0;
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (c + i < t.n_valid) part[(c + i) * kProductBM] = __uint_as_float(r[i >> 4][i & 15]);
+          if (c + i < t.n_valid) partial[(c + i) * kProductBM] = __uint_as_float(r[i >> 4][i & 15]);
       }
       __syncwarp();
       cluster_wait();
@@ -442,7 +450,7 @@ cudaError_t product_configure_device() {
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p0,
                            int num_sms, cudaStream_t st) {
   ProductParams p = p0;
-  const size_t fixed = 1024 + kEpiBytes + kBarBytes +
+  const size_t fixed = 1024 + static_cast<size_t>(epi_bytes(p)) + kBarBytes +
                        static_cast<size_t>(group_table_bytes(p.groups));
   const size_t slot = kSubs * (kABytes + static_cast<size_t>(b_bytes(mode, p.bn)));
   const int64_t tiles = product_tile_order(mode, kProductBM, &p);

@@ -405,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
           tc_fence_after();
         }
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
-        store_tile<MODE, T>(p, taddr, part, 2, min(hn, t.n_valid - h * hn), row0 + h * hn,
+        store_tile<MODE, T, 32>(p, taddr, part, 2, min(hn, t.n_valid - h * hn), row0 + h * hn,
                             t.f0 + static_cast<int>(rank) * kProductBM + q * 32, t.g, empty, stg,
                             lane);
         if (!empty) {
