@@ -370,7 +370,21 @@ __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable&
 // from 95 to 20 us (33.5 MB written).
 constexpr int kEpiPitch = 80;                  // bytes per staged row: 64 + 16 against bank conflicts
 constexpr int kEpiChunk = 16 * kEpiPitch;      // one staged chunk
-constexpr int kEpiWarpBytes = 2 * kEpiChunk;   // 32 rows, or 16 and the residual's 16
+// bytes per warp: `rows` rows, or 16 and a ring of `ahead` chunks of the residual
+__host__ __device__ __forceinline__ int epi_warp_bytes(const ProductParams& p, int rows, int ahead) {
+  return p.residual != nullptr ? (1 + ahead) * kEpiChunk : rows / 16 * kEpiChunk;
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
@@ -489,6 +503,32 @@ __device__ __forceinline__ void copy_rows(uint8_t* stg, T* base, int64_t ld, int
     copy_staged<T, ROWS, 1, OUT>(stg, base, ld, n, nf, lane);
 }
 
+// The activation, or its slope, of N values: the choice is made once.
+template <int N>
+__device__ __forceinline__ void slope_all(float (&v)[N], int act) {
+  switch (act) {
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activation_slope(v[i], MOE_ACT_RELU);
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activation_slope(v[i], MOE_ACT_SILU);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activation_slope(v[i], MOE_ACT_GELU);
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = activation_slope(v[i], MOE_ACT_GELU_TANH);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 1.f;
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
   switch (act) {
@@ -517,8 +557,8 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
 // taddr (quadrant and buffer included), in chunks of ROWS rows: `part`,
 // part + parts, ... below n_valid; row0 the tile's first output row, f0 the
 // warp's first feature.  zeros: the contraction was empty.  EXTRA: with a
-// residual or the pre-activation, whose staging takes the second 16 rows'.
-template <int MODE, typename T, int ROWS, bool EXTRA>
+// residual or the pre-activation.
+template <int MODE, typename T, int ROWS, bool EXTRA, int AHEAD>
 __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t taddr, int part,
                                              int parts, int n_valid, int64_t row0, int f0, int g,
                                              bool zeros, uint8_t* stg, int lane) {
@@ -549,31 +589,33 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
 #pragma unroll
   for (int i = 0; i < 16 * kB; ++i) r[i >> 3][i & 7] = 0;
   if (!zeros) load(part * ROWS);
-  // a chunk's residual of 16-byte pieces is fetched a chunk ahead
+  // a residual of 16-byte pieces comes by asynchronous copies AHEAD chunks ahead
+  // into a ring of staged chunks (4096 rows 1024 -> 4096 36 us, 31 without a
+  // residual; as register loads, whose arrival every later shared-memory read
+  // waits for, 49 us one chunk ahead and 47 us four ahead)
   const T* residual = static_cast<const T*>(p.residual) + row0 * p.ld_residual + f0;
-  const bool ahead = EXTRA && p.residual != nullptr && p.width_residual == 8;
-  const int piece = lane & 3, piece_row = lane >> 2;
-  uint4 res[2];
-  auto fetch = [&](int c) {
+  const bool ring = EXTRA && p.residual != nullptr && p.width_residual == 8;
+  auto fetch = [&](int c, int slot) {
+    const int piece = lane & 3;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (piece * 8 < nf && c + 8 * k + piece_row < n_valid)
-        res[k] = *reinterpret_cast<const uint4*>(
-            residual + (c + 8 * k + piece_row) * p.ld_residual + piece * 8);
+    for (int k = 0; k < 2; ++k) {
+      const int row = 8 * k + (lane >> 2);
+      if (piece * 8 < nf && c + row < n_valid)
+        cp_async_16(smem_u32(stg) + (1 + slot) * kEpiChunk + row * kEpiPitch + piece * 16,
+                    residual + (c + row) * p.ld_residual + piece * 8);
+    }
+    cp_async_commit();
   };
-  if (ahead && part * ROWS < n_valid) fetch(part * ROWS);
+  if (ring) {
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a) fetch((part + a * parts) * ROWS, a);
+  }
+  int slot = 0;
   for (int c = part * ROWS; c < n_valid; c += parts * ROWS) {
     const int n = min(ROWS, n_valid - c);
-    if (ahead) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<uint4*>(stg + kEpiChunk + (8 * k + piece_row) * kEpiPitch + piece * 16) =
-            res[k];
-      if (c + parts * ROWS < n_valid) fetch(c + parts * ROWS);
-    } else if (EXTRA && p.residual != nullptr) {
+    if (EXTRA && p.residual != nullptr && !ring)
       copy_rows<T, 16, false>(stg + kEpiChunk, const_cast<T*>(residual) + c * p.ld_residual,
                               p.ld_residual, n, nf, p.width_residual, lane);
-    }
     if (!zeros) tmem_ld_wait();
     // v[8 k + 2 m + e]: rows 8 k + 2 (lane % 4) + e of matrix m
     float v[16 * kB];
@@ -605,11 +647,12 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
     }
     if (MODE == kProductForward) activate_all(v, p.act);
     if (EXTRA && p.residual != nullptr) {
+      if (ring) cp_async_wait<AHEAD - 1>();
       __syncwarp();
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         uint32_t w[4];
-        ldmatrix_x4_trans(mat + kEpiChunk + k * 8 * kEpiPitch, w);
+        ldmatrix_x4_trans(mat + (1 + slot) * kEpiChunk + k * 8 * kEpiPitch, w);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           const float2 f = unpack2<T>(w[m]);
@@ -621,17 +664,22 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
     stage();
     copy_rows<T, ROWS, true>(stg, out + c * p.ld_out, p.ld_out, n, nf, p.width_out, lane);
     __syncwarp();
+    if (ring) {  // (every lane has read its part of this chunk's residual)
+      fetch(c + AHEAD * parts * ROWS, slot);
+      slot = slot + 1 < AHEAD ? slot + 1 : 0;
+    }
   }
+  if (ring) cp_async_wait<0>();
 }
 
-template <int MODE, typename T, int ROWS>
+template <int MODE, typename T, int ROWS, int AHEAD>
 __device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t taddr, int part,
                                            int parts, int n_valid, int64_t row0, int f0, int g,
                                            bool zeros, uint8_t* stg, int lane) {
   if (MODE == kProductForward && (p.preact != nullptr || p.residual != nullptr))
-    store_chunks<MODE, T, 16, true>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
+    store_chunks<MODE, T, 16, true, AHEAD>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
   else
-    store_chunks<MODE, T, ROWS, false>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
+    store_chunks<MODE, T, ROWS, false, AHEAD>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
 }
 
 // Four neighbouring features of a row of the split form.

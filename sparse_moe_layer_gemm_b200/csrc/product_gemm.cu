@@ -48,10 +48,10 @@ constexpr int kABytes = 2 * kSubBytes;
 constexpr int kSubs = 2;  // sub-slots of 64 contraction steps per slot
 constexpr int kMaxStages = 6;
 
-// staging of the epilogue: 16 rows per warp, twice that with a residual or the
-// pre-activation
+constexpr int kAhead = 2;  // residual chunks on their way
+// staging of the epilogue (a split tile's rows are stored from registers)
 __host__ __device__ __forceinline__ int epi_bytes(const ProductParams& p) {
-  return kEpiWarps * (p.residual != nullptr || p.preact != nullptr ? kEpiWarpBytes : kEpiChunk);
+  return p.split > 1 ? 0 : kEpiWarps * epi_warp_bytes(p, 16, kAhead);
 }
 constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
 
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
       if (split == 1) {
-        store_tile<MODE, T, 16>(p, taddr, part, kEpiWarps / 4, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
+        store_tile<MODE, T, 16, kAhead>(p, taddr, part, kEpiWarps / 4, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
         if (!empty) {
           tc_fence_before();
           __syncwarp();

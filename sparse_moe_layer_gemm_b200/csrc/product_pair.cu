@@ -52,17 +52,19 @@ constexpr int kOperand = 2 * kSubBytes;  // 128 rows or features of 64 steps
 constexpr int kAccCols = 256;
 constexpr int kLead = 2;  // slots by which the first accumulator leads at a tile's ends
 
+constexpr int kAhead = 4;  // residual chunks on their way
+
 template <int HALVES>
 struct PairShape {
   static constexpr int kSlot = (1 + HALVES) * kOperand;
-  static constexpr int kStages = HALVES == 1 ? 6 : 4;
-  static constexpr int kBars = 3 * kStages + 5;
+  static constexpr int kMaxStages = HALVES == 1 ? 6 : 4;
+  static constexpr int kBars = 3 * kMaxStages + 5;
   static constexpr int kBarBytes = (kBars + 1) / 2 * 16 + 16;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kSlot +
-                                  kEpiWarps * kEpiWarpBytes + kBarBytes;
-  static_assert(kLead < kStages, "the leading accumulator waits for slots that the other frees");
-  static_assert(kSmem + group_table_bytes(kProductMaxGroups) <= 227 * 1024, "shared memory");
 };
+
+__host__ __device__ __forceinline__ int epi_bytes(const ProductParams& p) {
+  return kEpiWarps * epi_warp_bytes(p, 32, kAhead);
+}
 
 // Whether the rows behind a dw tile's last one, up to a multiple of 16, are
 // another group's (behind the tensor's last row the load fills zeros).
@@ -77,7 +79,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   constexpr bool kAMn = MODE != kProductDx;
   constexpr bool kBMn = MODE == kProductDw;
   constexpr int kSlot = PairShape<HALVES>::kSlot;
-  constexpr int kStages = PairShape<HALVES>::kStages;
+  const uint32_t stages = static_cast<uint32_t>(p.stages);
+  constexpr int kMaxStages = PairShape<HALVES>::kMaxStages;
   constexpr int kBarBytes = PairShape<HALVES>::kBarBytes;
   // an accumulator's rows are rounded up to kUnit for the MMA, so that each CTA
   // supplies a multiple of 8 (MN-major: of 16; a half of 8 rows more is slow to
@@ -93,10 +96,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kSlot + kEpiWarps * kEpiWarpBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * kSlot + epi_bytes(p));
   const uint32_t full0 = smem_u32(bars);
-  const uint32_t empty0 = full0 + 8 * kStages;
-  const uint32_t tfull0 = empty0 + 8 * kStages;
+  const uint32_t empty0 = full0 + 8 * kMaxStages;
+  const uint32_t tfull0 = empty0 + 8 * kMaxStages;
   const uint32_t tempty0 = tfull0 + 16;
   const uint32_t drain = tempty0 + 16;
   const uint32_t tail0 = drain + 8;
@@ -111,7 +114,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   const int n_pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (uint32_t s = 0; s < stages; ++s) {
       mbar_init(full0 + 8 * s, 2);
       mbar_init(empty0 + 8 * s, 1);
       mbar_init(tail0 + 8 * s, 1);
@@ -201,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
         }
         __syncwarp();
         ++it;
-        if (++s == kStages) {
+        if (++s == stages) {
           s = 0;
           ph ^= 1u;
         }
@@ -210,10 +213,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
     // the leader sees every armed slot complete (both CTAs' loads); the peer is
     // held by the cluster barrier at the end
     if (rank == 0 && lane == 0) {
-      const uint32_t used = it < static_cast<uint32_t>(kStages) ? it : kStages;
+      const uint32_t used = it < stages ? it : stages;
       for (uint32_t s = 0; s < used; ++s) {
-        const uint32_t last = (it - 1u) - ((it - 1u - s) % kStages);
-        mbar_wait(full0 + 8 * s, (last / kStages) & 1u, nullptr, p.status);
+        const uint32_t last = (it - 1u) - ((it - 1u - s) % stages);
+        mbar_wait(full0 + 8 * s, (last / stages) & 1u, nullptr, p.status);
       }
     }
   } else if (warp == 1) {
@@ -260,8 +263,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
         // slot k slots on from the current one holds its loads
         auto wait_slot = [&](uint32_t k) {
           const uint32_t q = s + k;
-          const uint32_t bar = full0 + 8 * (q < kStages ? q : q - kStages);
-          const uint32_t par = q < kStages ? ph : ph ^ 1u;
+          const uint32_t bar = full0 + 8 * (q < stages ? q : q - stages);
+          const uint32_t par = q < stages ? ph : ph ^ 1u;
           // a cleared slot's zeros come from the peer's threads: cluster scope
           const bool r = __all_sync(
               0xffffffffu, MODE == kProductDw ? mbar_wait_cluster(bar, par, abort_flag, p.status)
@@ -272,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
         // the MMAs of half h on that slot, `left` contraction steps remaining
         auto issue = [&](int h, uint32_t k, int left) {
           const uint32_t q = s + k;
-          const uint64_t at = static_cast<uint64_t>((q < kStages ? q : q - kStages) * (kSlot >> 4));
+          const uint64_t at = static_cast<uint64_t>((q < stages ? q : q - stages) * (kSlot >> 4));
           const uint64_t ad = ad0 + at;
           const uint64_t bd = bd0 + at + static_cast<uint64_t>(h * (kOperand >> 4));
           const uint32_t acc = left < t.depth ? 1u : 0u;
@@ -293,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
         auto release = [&]() {
           if (elect_one()) tc_commit_pair_mc(empty0 + 8 * s, 3);  // frees the slot in both CTAs
           __syncwarp();
-          if (++s == kStages) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
@@ -362,8 +365,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
       const Tile t = decode<MODE, kPairBM>(p, tab, w);
       const uint32_t nkb = (t.depth + 63) >> 6;
       if (nkb == 0) continue;
-      const uint32_t last = (s + nkb - 1) % kStages;
-      s = (s + nkb) % kStages;
+      const uint32_t last = (s + nkb - 1) % stages;
+      s = (s + nkb) % stages;
       if (!cleared(t, p.rows)) continue;
       if (!warp_wait(tail0 + 8 * last, (phases >> last) & 1u, abort_flag, p.status)) break;
       phases ^= 1u << last;
@@ -385,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
     const int q = warp & 3;           // the TMEM lane quadrant this warp may read
     const int part = (warp - 2) >> 2;  // which of its quadrant's two warps
     const uint32_t tempty_leader = mapa_shared(tempty0, 0);
-    uint8_t* stg = smem + kStages * kSlot + (warp - 2) * kEpiWarpBytes;
+    uint8_t* stg = smem + stages * kSlot + (warp - 2) * (epi_bytes(p) / kEpiWarps);
     uint32_t tc = 0;
     for (int w = pair; w < total; w += n_pairs) {
       const Tile t = decode<MODE, kPairBM>(p, tab, w);
@@ -395,6 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
                                : static_cast<int64_t>(t.j0);
       bool ok = true;
       const int hn = half_rows(t.n_valid);
+      const int f0 = t.f0 + static_cast<int>(rank) * kProductBM + q * 32;
       for (int h = 0; h * hn < t.n_valid; ++h) {
         const uint32_t buf = tc & 1u;
         if (!empty) {
@@ -405,8 +409,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
           tc_fence_after();
         }
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
-        store_tile<MODE, T, 32>(p, taddr, part, 2, min(hn, t.n_valid - h * hn), row0 + h * hn,
-                            t.f0 + static_cast<int>(rank) * kProductBM + q * 32, t.g, empty, stg,
+        store_tile<MODE, T, 32, kAhead>(p, taddr, part, 2, min(hn, t.n_valid - h * hn), row0 + h * hn,
+                            f0, t.g, empty, stg,
                             lane);
         if (!empty) {
           tc_fence_before();
@@ -432,9 +436,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
 }
 
 template <int MODE, int HALVES, typename T>
-cudaError_t launch(const ProductMaps& m, const ProductParams& p, int grid, cudaStream_t st) {
+cudaError_t launch(const ProductMaps& m, const ProductParams& p0, int grid, cudaStream_t st) {
+  using S = PairShape<HALVES>;
+  ProductParams p = p0;
+  // (a residual's staging takes a slot's room)
+  const int fixed = 1024 + epi_bytes(p) + S::kBarBytes + group_table_bytes(p.groups);
+  p.stages = std::min(S::kMaxStages, (227 * 1024 - fixed) / S::kSlot);
+  if (p.stages <= kLead) return cudaErrorInvalidConfiguration;
   return launch_pdl(product_pair_kernel<MODE, HALVES, T>, dim3(static_cast<unsigned>(grid)),
-                    dim3(threads_of(MODE)), PairShape<HALVES>::kSmem + group_table_bytes(p.groups), st, m.a,
+                    dim3(threads_of(MODE)), static_cast<size_t>(fixed + p.stages * S::kSlot), st, m.a,
                     m.b, p);
 }
 

@@ -25,6 +25,8 @@ __device__ __forceinline__ void pack_row(const PackParams& p, int64_t row, int l
   if (i == 3) return;
   const PackOperand& o = p.op[i];
   const int64_t g = row / o.rows;
+  // (offsets that decrease are raised by the products: no such group has rows either)
+  if (o.offsets != nullptr && o.offsets[g + 1] <= o.offsets[g]) return;
   const uint16_t* s = static_cast<const uint16_t*>(o.src) + g * o.group_stride + (row - g * o.rows) * o.ld;
   uint16_t* d = static_cast<uint16_t*>(o.dst) + row * o.ld_dst;
   constexpr int U = 8;  // loads under way per lane
@@ -56,35 +58,39 @@ int64_t pack_ctas(const PackParams& p) {
 constexpr int kGradThreads = kPackThreads;  // 8 warps: rows of a chunk are dealt to them
 constexpr int kGradWarps = kGradThreads / 32;
 constexpr int kVec = 8;                    // elements per 16-byte access
-// elements of a row per lane: one 16-byte piece, or two single ones 32 apart
-template <bool VEC>
-constexpr int kLaneCols = VEC ? kVec : 2;
+// Forms of the dz kernel: 16-byte pieces; single elements, eight per row and
+// lane 32 apart; or two, for outputs of few CTAs.
+constexpr int kFormVec = 0, kFormWide = 1, kFormNarrow = 2;
+template <int FORM>
+constexpr int kLaneCols = FORM == kFormNarrow ? 2 : kVec;
 
 template <typename T>
 struct alignas(16) Vec {
   T v[kVec];
 };
 
-// One CTA: 32 rows of one group x 256 columns (64 where the rows are not
-// aligned), or with `direct` all rows of the group.  The column sums are added
+// One CTA: `chunk` rows of one group x 256 columns (narrow form: 64), or with
+// `direct` all rows of the group.  The column sums are added
 // in fp32, per warp over its rows, then over the warps in order; direct: they
-// are the group's and go to db at once.  VEC: every row starts at a 16-byte
-// boundary and cols % 8 == 0.  Each lane keeps U rows' loads under way.  The
-// first copy_ctas CTAs copy misaligned operands instead.
-template <typename T, bool VEC>
+// are the group's and go to db at once.  The vector form needs every row at a
+// 16-byte boundary and cols % 8 == 0.  Each lane keeps U rows' loads under way.
+// The first copy_ctas CTAs copy misaligned operands instead.
+// ACT: there is an activation (dz = dout otherwise).
+template <typename T, int FORM, bool ACT>
 __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGradParams p) {
-  constexpr int E = kLaneCols<VEC>;
-  constexpr int U = VEC ? 2 : 8;
+  constexpr bool VEC = FORM == kFormVec;
+  constexpr int E = kLaneCols<FORM>;
+  constexpr int U = FORM == kFormVec ? (ACT ? 1 : 4) : FORM == kFormWide ? (ACT ? 1 : 2) : (ACT ? 4 : 8);
   constexpr int kCols = 32 * E;
   extern __shared__ int tab_mem[];
-  __shared__ float sums[kGradWarps][kCols];
+  __shared__ alignas(16) float sums[kGradWarps][kCols];
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x < p.copy_ctas) {
     pack_row(p.copies, static_cast<int64_t>(blockIdx.x) * kGradWarps + warp, lane);
     return;
   }
-  const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, kRowChunk);
+  const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, p.chunk);
   const int col_blocks = (p.cols + kCols - 1) / kCols;
   const int total = (p.direct ? p.groups : tab.block_start[p.groups]) * col_blocks;
   const T* dout = static_cast<const T*>(p.dout);
@@ -94,8 +100,8 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
     const int chunk = w / col_blocks;  // (direct: the group)
     const int c0 = (w - chunk * col_blocks) * kCols;
     const int g = p.direct ? chunk : group_of_block(tab, p.groups, chunk);
-    const int first = p.direct ? 0 : (chunk - tab.block_start[g]) * kRowChunk;
-    const int n = p.direct ? tab.count(g) : min(kRowChunk, tab.count(g) - first);
+    const int first = p.direct ? 0 : (chunk - tab.block_start[g]) * p.chunk;
+    const int n = p.direct ? tab.count(g) : min(p.chunk, tab.count(g) - first);
     const int64_t row0 = static_cast<int64_t>(tab.row0[g]) + first;
     float acc[E] = {};
     const int col = VEC ? c0 + lane * kVec : c0 + lane;
@@ -105,44 +111,57 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
         Vec<T> dv[U], zv[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          if (r + k * kGradWarps >= n) break;
-          const int64_t row = row0 + r + k * kGradWarps;
+          const int64_t row = row0 + min(r + k * kGradWarps, n - 1);
           const T* d = dout + row * p.ld_dout + col;
           const T* z = preact + row * p.ld_preact + col;
           if (VEC) {
             dv[k] = *reinterpret_cast<const Vec<T>*>(d);
-            if (preact != nullptr) zv[k] = *reinterpret_cast<const Vec<T>*>(z);
+            if (ACT) zv[k] = *reinterpret_cast<const Vec<T>*>(z);
           } else {
 #pragma unroll
             for (int i = 0; i < E; ++i)
               if (col + 32 * i < p.cols) {
                 dv[k].v[i] = d[32 * i];
-                if (preact != nullptr) zv[k].v[i] = z[32 * i];
+                if (ACT) zv[k].v[i] = z[32 * i];
               }
           }
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          if (r + k * kGradWarps >= n) break;
-          T* out = dz + (row0 + r + k * kGradWarps) * p.ld_dz + col;
+          if (r + k * kGradWarps < n) {
+            T* out = dz + (row0 + r + k * kGradWarps) * p.ld_dz + col;
+            float v[E];
 #pragma unroll
-          for (int i = 0; i < E; ++i)
-            if (VEC || col + 32 * i < p.cols) {
-              float v = to_f32<T>(dv[k].v[i]);
-              if (preact != nullptr) {
-                v *= activation_slope(to_f32<T>(zv[k].v[i]), p.act);
-                dv[k].v[i] = from_f32<T>(v);
-                if (!VEC) out[32 * i] = dv[k].v[i];
-              }
-              acc[i] += v;
+            for (int i = 0; i < E; ++i) v[i] = to_f32<T>(dv[k].v[i]);
+            if (ACT) {
+              float s[E];
+#pragma unroll
+              for (int i = 0; i < E; ++i) s[i] = to_f32<T>(zv[k].v[i]);
+              slope_all(s, p.act);
+#pragma unroll
+              for (int i = 0; i < E; ++i) v[i] *= s[i];
             }
-          if (VEC && preact != nullptr) *reinterpret_cast<Vec<T>*>(out) = dv[k];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              if (VEC || col + 32 * i < p.cols) acc[i] += v[i];
+              dv[k].v[i] = from_f32<T>(v[i]);
+              if (!VEC && dz != nullptr && col + 32 * i < p.cols) out[32 * i] = dv[k].v[i];
+            }
+            if (VEC && dz != nullptr) *reinterpret_cast<Vec<T>*>(out) = dv[k];
+          }
         }
       }
     }
     if (p.db != nullptr) {
+      if (VEC) {
 #pragma unroll
-      for (int i = 0; i < E; ++i) sums[warp][VEC ? lane * kVec + i : lane + 32 * i] = acc[i];
+        for (int i = 0; i < E; i += 4)
+          *reinterpret_cast<float4*>(&sums[warp][lane * kVec + i]) =
+              make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) sums[warp][lane + 32 * i] = acc[i];
+      }
       __syncthreads();
       const int c = c0 + threadIdx.x;
       if (threadIdx.x < kCols && c < p.cols) {
@@ -166,7 +185,7 @@ __global__ void __launch_bounds__(kGradThreads) bias_grad_kernel(const RowGradPa
   extern __shared__ int tab_mem[];
   __shared__ float sums[kGradWarps][32];
   begin_ordered(p.order);
-  const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, kRowChunk);
+  const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, p.chunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col_blocks = (p.cols + 31) / 32;
   for (int w = blockIdx.x; w < p.groups * col_blocks; w += gridDim.x) {
@@ -176,7 +195,7 @@ __global__ void __launch_bounds__(kGradThreads) bias_grad_kernel(const RowGradPa
     float v = 0.f;
     if (c < p.cols) {
       const float* s = p.partial + static_cast<int64_t>(tab.block_start[g]) * p.cols + c;
-#pragma unroll 8
+#pragma unroll 16
       for (int i = warp; i < n; i += kGradWarps) v += s[static_cast<int64_t>(i) * p.cols];
     }
     sums[warp][lane] = v;
@@ -204,14 +223,24 @@ cudaError_t row_grad(const RowGradParams& p0, int num_sms, cudaStream_t st) {
   p.copy_ctas = static_cast<unsigned>(copies);
   const size_t tab = group_table_bytes(p.groups);
   const bool vec = p.cols % kVec == 0 && rows_aligned(p.dout, p.ld_dout) &&
-                   (p.preact == nullptr ||
-                    (rows_aligned(p.preact, p.ld_preact) && rows_aligned(p.dz, p.ld_dz)));
-  const int64_t items = static_cast<int64_t>(p.direct ? p.groups
-                                                      : row_grad_chunks(p.rows, p.groups) + 1) *
-                        ((p.cols + (vec ? 32 * kVec : 64) - 1) / (vec ? 32 * kVec : 64));
-  const unsigned grid = p.copy_ctas + static_cast<unsigned>(std::min<int64_t>(items, 8 * num_sms));
-  return vec ? launch_pdl(row_grad_kernel<T, true>, dim3(grid), dim3(kGradThreads), tab, st, p)
-             : launch_pdl(row_grad_kernel<T, false>, dim3(grid), dim3(kGradThreads), tab, st, p);
+                   (p.preact == nullptr || rows_aligned(p.preact, p.ld_preact)) &&
+                   (p.dz == nullptr || rows_aligned(p.dz, p.ld_dz));
+  const int64_t units =
+      p.direct ? p.groups : static_cast<int64_t>(row_grad_chunks(p.rows, p.groups, p.chunk)) + 1;
+  auto items = [&](int form) {
+    const int cols = 32 * (form == kFormNarrow ? 2 : kVec);
+    return units * ((p.cols + cols - 1) / cols);
+  };
+  const int form = vec ? kFormVec : items(kFormWide) >= 2 * num_sms ? kFormWide : kFormNarrow;
+  const dim3 grid(p.copy_ctas + static_cast<unsigned>(std::min<int64_t>(items(form), 4 * num_sms)));
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kGradThreads), tab, st, p); };
+  if (p.preact != nullptr)
+    return form == kFormVec    ? go(row_grad_kernel<T, kFormVec, true>)
+           : form == kFormWide ? go(row_grad_kernel<T, kFormWide, true>)
+                               : go(row_grad_kernel<T, kFormNarrow, true>);
+  return form == kFormVec    ? go(row_grad_kernel<T, kFormVec, false>)
+         : form == kFormWide ? go(row_grad_kernel<T, kFormWide, false>)
+                             : go(row_grad_kernel<T, kFormNarrow, false>);
 }
 
 template <typename T>

@@ -136,6 +136,7 @@ struct PackOperand {
   int cols;
   void* dst;
   int64_t ld_dst;
+  const int* offsets;  // not nullptr: groups of no rows are left out
 };
 struct PackParams {
   PackOperand op[3];
@@ -148,25 +149,29 @@ struct RowGradParams {
   unsigned copy_ctas;  // (filled in at launch)
   const void* dout;
   int64_t ld_dout;
-  const void* preact;  // nullptr: dz = dout, not written
+  const void* preact;  // nullptr: dz = dout
   int64_t ld_preact;
-  void* dz;
+  void* dz;            // nullptr: not written
   int64_t ld_dz;
   const int* offsets;
   int groups, rows, cols;
   int act;
   void* db;            // [groups, cols] or nullptr
   // db of few rows: a CTA sums all rows of a group, in the one launch; else each
-  // CTA sums a 32-row chunk into partial [chunks, cols] and a second launch
+  // CTA sums a chunk of rows into partial [chunks, cols] and a second launch
   // adds the chunks
   bool direct;
+  int chunk;           // rows of a chunk, see row_grad_chunk
   float* partial;
 };
-constexpr int kRowChunk = 32;
 // Up to here a CTA walks its group's rows alone: 16 rows per warp at most.
 constexpr int kRowDirect = 128;
-inline size_t row_grad_chunks(int rows, int groups) {
-  return static_cast<size_t>(rows) / kRowChunk + static_cast<size_t>(groups);
+inline size_t row_grad_chunks(int rows, int groups, int chunk) {
+  return static_cast<size_t>(rows) / chunk + static_cast<size_t>(groups);
+}
+// Rows of a chunk: 128 where that makes enough work for the device, else 32.
+inline int row_grad_chunk(int rows, int groups, int cols) {
+  return row_grad_chunks(rows, groups, 128) * ((cols + 255) / 256) >= 512 ? 128 : 32;
 }
 // dz = dout * act'(preact), and db (direct) or its partial sums from dz in fp32
 cudaError_t launch_row_grad(bool bf16, const RowGradParams& p, int num_sms, cudaStream_t st);

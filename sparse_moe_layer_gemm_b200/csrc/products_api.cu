@@ -274,7 +274,8 @@ BackwardWs backward_ws(const moe_linear_config_t* c, const moe_linear_grads_t* a
   if (w.make_dz || w.copy_dout) w.total += copy_bytes(c->rows, c->out_features);
   w.partial = w.total;
   if (a->dbias != nullptr && c->rows > kRowDirect)
-    w.total += ws_round(row_grad_chunks(c->rows, G) * static_cast<size_t>(c->out_features) * 4);
+    w.total += ws_round(row_grad_chunks(c->rows, G, row_grad_chunk(c->rows, G, c->out_features)) *
+                        static_cast<size_t>(c->out_features) * 4);
   return w;
 }
 
@@ -294,7 +295,8 @@ struct Choice {
 // contraction steps per tile.
 struct Shape {
   int64_t feats, groups, mean, blocks64;
-  bool ragged, dw, act;
+  bool ragged, dw, epilogue;  // epilogue: more than a bias
+  int width;                  // of the output's accesses, see row_width
 };
 
 // Row blocks of bn rows over all groups; a ragged group fills half of its last
@@ -320,12 +322,18 @@ int pair_slot_ns(int bn) {
   return 440 + std::max(0, bn - 320) * 240 / 192;
 }
 constexpr int kPairTileNs = 500, kPairTwoTileNs = 4600;
+// Nanoseconds of a tile's epilogue, the least that a tile takes (dw of few rows
+// per group: 48 x 3588 x 744 103 us in one-CTA tiles of 128 rows, 36 x 4096 x
+// 1280 117 us in pair tiles of 256); twice that where rows are not at 16 bytes.
+int one_cta_epilogue_ns(int bn) { return 400 + 12 * bn; }
+int pair_epilogue_ns(int bn) { return 700 + 10 * bn; }
 // Joining a split tile: 1.6 us and 30 ns per row (one token 4096 -> 1280: 15.0
 // us unsplit, 11.4, 8.8, 7.9 in 2, 4, 8 parts; 128 tokens 20.0, 18.3, 13.7, 12.1).
 constexpr int kJoinNs = 1600, kJoinRowNs = 30;
 
 Choice choose(const Shape& q, int num_sms) {
   Choice best{false, 0, 1, 1};
+  const int slow = q.width == 8 ? 1 : 2;
   int64_t best_ns = 0;
   auto offer = [&](bool pair, int bn, int split, int64_t ns) {
     if (best.bn == 0 || ns < best_ns) {
@@ -341,21 +349,22 @@ Choice choose(const Shape& q, int num_sms) {
       if (split > 1 && (tiles * split > num_sms || split > q.blocks64)) break;
       const int64_t waves = (tiles + num_sms - 1) / num_sms;
       const int64_t slots = (q.blocks64 + split - 1) / split;
+      const int64_t ns = slots * one_cta_slot_ns(bn);
       offer(false, bn, split,
-            waves * slots * one_cta_slot_ns(bn) +
-                (split > 1 ? kJoinNs + kJoinRowNs * std::min<int64_t>(bn, q.mean) : 0));
+            split > 1 ? ns + kJoinNs + kJoinRowNs * std::min<int64_t>(bn, q.mean)
+                      : waves * std::max<int64_t>(ns, slow * one_cta_epilogue_ns(bn)));
     }
   }
   const int64_t f2 = (q.feats + 2 * kProductBM - 1) / (2 * kProductBM);
-  // (dw's rows per tile are multiples of 32, see product_pair.cu.  An activation
-  // costs two accumulators' poorer overlap more: gelu 4096 -> 11264 272 us with
+  // (dw's rows per tile are multiples of 32, see product_pair.cu.  A longer
+  // epilogue costs two accumulators' poorer overlap more: gelu 4096 -> 11264 272 us with
   // two, 254 with one; 251 and 242 without.)
   const int step = q.dw ? 32 : 16;
-  for (int bn = q.act ? 256 : kProductPairMaxBN; bn >= 128 && q.mean > 64; bn -= step) {
+  for (int bn = q.epilogue ? 256 : kProductPairMaxBN; bn >= 128 && q.mean > 64; bn -= step) {
     const int64_t tiles = f2 * row_blocks(q, bn);
     const int64_t waves = (tiles + num_sms / 2 - 1) / (num_sms / 2);
-    offer(true, bn, 1,
-          waves * (q.blocks64 * pair_slot_ns(bn) + (bn <= 256 ? kPairTileNs : kPairTwoTileNs)));
+    const int64_t ns = std::max<int64_t>(q.blocks64 * pair_slot_ns(bn), slow * pair_epilogue_ns(bn));
+    offer(true, bn, 1, waves * (ns + (bn <= 256 ? kPairTileNs : slow * kPairTwoTileNs)));
   }
   // a chunk's rows stay in L2 across its weight tiles: up to 32 MB of them
   // (4096 x 4096 -> 11264: 259 us with 8 blocks, 274 with 4; its dx, with rows
@@ -387,9 +396,11 @@ struct Operand {
 };
 
 // Turns *o into its copy at dst with 16-byte aligned rows.
-PackOperand aligned_copy(Operand* o, int64_t groups, int64_t rows, int64_t cols, void* dst) {
+// offsets: of weights by group, those of groups without rows stay away.
+PackOperand aligned_copy(Operand* o, int64_t groups, int64_t rows, int64_t cols, void* dst,
+                         const int32_t* offsets = nullptr) {
   const int64_t ld = padded(cols);
-  const PackOperand c{o->p, o->ld, o->gs, groups, rows, static_cast<int>(cols), dst, ld};
+  const PackOperand c{o->p, o->ld, o->gs, groups, rows, static_cast<int>(cols), dst, ld, offsets};
   *o = {dst, ld, groups > 1 || o->gs > 0 ? ld * rows : 0};
   return c;
 }
@@ -436,7 +447,7 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
   PackParams pack{};
   if (ws.copy_x) pack.op[0] = aligned_copy(&x, 1, R, K, base + ws.x);
-  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w);
+  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w, a->offsets);
   MOE_CUDA(launch_pack_rows(pack, st));
   ProductParams p{};
   p.offsets = a->offsets;
@@ -447,7 +458,10 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   int64_t n_groups, mean;
   filled(a->offsets, G, R, &n_groups, &mean);
   const Choice ch = choose({N, n_groups, mean, (K + 63) / 64, n_groups > 1, false,
-                            c->activation != MOE_ACT_NONE}, sms);
+                            c->activation != MOE_ACT_NONE || a->residual != nullptr ||
+                                a->preact != nullptr,
+                            row_width(a->out, a->ld_out, N)},
+                           sms);
   p.bn = ch.bn;
   p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
@@ -499,8 +513,8 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
   const bool joins = a->dbias != nullptr && c->rows > kRowDirect;  // a launch of its own adds db
   // copies and dz in one launch, then dx, then dw beside it, then db beside both
   PackParams pack{};
-  if (ws.copy_dout) pack.op[0] = aligned_copy(&dz, 1, R, N, base + ws.dz);
-  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w);
+  if (ws.copy_dout && !row_pass) pack.op[0] = aligned_copy(&dz, 1, R, N, base + ws.dz);
+  if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w, a->offsets);
   if (ws.copy_x) pack.op[2] = aligned_copy(&x, 1, R, K, base + ws.x);
   RowGradParams q{};
   if (!row_pass) {
@@ -511,7 +525,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     q.ld_dout = a->ld_dout;
     q.preact = a->preact;
     q.ld_preact = a->ld_preact;
-    q.dz = base + ws.dz;
+    q.dz = ws.make_dz || ws.copy_dout ? base + ws.dz : nullptr;
     q.ld_dz = padded(N);
     q.offsets = a->offsets;
     q.groups = G;
@@ -520,9 +534,10 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     q.act = c->activation;
     q.db = a->dbias;
     q.direct = a->dbias != nullptr && !joins;
+    q.chunk = row_grad_chunk(c->rows, G, c->out_features);
     q.partial = reinterpret_cast<float*>(base + ws.partial);
     MOE_CUDA(launch_row_grad(bf16, q, sms, st));
-    if (ws.make_dz) dz = {base + ws.dz, padded(N), 0};
+    if (q.dz != nullptr) dz = {base + ws.dz, padded(N), 0};
   }
   ProductParams p{};
   p.offsets = a->offsets;
@@ -539,7 +554,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     int64_t n_groups, mean;
     filled(a->offsets, G, R, &n_groups, &mean);
     const Choice ch =
-        choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false}, sms);
+        choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false, p.width_out}, sms);
     p.bn = ch.bn;
   p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
@@ -559,7 +574,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.ld_out = N;
     p.width_out = row_width(a->dw, N, N);
     const Choice ch =
-        choose({N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), false, true, false}, sms);
+        choose({N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), false, true, false, p.width_out}, sms);
     p.bn = ch.bn;
   p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
