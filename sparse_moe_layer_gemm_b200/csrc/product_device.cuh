@@ -50,8 +50,8 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 // exp(x^2) erfc(x) / t over 0 <= x <= 10 by reweighted least squares (relative
 // error 3.0e-7; evaluated in fp32 1.7e-6 for |z| < 6, from the exponent's
 // rounding).  The tail keeps its relative accuracy, where 1 + erf cancels.
-// (4096 x 4096 -> 11264: 12 us over no activation; erfcf in its place 87 us.)  gelu_tanh is 0.5 (1 + tanh u) = sigmoid(2 u), for the same
-// reason.
+// (4096 x 4096 -> 11264: 12 us over no activation; erfcf in its place 87 us.)
+// gelu_tanh is 0.5 (1 + tanh u) = sigmoid(2 u), for the same reason.
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
@@ -311,14 +311,14 @@ struct Tile {
   int depth;    // contraction length
 };
 
-// Tile w.  Inside a group, chunks of p.chunk row blocks run feature-major: a
-// weight tile's readers follow one another, and the chunk's rows stay in L2
-// across its weight tiles.
 __device__ __forceinline__ int divide(int n, const FastDiv& f) {
   return static_cast<int>((__umulhi(static_cast<uint32_t>(n), f.mul) + static_cast<uint32_t>(n)) >>
                           f.shift);
 }
 
+// Tile w.  Inside a group, chunks of p.chunk row blocks run feature-major: a
+// weight tile's readers follow one another, and the chunk's rows stay in L2
+// across its weight tiles.
 template <int MODE, int BM>
 __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable& t, int w) {
   Tile r;
@@ -360,13 +360,13 @@ __device__ __forceinline__ Tile decode(const ProductParams& p, const GroupTable&
 // ---------------------------------------------------------------- epilogue
 // An accumulator holds features on its lanes and output rows on its columns;
 // the output is row-major with features contiguous.  A warp takes 32 features
-// x 32 rows at a time (16 with a residual or pre-activation) as two 16x256b
-// tensor-memory loads per 16 rows: the values then lie
-// in the registers as 8 x 8 matrices (feature lane / 4, rows 2 (lane % 4) and
-// + 1), so after packing two rows into 32 bits one transposing stmatrix per 8
-// rows lays [row][32 features] into shared memory, from where 16-byte pieces
-// go out, 64 contiguous bytes per row.  The residual comes in the same way
-// backwards.  Against one 2-byte store per value, 4096 rows 64 -> 4096 went
+// x 32 rows at a time on pair tiles (16 on one-CTA tiles, or with a residual or
+// pre-activation) as two 16x256b tensor-memory loads per 16 rows: the values
+// then lie in the registers as 8 x 8 matrices (feature lane / 4, rows 2 (lane %
+// 4) and + 1), so after packing two rows into 32 bits one transposing stmatrix
+// per 8 rows lays [row][32 features] into shared memory, from where 16-byte
+// pieces go out (4 or 2 bytes where the rows' alignment allows no more), 64
+// contiguous bytes per row.  The residual comes in the same way backwards.  Against one 2-byte store per value, 4096 rows 64 -> 4096 went
 // from 95 to 20 us (33.5 MB written).
 constexpr int kEpiPitch = 80;                  // bytes per staged row: 64 + 16 against bank conflicts
 constexpr int kEpiChunk = 16 * kEpiPitch;      // one staged chunk

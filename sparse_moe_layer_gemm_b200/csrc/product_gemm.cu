@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
       if (split == 1) {
-        store_tile<MODE, T, 16, kAhead>(p, taddr, part, kEpiWarps / 4, t.n_valid, row0, t.f0 + q * 32, t.g, empty, stg, lane);
+        store_tile<MODE, T, 16, kAhead>(p, taddr, part, kEpiWarps / 4, t.n_valid, row0,
+                                        t.f0 + q * 32, t.g, empty, stg, lane);
         if (!empty) {
           tc_fence_before();
           __syncwarp();

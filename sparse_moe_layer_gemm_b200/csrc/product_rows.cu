@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParam
            threadIdx.x & 31);
 }
 
-// CTAs for the copies (a warp per row), and whether that is too many
+// CTAs for the copies: a warp per row
 int64_t pack_ctas(const PackParams& p) {
   int64_t rows = 0;
   for (const PackOperand& o : p.op) rows += o.groups * o.rows;
@@ -70,12 +70,12 @@ struct alignas(16) Vec {
 };
 
 // One CTA: `chunk` rows of one group x 256 columns (narrow form: 64), or with
-// `direct` all rows of the group.  The column sums are added
-// in fp32, per warp over its rows, then over the warps in order; direct: they
-// are the group's and go to db at once.  The vector form needs every row at a
-// 16-byte boundary and cols % 8 == 0.  Each lane keeps U rows' loads under way.
+// `direct` all rows of the group.  The column sums are added in fp32, per warp
+// over its rows, then over the warps in order; direct: they are the group's and
+// go to db at once.  The vector form needs every row at a 16-byte boundary and
+// cols % 8 == 0.  Each lane keeps U rows' loads under way; with an activation
+// (ACT, else dz = dout) the slope's registers leave room for one row of eight.
 // The first copy_ctas CTAs copy misaligned operands instead.
-// ACT: there is an activation (dz = dout otherwise).
 template <typename T, int FORM, bool ACT>
 __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGradParams p) {
   constexpr bool VEC = FORM == kFormVec;

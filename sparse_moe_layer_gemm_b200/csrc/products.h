@@ -39,8 +39,7 @@ inline FastDiv fast_div(uint32_t d) {
 
 // The kernels of one backward call run one after another in the stream, but
 // some do not need the one before: dw runs beside dx, the bias gradient beside
-// both.  Such a kernel (late_wait) starts
-// once every CTA of its predecessor runs, which the predecessor allows
+// both.  Such a kernel (late_wait) starts once every CTA of its predecessor runs, which the predecessor allows
 // (trigger) only after its own wait, so that all before the predecessor is
 // complete; and it waits for the predecessor before it ends, so that what
 // follows it in the stream follows both.
@@ -66,8 +65,8 @@ struct ProductParams {
   bool wide_a;
   int split;           // CTAs of a cluster sharing one tile's contraction
   // of the tile order, filled in at launch: feature tiles, row blocks per group
-  // and their rows (dw: even parts rounded up to 32), and divisions by the tiles of a group (dw) or of a row block, and by
-  // those of an ordering chunk
+  // and their rows (dw: even parts rounded up to 32), and divisions by the tiles
+  // of a group (dw) or of a row block, and by those of an ordering chunk
   int f_tiles, dw_blocks, dw_rows;
   FastDiv by_group, by_chunk;
   void* out;

@@ -43,8 +43,8 @@ int device_of(int* sms, int** status) {
   Entry& e = cache[dev];
   CUcontext ctx = nullptr;
   unsigned long long id = 0;
-  static PFN_cuCtxGetCurrent_v4000 get_ctx = nullptr;
-  static PFN_cuCtxGetId_v12000 get_id = nullptr;
+  static thread_local PFN_cuCtxGetCurrent_v4000 get_ctx = nullptr;
+  static thread_local PFN_cuCtxGetId_v12000 get_id = nullptr;
   if (get_ctx == nullptr || get_id == nullptr) {
     cudaDriverEntryPointQueryResult q;
     void *a = nullptr, *b = nullptr;
@@ -260,8 +260,8 @@ BackwardWs backward_ws(const moe_linear_config_t* c, const moe_linear_grads_t* a
   if (c->rows == 0) return w;
   const int G = std::max(1, c->groups);
   const bool products = a->dx != nullptr || a->dw != nullptr;
-  w.make_dz = c->activation != MOE_ACT_NONE;
-  w.copy_dout = !w.make_dz && products && !tma_ready(a->dout, a->ld_dout, 0);
+  w.make_dz = c->activation != MOE_ACT_NONE && products;
+  w.copy_dout = c->activation == MOE_ACT_NONE && products && !tma_ready(a->dout, a->ld_dout, 0);
   w.copy_x = a->dw != nullptr && !tma_ready(a->x, a->ld_x, 0);
   w.copy_w = a->dx != nullptr &&
              !tma_ready(a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w));
@@ -356,9 +356,9 @@ Choice choose(const Shape& q, int num_sms) {
     }
   }
   const int64_t f2 = (q.feats + 2 * kProductBM - 1) / (2 * kProductBM);
-  // (dw's rows per tile are multiples of 32, see product_pair.cu.  A longer
-  // epilogue costs two accumulators' poorer overlap more: gelu 4096 -> 11264 272 us with
-  // two, 254 with one; 251 and 242 without.)
+  // dw's rows per tile are multiples of 32, see product_pair.cu.  A longer epilogue
+  // costs two accumulators' poorer overlap more, and takes one (4096 -> 11264 with
+  // gelu: 272 us with two, 254 with one; without it 251 and 242).
   const int step = q.dw ? 32 : 16;
   for (int bn = q.epilogue ? 256 : kProductPairMaxBN; bn >= 128 && q.mean > 64; bn -= step) {
     const int64_t tiles = f2 * row_blocks(q, bn);
@@ -395,8 +395,8 @@ struct Operand {
   int64_t ld, gs;
 };
 
-// Turns *o into its copy at dst with 16-byte aligned rows.
-// offsets: of weights by group, those of groups without rows stay away.
+// Turns *o into its copy at dst with 16-byte aligned rows.  With offsets the
+// weights of groups without rows are left out.
 PackOperand aligned_copy(Operand* o, int64_t groups, int64_t rows, int64_t cols, void* dst,
                          const int32_t* offsets = nullptr) {
   const int64_t ld = padded(cols);
@@ -457,11 +457,11 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.depth = c->in_features;
   int64_t n_groups, mean;
   filled(a->offsets, G, R, &n_groups, &mean);
-  const Choice ch = choose({N, n_groups, mean, (K + 63) / 64, n_groups > 1, false,
-                            c->activation != MOE_ACT_NONE || a->residual != nullptr ||
-                                a->preact != nullptr,
-                            row_width(a->out, a->ld_out, N)},
-                           sms);
+  p.width_out = row_width(a->out, a->ld_out, N);
+  const bool epilogue =
+      c->activation != MOE_ACT_NONE || a->residual != nullptr || a->preact != nullptr;
+  const Choice ch = choose(
+      {N, n_groups, mean, (K + 63) / 64, n_groups > 1, false, epilogue, p.width_out}, sms);
   p.bn = ch.bn;
   p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
@@ -474,7 +474,6 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   p.preact = a->preact;
   p.ld_preact = a->ld_preact;
   p.act = c->activation;
-  p.width_out = row_width(a->out, a->ld_out, N);
   p.width_residual = row_width(a->residual, a->ld_residual, N);
   p.width_preact = row_width(a->preact, a->ld_preact, N);
   p.status = status;
@@ -509,7 +508,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
   Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
   Operand dz{a->dout, a->ld_dout, 0};
   const bool products = a->dx != nullptr || a->dw != nullptr;
-  const bool row_pass = (ws.make_dz && products) || a->dbias != nullptr;
+  const bool row_pass = ws.make_dz || a->dbias != nullptr;
   const bool joins = a->dbias != nullptr && c->rows > kRowDirect;  // a launch of its own adds db
   // copies and dz in one launch, then dx, then dw beside it, then db beside both
   PackParams pack{};
@@ -556,12 +555,11 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     const Choice ch =
         choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false, p.width_out}, sms);
     p.bn = ch.bn;
-  p.box_rows = box_rows(ch, c->rows);
-  p.chunk = ch.chunk;
+    p.box_rows = box_rows(ch, c->rows);
+    p.chunk = ch.chunk;
     p.split = ch.split;
     if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, kProductBM, false) ||
-        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, p.box_rows,
-                false))
+        !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, p.box_rows, false))
       return MOE_ERR_CUDA;
     p.order = {false, a->dw != nullptr || joins};
     MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
@@ -573,11 +571,11 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.out = a->dw;
     p.ld_out = N;
     p.width_out = row_width(a->dw, N, N);
-    const Choice ch =
-        choose({N, G, K, std::max<int64_t>(1, (R / G + 63) / 64), false, true, false, p.width_out}, sms);
+    const int64_t steps = std::max<int64_t>(1, (R / G + 63) / 64);
+    const Choice ch = choose({N, G, K, steps, false, true, false, p.width_out}, sms);
     p.bn = ch.bn;
-  p.box_rows = box_rows(ch, c->rows);
-  p.chunk = ch.chunk;
+    p.box_rows = box_rows(ch, c->rows);
+    p.chunk = ch.chunk;
     p.split = ch.split;
     if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 64, false) ||
         !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 64, false))

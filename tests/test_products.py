@@ -306,6 +306,88 @@ def test_linear_large(rows, k, n, act):
     check_grads(*grads, dout, x, w, pre, act)
 
 
+@gpu
+@pytest.mark.parametrize("rows,k,n", [(2100, 1000, 2307), (1500, 1001, 2600), (2048, 520, 2314)])
+def test_linear_large_odd_rows(rows, k, n):
+    """Pair tiles whose outputs, residual and pre-activation allow 2- and 4-byte
+    accesses only, at strides of their own."""
+    gen = torch.Generator().manual_seed(rows + n)
+    dt = torch.bfloat16
+    x, w = normal(gen, dt, rows, k), normal(gen, dt, k, n, std=k ** -0.5)
+    bias, res = normal(gen, dt, n), normal(gen, dt, rows, n + 3)[:, 1:n + 1]
+    out = torch.full((rows, n + 5), 7.0, dtype=dt, device="cuda")
+    pre = torch.full((rows, n + 2), 7.0, dtype=dt, device="cuda")
+    B.linear(x, w, bias, residual=res, activation="gelu", out=out[:, 2:n + 2], preact=pre[:, :n])
+    check_rows(out[:, 2:n + 2], x, w, bias, res, "gelu", pre[:, :n])
+    assert (out[:, :2] == 7).all() and (out[:, n + 2:] == 7).all() and (pre[:, n:] == 7).all()
+    dout = normal(gen, dt, rows, n)
+    grads = B.linear_backward(dout, x, w, preact=pre[:, :n], activation="gelu")
+    check_grads(*grads, dout, x, w, pre[:, :n], "gelu")
+
+
+@gpu
+@pytest.mark.parametrize("rows,k,n", [(4096, 256, 2048), (1000, 64, 520), (300, 512, 1000)])
+def test_linear_large_residual_in_place(rows, k, n):
+    """The residual is read several chunks of rows ahead: in place it gives the
+    same bits as apart from the output."""
+    gen = torch.Generator().manual_seed(rows)
+    x, w = normal(gen, torch.bfloat16, rows, k), normal(gen, torch.bfloat16, k, n, std=0.1)
+    res = normal(gen, torch.bfloat16, rows, n)
+    want = B.linear(x, w, residual=res, activation="silu")
+    check_rows(want, x, w, None, res, "silu")
+    B.linear(x, w, residual=res, activation="silu", out=res)
+    assert torch.equal(res, want)
+
+
+@gpu
+@pytest.mark.parametrize("rows", [100, 5000])
+def test_bias_gradient_alone(rows):
+    """db without dx and dw: the same bits as with them."""
+    gen = torch.Generator().manual_seed(rows)
+    dout, pre = normal(gen, torch.bfloat16, rows, 328), normal(gen, torch.bfloat16, rows, 328)
+    x, w = normal(gen, torch.bfloat16, rows, 72), normal(gen, torch.bfloat16, 72, 328)
+    for act in ("none", "gelu"):
+        kw = dict(preact=None if act == "none" else pre, activation=act)
+        db = B.linear_backward(dout, x, w, **kw)[2]
+        dx, dw, alone = B.linear_backward(dout, None, w, need_dx=False, need_dw=False, **kw)
+        assert dx is None and dw is None and torch.equal(alone, db)
+        check_grads(None, None, db, dout, x, w, pre, act)
+
+
+@gpu
+def test_backward_calls_at_once():
+    """Calls on two streams, their launches interleaved by two host threads,
+    give the bits of calls one after another."""
+    import threading
+    gen = torch.Generator().manual_seed(21)
+    sets = []
+    for rows, k, n in ((700, 513, 771), (1500, 640, 1288)):
+        x, w = normal(gen, torch.bfloat16, rows, k), normal(gen, torch.bfloat16, k, n, std=k ** -0.5)
+        dout, pre = normal(gen, torch.bfloat16, rows, n), normal(gen, torch.bfloat16, rows, n)
+        sets.append((dout, x, w, pre))
+    run = lambda s: B.linear_backward(*s[:3], preact=s[3], activation="silu")
+    want = [run(s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[i].append(run(sets[i]))
+        torch.cuda.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+    assert B.linear_device_error() == 0
+
+
 # ----------------------------------------------------------------- grouped
 def offsets_of(sizes, first=0):
     o = torch.tensor([first] + list(sizes), dtype=torch.int64).cumsum(0)
@@ -460,6 +542,30 @@ def test_grouped_weights_with_strides():
     off = offsets_of(sizes)
     for w in (both[:, :, :72], both[:, :, 72:], both[:, :, 1:73]):
         assert torch.equal(B.grouped_linear(x, off, w), B.grouped_linear(x, off, w.contiguous()))
+
+
+@gpu
+def test_grouped_odd_weights_of_empty_groups():
+    """Weights that the kernels cannot address are copied, but not those of
+    groups without rows: theirs may hold anything."""
+    gen = torch.Generator().manual_seed(22)
+    sizes = [0, 0, 17, 0, 1, 0, 140, 0]
+    k, n = 77, 131
+    x, w = normal(gen, torch.bfloat16, 158, k), normal(gen, torch.bfloat16, 8, k, n, std=0.1)
+    dout, off = normal(gen, torch.bfloat16, 158, n), offsets_of(sizes)
+    for g, c in enumerate(sizes):
+        if c == 0:
+            w[g] = math.nan
+    out = B.grouped_linear(x, off, w)
+    dx, dw, db = B.grouped_linear_backward(dout, x, off, w)
+    o = off.tolist()
+    for g, c in enumerate(sizes):
+        a, b = o[g], o[g + 1]
+        if c == 0:
+            assert (dw[g] == 0).all() and (db[g] == 0).all()
+            continue
+        check_rows(out[a:b], x[a:b], w[g], None, None, "none")
+        check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g], None, "none")
 
 
 @gpu
@@ -862,6 +968,9 @@ def test_linear_backward_workspace(lib):
     assert size(_cfg(), _grads(w=None, dx=None, dbias=None)) == 0
     with_dz = size(_cfg(activation=2), _grads(preact=OFF, ld_preact=72, dbias=None))
     assert with_dz >= 4 * 72 * 2
+    # no dz where only the bias gradient is wanted
+    assert size(_cfg(activation=2), _grads(preact=OFF, ld_preact=72, w=None, dx=None, x=None,
+                                           dw=None)) == 0
     # the column sums of many rows meet in the workspace
     c, a = _cfg(rows=200), _grads()
     assert size(c, a) >= 200 // 32 * 72 * 4
