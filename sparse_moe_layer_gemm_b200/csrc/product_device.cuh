@@ -12,10 +12,12 @@
 namespace moe {
 namespace product {
 
-// Launch order of the kernels of one call (see LaunchOrder in products.h).
+// Launch order of the kernels (see LaunchOrder in products.h).
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 __device__ __forceinline__ void begin_ordered(LaunchOrder o) {
   if (!o.late_wait) pdl_wait();
-  if (o.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void end_ordered(LaunchOrder o) {
   if (o.late_wait) pdl_wait();

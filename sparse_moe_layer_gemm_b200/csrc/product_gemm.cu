@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const GroupTable tab = build_group_table(tab_mem, p.offsets, p.groups, p.rows, p.bn);
   tc_fence_before();
   __syncthreads();
+  pdl_trigger();
   // this CTA's barriers are ready; the peers' are needed only where the partials
   // meet, so the loads do not wait for them
   if (split > 1) cluster_arrive();

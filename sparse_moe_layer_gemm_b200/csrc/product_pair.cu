@@ -140,6 +140,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers are ready before remote use
+  pdl_trigger();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = p.f_tiles * (MODE == kProductDw ? p.groups * p.dw_blocks

@@ -37,14 +37,19 @@ inline FastDiv fast_div(uint32_t d) {
   return {static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1), s, d};
 }
 
-// The kernels of one backward call run one after another in the stream, but
-// some do not need the one before: dw runs beside dx, the bias gradient beside
-// both.  Such a kernel (late_wait) starts once every CTA of its predecessor runs, which the predecessor allows
-// (trigger) only after its own wait, so that all before the predecessor is
-// complete; and it waits for the predecessor before it ends, so that what
-// follows it in the stream follows both.
+// Every kernel here lets its successor in the stream start (pdl_trigger) once it
+// has waited for its predecessor and allocated its tensor memory; the successor
+// sets itself up below it and waits for its end before it touches a tensor.
+// (An allocation of the successor's that came first would wait with it for
+// good.)  Calls in a row, 32 rows 1280 -> 4096: 7.7 us each without, 6.8 so.
+//
+// The kernels of one backward call run one after another, but some do not need
+// the one before: dw runs beside dx, the bias gradient beside both.  Such a
+// kernel (late_wait) starts when its predecessor does, so that what came before
+// the predecessor is complete, and waits for it only before it ends, so that
+// what follows it in the stream follows both.
 struct LaunchOrder {
-  bool late_wait, trigger;
+  bool late_wait;
 };
 
 struct ProductParams {

@@ -561,7 +561,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, kProductBM, false) ||
         !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, p.box_rows, false))
       return MOE_ERR_CUDA;
-    p.order = {false, a->dw != nullptr || joins};
+    p.order = {false};
     MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
   }
   if (a->dw != nullptr) {
@@ -580,11 +580,11 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 64, false) ||
         !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 64, false))
       return MOE_ERR_CUDA;
-    p.order = {a->dx != nullptr, joins};
+    p.order = {a->dx != nullptr};
     MOE_CUDA(launch_any(ch, kProductDw, bf16, m, p, sms, st));
   }
   if (joins) {
-    q.order = {products, false};
+    q.order = {products};
     MOE_CUDA(launch_bias_grad(bf16, q, sms, st));
   }
   return MOE_OK;

@@ -67,6 +67,7 @@ __device__ __forceinline__ void row_range(const SwigluParams& p, int* r0, int* r
 template <typename T, int V, int TEAM, int U, bool CLAMP>
 __global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 6) swiglu_kernel(const SwigluParams p) {
   pdl_wait();
+  pdl_trigger();
   int r0, r1;
   row_range(p, &r0, &r1);
   const float L = p.limit;
@@ -111,6 +112,7 @@ template <typename T, int V, int TEAM, int U, bool CLAMP>
 __global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 6) swiglu_backward_kernel(const SwigluParams p) {
   __shared__ float sums[kWarps];
   pdl_wait();
+  pdl_trigger();
   int r0, r1;
   row_range(p, &r0, &r1);
   const float L = p.limit;
