@@ -555,18 +555,164 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
   }
 }
 
+// ------------------------------------------------------ shared contractions
+// `split` ranks of a cluster (CTAs, or pairs of them) share a tile, each with a
+// part of its contraction.  The tile's rows, 16 at a time, are dealt to the
+// ranks; each rank sends the owners its fp32 partials of their rows, and an
+// owner adds what it gets to its own, always in the same order: the same sum on
+// every run, no workspace, no counters.  A warp sends the chunks of its
+// accumulator quadrant in the epilogue's register layout: into the slots of its
+// CTA (their MMAs are done), then by a bulk copy that counts its bytes off on
+// the owner's mbarrier, and the owner's epilogue adds them as it goes.  The code
+// runs once per CTA, so what it costs is mostly instructions fetched for the
+// first time and their latency: JOIN.
+//
+// What comes in: [source][chunk of 16 rows][quadrant] 2 KB, 1 KB per 8 rows.
+constexpr int split_chunks(int rows, int split) { return ((rows + 15) / 16 + split - 1) / split; }
+constexpr int split_bytes(int bn, int split) {
+  return split > 1 ? (split - 1) * split_chunks(bn, split) * 8192 : 0;
+}
+
+struct Split {
+  int ranks, rank;
+  int cta0, step;         // the CTA of rank k in the cluster: cta0 + step k
+  uint32_t out, in, bar;  // this CTA's slots, buffer and its mbarrier (one arrival)
+  int n_valid, per;       // rows of the tile, chunks of 16 per rank
+  __device__ __forceinline__ Split(int n_valid_, int ranks_, int rank_, int cta0_, int step_,
+                                   uint32_t out_, uint32_t in_, uint32_t bar_)
+      : ranks(ranks_), rank(rank_), cta0(cta0_), step(step_), out(out_), in(in_), bar(bar_),
+        n_valid(n_valid_), per(split_chunks(n_valid_, ranks_)) {}
+  __device__ __forceinline__ int first() const { return rank * per * 16; }
+  // rows of rank k
+  __device__ __forceinline__ int rows(int k) const {
+    return max(0, min(per * 16, n_valid - k * per * 16));
+  }
+  __device__ __forceinline__ uint32_t at(int source, int chunk, int q) const {
+    return in + ((source * per + chunk) * 4 + q) * 2048;
+  }
+};
+
+// shared memory of this CTA to one of the cluster's, in 16-byte pieces
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, uint32_t src, uint32_t bytes,
+                                                  uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// What this rank is sent, announced once.
+__device__ __forceinline__ void split_expect(const Split& x) {
+  const int mine = x.rows(x.rank);
+  if (mine > 0) mbar_arrive_expect_tx(x.bar, (x.ranks - 1) * ((mine + 7) >> 3) * 4096);
+}
+
+// Waits, with a limit, for what the others send although a wait here gave up.
+__device__ __forceinline__ void split_abandon(const ProductParams& p, const Split& x) {
+  if (x.rows(x.rank) > 0) mbar_wait(x.bar, 0, nullptr, p.status);
+}
+
+// The others' rows of this warp's 32 features (accumulator lanes of quadrant q
+// at taddr, a second part `second` columns on), every second chunk of them.
+// zeros: nothing was added up.
+__device__ __forceinline__ void split_send(const Split& x, uint32_t taddr, uint32_t second, int q,
+                                           int part, bool zeros, int lane) {
+  uint32_t at = x.out + q * 2048;
+  int n = 0;
+#pragma unroll 1
+  for (int o = 1; o < x.ranks; ++o) {
+    const int to = (x.rank + o) & (x.ranks - 1);
+    const int rows = x.rows(to);
+#pragma unroll 1
+    for (int c = 0; c < rows; c += 16, at += 8192) {
+      if ((n++ & 1) != part) continue;
+      uint32_t r[2][8], r2[2][8];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i >> 3][i & 7] = r2[i >> 3][i & 7] = 0;
+      if (!zeros) {
+        const uint32_t from = taddr + to * x.per * 16 + c;
+        tmem_ld_16x256b_x2(from, r[0]);
+        tmem_ld_16x256b_x2(from + (16u << 16), r[1]);
+        if (second != 0) {
+          tmem_ld_16x256b_x2(from + second, r2[0]);
+          tmem_ld_16x256b_x2(from + second + (16u << 16), r2[1]);
+        }
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // rows 8 (k / 2) on, features 16 (k % 2) on
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = __uint_as_float(r[k & 1][4 * (k >> 1) + e]) +
+                 __uint_as_float(r2[k & 1][4 * (k >> 1) + e]);
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + k * 512 + lane * 16),
+                     "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+                     : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (elect_one()) {
+        const uint32_t cta = x.cta0 + x.step * to;
+        bulk_copy_cluster(mapa_shared(x.at(x.rank < to ? x.rank : x.rank - 1, c >> 4, q), cta), at,
+                          rows - c > 8 ? 2048 : 1024, mapa_shared(x.bar, cta));
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// What the epilogue adds to its chunk of 16 rows at row c: nothing, or what the
+// other ranks sent, once it has come.  False if it did not come in time.
+struct Alone {
+  template <int N>
+  __device__ __forceinline__ bool operator()(float (&)[N], int) {
+    return true;
+  }
+};
+struct Joined {
+  const Split& x;
+  int q, lane;
+  volatile int* abort;
+  int* status;
+  bool waited;
+  template <int N>
+  __device__ __forceinline__ bool operator()(float (&v)[N], int c) {
+    static_assert(N == 16, "a chunk of 16 rows");
+    if (!waited && !__all_sync(0xffffffffu, mbar_wait_cluster(x.bar, 0, abort, status))) return false;
+    waited = true;
+#pragma unroll 1
+    for (int s = 0; s < x.ranks - 1; ++s) {
+      const uint32_t at = x.at(s, c >> 4, q) + lane * 16;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float u[4];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3])
+                     : "r"(at + k * 512));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * k + e] += u[e];
+      }
+    }
+    return true;
+  }
+};
+
 // One warp's part of a tile: lanes [32 q, 32 q + 32) of the accumulator at
 // taddr (quadrant and buffer included), in chunks of ROWS rows: `part`,
 // part + parts, ... below n_valid; row0 the tile's first output row, f0 the
-// warp's first feature.  zeros: the contraction was empty.  EXTRA: with a
+// warp's first feature.  zeros: the contraction was empty.  TWO: a second part
+// of the sum may lie `second` columns on (0: it does not).  EXTRA: with a
 // residual or the pre-activation.
-template <int MODE, typename T, int ROWS, bool EXTRA, int AHEAD>
-__device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t taddr, int part,
-                                             int parts, int n_valid, int64_t row0, int f0, int g,
-                                             bool zeros, uint8_t* stg, int lane) {
+// False if `join` gave up.
+template <int MODE, typename T, int ROWS, bool EXTRA, int AHEAD, bool TWO, typename Join>
+__device__ __forceinline__ bool store_chunks(const ProductParams& p, uint32_t taddr,
+                                             uint32_t second, int part, int parts, int n_valid,
+                                             int64_t row0, int f0, int g, bool zeros, uint8_t* stg,
+                                             int lane, Join join) {
   static_assert(!EXTRA || ROWS == 16, "staging");
   const int nf = p.feats - f0;
-  if (nf <= 0) return;
+  if (nf <= 0) return true;
   // matrix m: features 8 m + lane / 4
   float bias[4] = {0.f, 0.f, 0.f, 0.f};
   if (MODE == kProductForward && p.bias != nullptr) {
@@ -579,17 +725,21 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
   const uint32_t mat = smem_u32(stg) + (lane & 7) * kEpiPitch + (lane >> 3) * 16;
   T* out = static_cast<T*>(p.out) + row0 * p.ld_out + f0;
   constexpr int kB = ROWS / 16;  // 16-row loads per chunk
-  uint32_t r[2 * kB][8];
+  uint32_t r[2 * kB][8], r2[2 * kB][8];
   auto load = [&](int c) {
 #pragma unroll
     for (int b = 0; b < kB; ++b) {
       if (c + 16 * b >= n_valid) break;
       tmem_ld_16x256b_x2(taddr + c + 16 * b, r[2 * b]);
       tmem_ld_16x256b_x2(taddr + (16u << 16) + c + 16 * b, r[2 * b + 1]);
+      if (TWO && second != 0) {
+        tmem_ld_16x256b_x2(taddr + second + c + 16 * b, r2[2 * b]);
+        tmem_ld_16x256b_x2(taddr + second + (16u << 16) + c + 16 * b, r2[2 * b + 1]);
+      }
     }
   };
 #pragma unroll
-  for (int i = 0; i < 16 * kB; ++i) r[i >> 3][i & 7] = 0;
+  for (int i = 0; i < 16 * kB; ++i) r[i >> 3][i & 7] = r2[i >> 3][i & 7] = 0;
   if (!zeros) load(part * ROWS);
   // a residual of 16-byte pieces comes by asynchronous copies AHEAD chunks ahead
   // into a ring of staged chunks (4096 rows 1024 -> 4096 36 us, 31 without a
@@ -627,10 +777,19 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
+        {
+          const int a = 2 * (k >> 1) + (m >> 1), b = 4 * (k & 1) + 2 * (m & 1) + e;
           v[8 * k + 2 * m + e] =
-              __uint_as_float(r[2 * (k >> 1) + (m >> 1)][4 * (k & 1) + 2 * (m & 1) + e]) + bias[m];
+              TWO ? __uint_as_float(r[a][b]) + __uint_as_float(r2[a][b]) : __uint_as_float(r[a][b]);
+        }
     // the next chunk's load runs below this one's arithmetic and stores
     if (!zeros && c + parts * ROWS < n_valid) load(c + parts * ROWS);
+    if (!join(v, c)) {
+      if (ring) cp_async_wait<0>();
+      return false;
+    }
+#pragma unroll
+    for (int i = 0; i < 16 * kB; ++i) v[i] += bias[(i >> 1) & 3];
     auto stage = [&]() {
 #pragma unroll
       for (int k = 0; k < 2 * kB; ++k) {
@@ -672,53 +831,18 @@ __device__ __forceinline__ void store_chunks(const ProductParams& p, uint32_t ta
     }
   }
   if (ring) cp_async_wait<0>();
+  return true;
 }
 
-template <int MODE, typename T, int ROWS, int AHEAD>
-__device__ __forceinline__ void store_tile(const ProductParams& p, uint32_t taddr, int part,
-                                           int parts, int n_valid, int64_t row0, int f0, int g,
-                                           bool zeros, uint8_t* stg, int lane) {
+template <int MODE, typename T, int ROWS, int AHEAD, bool TWO, typename Join>
+__device__ __forceinline__ bool store_tile(const ProductParams& p, uint32_t taddr, uint32_t second,
+                                           int part, int parts, int n_valid, int64_t row0, int f0,
+                                           int g, bool zeros, uint8_t* stg, int lane, Join join) {
   if (MODE == kProductForward && (p.preact != nullptr || p.residual != nullptr))
-    store_chunks<MODE, T, 16, true, AHEAD>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
-  else
-    store_chunks<MODE, T, ROWS, false, AHEAD>(p, taddr, part, parts, n_valid, row0, f0, g, zeros, stg, lane);
-}
-
-// Four neighbouring features of a row of the split form.
-template <typename T>
-__device__ __forceinline__ void store4(T* at, const float (&v)[4], int n, bool vec) {
-  if (vec && n == 4) {
-    *reinterpret_cast<uint2*>(at) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) at[i] = from_f32<T>(v[i]);
-  }
-}
-
-template <int MODE, typename T>
-__device__ __forceinline__ void finish_row4(const ProductParams& p, int64_t row, int feat, int g,
-                                            float (&v)[4]) {
-  const int n = min(4, p.feats - feat);
-  if (n <= 0) return;
-  if (MODE == kProductForward) {
-    if (p.bias != nullptr) {
-      const T* b = static_cast<const T*>(p.bias) + static_cast<int64_t>(g) * p.feats + feat;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) v[i] += to_f32<T>(b[i]);
-    }
-    if (p.preact != nullptr)
-      store4<T>(static_cast<T*>(p.preact) + row * p.ld_preact + feat, v, n, p.width_preact == 8);
-    activate_all(v, p.act);
-    if (p.residual != nullptr) {
-      const T* r = static_cast<const T*>(p.residual) + row * p.ld_residual + feat;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) v[i] += to_f32<T>(r[i]);
-    }
-  }
-  store4<T>(static_cast<T*>(p.out) + row * p.ld_out + feat, v, n, p.width_out == 8);
+    return store_chunks<MODE, T, 16, true, AHEAD, TWO>(p, taddr, second, part, parts, n_valid, row0,
+                                                       f0, g, zeros, stg, lane, join);
+  return store_chunks<MODE, T, ROWS, false, AHEAD, TWO>(p, taddr, second, part, parts, n_valid, row0,
+                                                        f0, g, zeros, stg, lane, join);
 }
 
 template <typename T>

@@ -42,31 +42,25 @@ namespace {
 
 using namespace product;
 
+constexpr int kPipes = 2;     // pipelines of a CTA: a producer and an MMA warp each
 constexpr int kEpiWarps = 8;  // two per accumulator lane quadrant, on alternate chunks of rows
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kThreads = 32 * (2 * kPipes + kEpiWarps);
 constexpr int kABytes = 2 * kSubBytes;
-constexpr int kSubs = 2;  // sub-slots of 64 contraction steps per slot
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 5;  // per pipeline
+// sub-slots of 64 contraction steps per slot: what leaves room for enough slots
+constexpr int subs_of(int bn) { return bn <= 16 ? 2 : 1; }
 
 constexpr int kAhead = 2;  // residual chunks on their way
-// staging of the epilogue (a split tile's rows are stored from registers)
+// staging of the epilogue
 __host__ __device__ __forceinline__ int epi_bytes(const ProductParams& p) {
-  return p.split > 1 ? 0 : kEpiWarps * epi_warp_bytes(p, 16, kAhead);
+  return kEpiWarps * epi_warp_bytes(p, 16, kAhead);
 }
-constexpr int kBarBytes = (2 * kMaxStages + 6) * 8 + 16;
+constexpr int kBars = 2 * kPipes * kMaxStages + 4 + kPipes + 1;
+constexpr int kBarBytes = (kBars + 1) / 2 * 16 + 16;
 
 // bytes of the B operand of one slot
 __host__ __device__ constexpr int b_bytes(int mode, int bn) {
   return mode == kProductDw ? (bn + 63) / 64 * kSubBytes : bn * 128;
-}
-
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
 }
 
 // The two halves of cluster_sync_all.
@@ -84,39 +78,6 @@ __device__ __forceinline__ void my_slots(int depth, int rank, int split, int* kb
   *kb1 = static_cast<int>(static_cast<int64_t>(nkb) * (rank + 1) / split);
 }
 
-// Rows j, j + kEpiWarps, ... below j1 of a tile whose SPLIT partials lie at `mine` in
-// the cluster's CTAs: a lane adds 4 features of a row in rank order, with 16
-// of a thread's loads under way at once.
-template <int SPLIT, typename Store>
-__device__ __forceinline__ void join_rows(uint32_t mine, int j, int j1, Store store) {
-  constexpr int kRows = 16 / SPLIT;
-  uint32_t from[SPLIT];
-#pragma unroll
-  for (int k = 0; k < SPLIT; ++k) from[k] = mapa_shared(mine, k);
-  for (; j < j1; j += kEpiWarps * kRows) {
-    float4 got[kRows][SPLIT];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-#pragma unroll
-      for (int k = 0; k < SPLIT; ++k)
-        if (j + kEpiWarps * i < j1)
-          got[i][k] = ld_cluster_f32x4(from[k] + (j + kEpiWarps * i) * (kProductBM * 4));
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (j + kEpiWarps * i >= j1) break;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < SPLIT; ++k) {
-        v[0] += got[i][k].x;
-        v[1] += got[i][k].y;
-        v[2] += got[i][k].z;
-        v[3] += got[i][k].w;
-      }
-      store(j + kEpiWarps * i, v);
-    }
-  }
-}
-
 template <int MODE, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -131,16 +92,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   // what a sub-slot's loads bring: of a problem with fewer rows than the tile
   // only those (what lies behind them in shared memory reaches no kept result)
   const int load_bytes = kABytes + (kBMn ? b_bytes(MODE, p.bn) : p.box_rows * 128);
-  const int slot_bytes = kSubs * sub_bytes;
-  uint8_t* epi = smem + stages * slot_bytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + epi_bytes(p));
-  const uint32_t full0 = smem_u32(bars);
-  const uint32_t empty0 = full0 + 8 * kMaxStages;
-  const uint32_t tfull0 = empty0 + 8 * kMaxStages;
+  const int subs = p.subs;
+  const int slot_bytes = subs * sub_bytes;
+  uint8_t* epi = smem + kPipes * stages * slot_bytes;
+  uint8_t* received = epi + epi_bytes(p);  // of a split tile: what the other CTAs send
+  uint64_t* bars = reinterpret_cast<uint64_t*>(received + split_bytes(p.bn, p.split));
+  const uint32_t full_all = smem_u32(bars);  // [pipeline][kMaxStages]
+  const uint32_t empty_all = full_all + 8 * kPipes * kMaxStages;
+  const uint32_t tfull0 = empty_all + 8 * kPipes * kMaxStages;
   const uint32_t tempty0 = tfull0 + 16;
-  const uint32_t drain = tempty0 + 16;
-  const uint32_t xfull = drain + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
+  const uint32_t drain0 = tempty0 + 16;
+  const uint32_t xfull = drain0 + 8 * kPipes;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* tab_mem = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
 
@@ -150,22 +113,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster = blockIdx.x / split;
   const int clusters = gridDim.x / split;
-  // accumulator columns, two buffers (a power of two, at least 32)
+  // accumulator columns, two buffers of one accumulator per pipeline (a power of
+  // two, at least 32)
   uint32_t acc_cols = 16;
   while (acc_cols < static_cast<uint32_t>(p.bn)) acc_cols <<= 1;
-  const uint32_t tmem_cols = 2 * acc_cols;
+  const uint32_t buf_cols = kPipes * acc_cols;
+  const uint32_t tmem_cols = 2 * buf_cols;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
+    for (int s = 0; s < kPipes * kMaxStages; ++s) {
+      mbar_init(full_all + 8 * s, 1);
+      mbar_init(empty_all + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tfull0 + 8 * b, kPipes);
       mbar_init(tempty0 + 8 * b, kEpiWarps);
     }
-    mbar_init(drain, 1);
-    mbar_init(xfull, kEpiWarps * split);
+    for (int u = 0; u < kPipes; ++u) mbar_init(drain0 + 8 * u, 1);
+    mbar_init(xfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -173,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA);
     prefetch_tmap(&tmB);
   }
-  if (warp == 1) {
+  if (warp == kPipes) {
     tmem_alloc(smem_u32(tmem_slot), tmem_cols);
     tmem_relinquish();
   }
@@ -190,9 +155,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = p.f_tiles * (MODE == kProductDw ? p.groups * p.dw_blocks
                                                     : tab.block_start[p.groups]);
 
-  bool peers_ready = false;  // this warp has passed the cluster barrier above
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  // this warp has passed the cluster barrier above, and has arrived at the next
+  bool peers_ready = false, left = false;
+  if (warp < kPipes) {
+    // ------------------------------------------------------------ producers
+    const uint32_t full0 = full_all + 8 * kMaxStages * warp;
+    const uint32_t empty0 = empty_all + 8 * kMaxStages * warp;
+    const uint32_t ring = smem_u32(smem) + warp * stages * slot_bytes;
     const uint64_t pol = l2_policy_evict_normal();
     uint32_t it = 0, s = 0, ph = 0;
     bool ok = true;
@@ -200,15 +169,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
       int kb0, kb1;
       my_slots(t.depth, rank, split, &kb0, &kb1);
-      for (int kb = kb0; kb < kb1; kb += kSubs) {
+      for (int kb = kb0 + warp * subs; kb < kb1; kb += kPipes * subs) {
         if (!(ok = warp_wait(empty0 + 8 * s, ph ^ 1u, abort_flag, p.status))) break;
-        const int subs = min(kSubs, kb1 - kb);
+        const int n = min(subs, kb1 - kb);
         if (elect_one()) {
           const uint32_t bar = full0 + 8 * s;
-          mbar_arrive_expect_tx(bar, subs * load_bytes);
-          uint32_t sa = smem_u32(smem) + s * slot_bytes;
+          mbar_arrive_expect_tx(bar, n * load_bytes);
+          uint32_t sa = ring + s * slot_bytes;
           int c = t.c0 + kb * 64;
-          for (int i = 0; i < subs; ++i, sa += sub_bytes, c += 64) {
+          for (int i = 0; i < n; ++i, sa += sub_bytes, c += 64) {
             const uint32_t sb = sa + kABytes;
             if (MODE == kProductForward) {
               if (p.wide_a) {
@@ -247,11 +216,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(full0 + 8 * q, (last / stages) & 1u, nullptr, p.status);
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp < 2 * kPipes) {
+    // ------------------------------------------------------------ MMA issuers
+    const int pipe = warp - kPipes;
+    const uint32_t full0 = full_all + 8 * kMaxStages * pipe;
+    const uint32_t empty0 = empty_all + 8 * kMaxStages * pipe;
+    uint8_t* ring = smem + pipe * stages * slot_bytes;
     constexpr uint64_t kStepA = (kAMn ? 2048 : 32) >> 4;
     constexpr uint64_t kStepB = (kBMn ? 2048 : 32) >> 4;
-    const uint32_t sa0 = smem_u32(smem);
+    const uint32_t sa0 = smem_u32(ring);
     const uint64_t ad0 = kAMn ? sdesc_mn_sw128(sa0) : sdesc_k_sw<128>(sa0);
     const uint64_t bd0 = kBMn ? sdesc_mn_sw128(sa0 + kABytes) : sdesc_k_sw<128>(sa0 + kABytes);
     uint32_t s = 0, ph = 0, tc = 0;
@@ -266,18 +239,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t buf = tc & 1u;
       if (!warp_wait(tempty0 + 8 * buf, ((tc >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
       tc_fence_after();
+      ++tc;
+      const int first = kb0 + pipe * subs;
+      if (first >= kb1) {  // all of it is the first pipeline's
+        if (lane == 0) mbar_arrive(tfull0 + 8 * buf);
+        __syncwarp();
+        continue;
+      }
       any = true;
-      const uint32_t d = tmem_base + buf * acc_cols;
+      const uint32_t d = tmem_base + buf * buf_cols + pipe * acc_cols;
       uint32_t acc = 0;
-      for (int kb = kb0; kb < kb1; kb += kSubs) {
+      for (int kb = first; kb < kb1; kb += kPipes * subs) {
         if (!(ok = warp_wait(full0 + 8 * s, ph, abort_flag, p.status))) break;
         // contraction steps of this CTA that exist from here on
         const int left = min(t.depth, kb1 * 64) - kb * 64;
-        if (MODE == kProductDw && (left & 15) != 0 && left < 64 * kSubs &&
+        if (MODE == kProductDw && (left & 15) != 0 && left < 64 * subs &&
             t.c0 + t.depth < p.rows) {
           // up to the next multiple of 16 the steps are another group's rows (behind
           // the tensor's last row the load fills zeros): clear them in every box
-          uint8_t* sub = smem + s * slot_bytes + (left >> 6) * sub_bytes;
+          uint8_t* sub = ring + s * slot_bytes + (left >> 6) * sub_bytes;
           const int from = left & 63;
           const int n16 = (((from + 15) & ~15) - from) * 8;  // 16-byte pieces per box
           const int boxes = sub_bytes / kSubBytes;
@@ -293,9 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           uint64_t ad = ad0 + static_cast<uint64_t>((s * slot_bytes) >> 4);
           uint64_t bd = bd0 + static_cast<uint64_t>((s * slot_bytes) >> 4);
-          if (left > 64 * kSubs - 16) {
-#pragma unroll
-            for (int h = 0; h < kSubs; ++h) {
+          if (left > 64 * subs - 16) {
+            for (int h = 0; h < subs; ++h) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 tc_mma_bf16(d, ad + i * kStepA, bd + i * kStepB, idesc, h + i > 0 ? 1u : acc);
@@ -312,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_commit(empty0 + 8 * s);
-          if (kb + kSubs >= kb1) tc_commit(tfull0 + 8 * buf);
+          if (kb + kPipes * subs >= kb1) tc_commit(tfull0 + 8 * buf);
         }
         __syncwarp();
         acc = 1;
@@ -321,19 +300,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1u;
         }
       }
-      ++tc;
     }
     if (any) {  // no MMA may still be writing TMEM at deallocation
-      if (elect_one()) tc_commit(drain);
+      if (elect_one()) tc_commit(drain0 + 8 * pipe);
       __syncwarp();
-      mbar_wait(drain, 0, nullptr, p.status);
+      mbar_wait(drain0 + 8 * pipe, 0, nullptr, p.status);
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // the TMEM lane quadrant this warp may read
     uint32_t tc = 0;
-    const int part = (warp - 2) >> 2;  // which of its quadrant's warps
-    uint8_t* stg = epi + (warp - 2) * (epi_bytes(p) / kEpiWarps);
+    const int epi_warp = warp - 2 * kPipes;
+    const int part = epi_warp >> 2;  // which of its quadrant's warps
+    uint8_t* stg = epi + epi_warp * (epi_bytes(p) / kEpiWarps);
     for (int w = cluster; w < total; w += clusters) {
       const Tile t = decode<MODE, kProductBM>(p, tab, w);
       int kb0, kb1;
@@ -343,17 +322,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t row0 = MODE == kProductDw
                                ? static_cast<int64_t>(t.g) * p.cols + t.j0
                                : static_cast<int64_t>(t.j0);
+      const Split x(t.n_valid, split, rank, 0, 1, smem_u32(smem), smem_u32(received),
+                    xfull);
+      if (split > 1) {
+        if (epi_warp == 0 && lane == 0) split_expect(x);
+        cluster_wait();
+        peers_ready = true;
+      }
       if (!empty) {
         int go = 1;
         if (lane == 0)
           go = mbar_wait(tfull0 + 8 * buf, (tc >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, go, 0)) break;
+        if (!__shfl_sync(0xffffffffu, go, 0)) {
+          if (split > 1) split_abandon(p, x);
+          break;
+        }
         tc_fence_after();
       }
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * acc_cols;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * buf_cols;
+      // the second pipeline's accumulator, if it had a part
+      const uint32_t second = kb1 - kb0 > subs ? acc_cols : 0;
       if (split == 1) {
-        store_tile<MODE, T, 16, kAhead>(p, taddr, part, kEpiWarps / 4, t.n_valid, row0,
-                                        t.f0 + q * 32, t.g, empty, stg, lane);
+        store_tile<MODE, T, 16, kAhead, true>(p, taddr, second, part, kEpiWarps / 4, t.n_valid, row0,
+                                              t.f0 + q * 32, t.g, empty, stg, lane, Alone{});
         if (!empty) {
           tc_fence_before();
           __syncwarp();
@@ -362,53 +353,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      // one tile per cluster in this form (the launch has a cluster per tile):
-      // the partial goes where the slots were, [row][128 features]
-      float* partial = reinterpret_cast<float*>(smem) + q * 32 + lane;
-      for (int c = 32 * part; c < t.n_valid; c += 32 * (kEpiWarps / 4)) {
-        uint32_t r[2][16];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) r[i >> 4][i & 15] = 0;
-        if (!empty) {
-          tmem_ld_x16(taddr + c, r[0]);
-          if (c + 16 < t.n_valid) tmem_ld_x16(taddr + c + 16, r[1]);
-          tmem_ld_wait();
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < t.n_valid) partial[(c + i) * kProductBM] = __uint_as_float(r[i >> 4][i & 15]);
-      }
-      __syncwarp();
-      cluster_wait();
-      peers_ready = true;
-      if (lane < split) mbar_arrive_cluster(mapa_shared(xfull, lane));
-      int go = 1;
-      if (lane == 0) go = mbar_wait_cluster(xfull, 0, abort_flag, p.status) ? 1 : 0;
-      if (!__shfl_sync(0xffffffffu, go, 0)) break;
-      const int share = (t.n_valid + split - 1) / split;
-      const int j0 = rank * share, j1 = min(j0 + share, t.n_valid);
-      const uint32_t mine = smem_u32(smem) + lane * 16;
-      auto store = [&](int j, float (&v)[4]) {
-        finish_row4<MODE, T>(p, row0 + j, t.f0 + lane * 4, t.g, v);
-      };
-      if (split == 2)
-        join_rows<2>(mine, j0 + warp - 2, j1, store);
-      else if (split == 4)
-        join_rows<4>(mine, j0 + warp - 2, j1, store);
-      else
-        join_rows<8>(mine, j0 + warp - 2, j1, store);
+      // one tile per cluster in this form (the launch has a cluster per tile)
+      split_send(x, taddr, second, q, part, empty, lane);
+      if (!store_tile<MODE, T, 16, kAhead, true>(
+              p, taddr + x.first(), second, part, kEpiWarps / 4, x.rows(rank), row0 + x.first(),
+              t.f0 + q * 32, t.g, empty, stg, lane, Joined{x, q, lane, abort_flag, p.status, false}))
+        split_abandon(p, x);
+      cluster_arrive();
+      left = true;
       break;
     }
   }
 
   tc_fence_before();
   if (split > 1 && !peers_ready) cluster_wait();
+  if (split > 1 && !left) cluster_arrive();
   __syncthreads();
-  if (split > 1) cluster_sync_all();  // no CTA leaves while its peers may still reach it
-  if (warp == 1) {
+  if (warp == kPipes) {
     tc_fence_after();
     tmem_dealloc(tmem_base, tmem_cols);
   }
+  if (split > 1) cluster_wait();  // what this CTA sent has been received
   end_ordered(p.order);
 }
 
@@ -452,9 +417,10 @@ cudaError_t product_configure_device() {
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p0,
                            int num_sms, cudaStream_t st) {
   ProductParams p = p0;
-  const size_t fixed = 1024 + static_cast<size_t>(epi_bytes(p)) + kBarBytes +
-                       static_cast<size_t>(group_table_bytes(p.groups));
-  const size_t slot = kSubs * (kABytes + static_cast<size_t>(b_bytes(mode, p.bn)));
+  const size_t fixed = 1024 + static_cast<size_t>(epi_bytes(p) + split_bytes(p.bn, p.split)) +
+                       kBarBytes + static_cast<size_t>(group_table_bytes(p.groups));
+  p.subs = subs_of(p.bn);
+  const size_t slot = kPipes * p.subs * (kABytes + static_cast<size_t>(b_bytes(mode, p.bn)));
   const int64_t tiles = product_tile_order(mode, kProductBM, &p);
   if (tiles <= 0) return cudaSuccess;
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;

@@ -410,8 +410,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
           tc_fence_after();
         }
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
-        store_tile<MODE, T, 32, kAhead>(p, taddr, part, 2, min(hn, t.n_valid - h * hn),
-                                        row0 + h * hn, f0, t.g, empty, stg, lane);
+        store_tile<MODE, T, 32, kAhead, false>(p, taddr, 0, part, 2, min(hn, t.n_valid - h * hn),
+                                               row0 + h * hn, f0, t.g, empty, stg, lane, Alone{});
         if (!empty) {
           tc_fence_before();
           __syncwarp();

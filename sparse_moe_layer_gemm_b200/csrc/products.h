@@ -63,7 +63,7 @@ struct ProductParams {
   int bn;              // rows per tile, a multiple of 16
   int box_rows;        // rows of map b's box (forward, dx)
   int chunk;           // row blocks per ordering chunk
-  int stages;          // pipeline slots
+  int stages, subs;    // pipeline slots, sub-slots of 64 steps in each
   // forward: the weights' map walks 64-element chunks in a dimension of its own,
   // so that one load brings both chunks of a CTA's 128 features (else one each;
   // 4096 x 4096 -> 11264 248 us against 258; dw gained nothing from it)
