@@ -564,8 +564,10 @@ __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
 // accumulator quadrant in the epilogue's register layout: into the slots of its
 // CTA (their MMAs are done), then by a bulk copy that counts its bytes off on
 // the owner's mbarrier, and the owner's epilogue adds them as it goes.  The code
-// runs once per CTA, so what it costs is mostly instructions fetched for the
-// first time and their latency: JOIN.
+// runs once per CTA, so that most of its cost is instructions fetched for the
+// first time: 2.5 us over an unsplit tile's end for 16 rows of 4 ranks, and 5.2
+// for 128, with rows dealt by fours in loops unrolled eightfold and an epilogue
+// of its own; 1.2 and 2.0 as it is (128 rows 4096 -> 4096: 13.3 us, now 10.8).
 //
 // What comes in: [source][chunk of 16 rows][quadrant] 2 KB, 1 KB per 8 rows.
 constexpr int split_chunks(int rows, int split) { return ((rows + 15) / 16 + split - 1) / split; }

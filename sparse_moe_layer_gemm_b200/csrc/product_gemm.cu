@@ -10,22 +10,24 @@
 // the forward and dx, and x and dz the weight gradient, with no transposed
 // copies.
 //
-// Few tiles (a decode batch): `split` CTAs of a cluster share a tile, each
-// taking a part of its contraction.  Every CTA leaves its fp32 partial in its
-// own shared memory (the pipeline's, done by then); the rows of the tile are
-// dealt out to the CTAs, which read the others' partials of their rows over
-// the cluster and add them in rank order: the same sum on every run, no
-// workspace, no counters.
+// Few tiles (a decode batch, some hundred rows): `split` CTAs of a cluster share
+// a tile, each taking a part of its contraction; see Split in
+// product_device.cuh for how their partials meet.
 //
-// Roles per CTA (10 warps): warp 0 TMA producer, warp 1 tensor memory and MMA
-// issue, warps 2-9 epilogue (two per accumulator lane quadrant).  Persistent
-// over tiles w = cluster, cluster + clusters, ...; the accumulator is
-// double-buffered.  A slot holds two sub-slots of 64 steps: with few rows the
-// weights stream no faster than the issuing warps turn slots over (one tile of
-// 16 rows, 4096 steps: 30.4 us with one-lane loops, 22.5 with whole-warp loops
-// and elect, 15.0 with two sub-slots per turn).  With enough tiles HBM is the
-// bound: 512 rows over 288 groups, 4096 -> 1280, read their weights at 6.6 TB/s.
-// Every wait is bounded (moe_ptx.cuh).
+// Roles per CTA (12 warps): warps 0 and 1 TMA producers, warp 2 tensor memory,
+// warps 2 and 3 MMA issue, warps 4-11 epilogue (two per accumulator lane
+// quadrant).  Persistent over tiles w = cluster, cluster + clusters, ...; the
+// accumulators are double-buffered.  A producer and an MMA warp are a pipeline
+// of their own, with its slots and its accumulator: the first takes the even
+// slots of a tile's contraction, the second the odd ones, and the epilogue adds
+// the two sums.  With one pipeline a turn of its MMA warp (wait, issue, commit)
+// bounds small tiles, whatever their rows: 173 ns per 64 steps at 16 rows, 215 at
+// 128 (16 CTAs alone), 135 and 162 with two.  Before that, 16 rows took 475 ns
+// with one-lane loops and 350 with whole-warp loops and elect.  Up to 16 rows a
+// slot holds two sub-slots of 64 steps.  With enough tiles HBM is the bound: 512
+// rows over 288 groups, 4096 -> 1280, read their weights at 6.6 TB/s; with
+// weights in L2 its delivery, 16 bytes a picosecond (512 rows 4096 -> 4096 on 128
+// CTAs: 22 us).  Every wait is bounded (moe_ptx.cuh).
 //
 // Weight gradient: the contraction runs over the group's rows, which end
 // inside a slot; the rows behind the last one belong to the next group.  The
@@ -411,6 +413,25 @@ cudaError_t product_configure_device() {
   set(product_kernel<kProductForward, __half>);
   set(product_kernel<kProductDx, __half>);
   set(product_kernel<kProductDw, __half>);
+  return e;
+}
+
+cudaError_t product_cluster_room(int cluster, int* ctas) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 227 * 1024;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  const cudaError_t e =
+      cudaOccupancyMaxActiveClusters(&n, product_kernel<kProductForward, __nv_bfloat16>, &cfg);
+  *ctas = n * cluster;
   return e;
 }
 

@@ -8,9 +8,11 @@
 //
 // HALVES = 1: tiles of up to 256 rows, the accumulator double-buffered, so the
 // epilogue runs below the next tile's mainloop.  At 256 rows an SM's share of a
-// slot is 32 KB to load and 512 cycles of MMAs: what it draws from L2, 64 bytes
-// per cycle, and the tensor cores bound it alike (4096^3: 94 to 98 us, 23 us
-// per wave of tiles; the library's product 91 to 93).
+// slot is 32 KB to load and 512 cycles of MMAs (4096^3: 94 to 98 us, 23 us per
+// wave of tiles; the library's product 91 to 93).  Problems of few such tiles
+// share them: the pairs of a cluster each take a part of a tile's contraction
+// (Split in product_device.cuh; 512 rows 4096 -> 4096 18.6 us in 2 parts, 21.8 on
+// one-CTA tiles).
 // HALVES = 2: tiles of up to 512 rows in two even accumulators that share the
 // features' loads, a quarter less per flop.  They fill tensor memory, so the
 // epilogue overlaps the next tile only by skewing them: a tile's first kLead
@@ -52,18 +54,31 @@ constexpr int kOperand = 2 * kSubBytes;  // 128 rows or features of 64 steps
 constexpr int kAccCols = 256;
 constexpr int kLead = 2;  // slots by which the first accumulator leads at a tile's ends
 
-constexpr int kAhead = 4;  // residual chunks on their way
+// residual chunks on their way; of a split tile, where a pair has few
+constexpr int kAhead = 4, kAheadSplit = 2;
 
 template <int HALVES>
 struct PairShape {
-  static constexpr int kSlot = (1 + HALVES) * kOperand;
-  static constexpr int kMaxStages = HALVES == 1 ? 6 : 4;
-  static constexpr int kBars = 3 * kMaxStages + 5;
+  static constexpr int kMaxStages = HALVES == 1 ? 8 : 4;
+  static constexpr int kBars = 3 * kMaxStages + 6;
   static constexpr int kBarBytes = (kBars + 1) / 2 * 16 + 16;
 };
 
+// an accumulator's rows are rounded up to this for the MMA, so that each CTA
+// supplies a multiple of 8 (MN-major: of 16; a half of 8 rows more is slow to
+// read, 58 us against 45 for 4096 x 1280 gradients)
+__host__ __device__ constexpr int pair_unit(int mode) { return mode == kProductDw ? 32 : 16; }
+// bytes of a slot's rows per CTA and half, and of a slot
+__host__ __device__ constexpr int pair_half_bytes(int mode, int bn) {
+  const int rows = product_pair_half(bn, pair_unit(mode)) / 2;
+  return mode == kProductDw ? (rows + 63) / 64 * kSubBytes : rows * 128;
+}
+__host__ __device__ constexpr int pair_slot_bytes(int mode, int halves, int bn) {
+  return halves == 1 ? kOperand + pair_half_bytes(mode, bn) : 3 * kOperand;
+}
+
 __host__ __device__ __forceinline__ int epi_bytes(const ProductParams& p) {
-  return kEpiWarps * epi_warp_bytes(p, 32, kAhead);
+  return kEpiWarps * (p.split > 1 ? epi_warp_bytes(p, 16, kAheadSplit) : epi_warp_bytes(p, 32, kAhead));
 }
 
 // Whether the rows behind a dw tile's last one, up to a multiple of 16, are
@@ -72,23 +87,31 @@ __device__ __forceinline__ bool cleared(const Tile& t, int rows) {
   return (t.depth & 15) != 0 && t.c0 + t.depth < rows;
 }
 
+// Rank k of `split` takes a part of the tile's contraction.
+__device__ __forceinline__ void take_part(Tile* t, int k, int split) {
+  const int64_t nkb = (t->depth + 63) >> 6;
+  const int from = static_cast<int>(nkb * k / split) * 64;
+  const int to = min(t->depth, static_cast<int>(nkb * (k + 1) / split) * 64);
+  t->c0 += from;
+  t->depth = to - from;
+}
+
 template <int MODE, int HALVES, typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
+__global__ void __launch_bounds__(threads_of(MODE), 1)
     product_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB, const ProductParams p) {
   constexpr bool kAMn = MODE != kProductDx;
   constexpr bool kBMn = MODE == kProductDw;
-  constexpr int kSlot = PairShape<HALVES>::kSlot;
+  // (dw is not split: its contraction may be empty, and ends inside a slot)
+  constexpr bool kSplits = HALVES == 1 && MODE != kProductDw;
+  const int slot_bytes = pair_slot_bytes(MODE, HALVES, p.bn);
   const uint32_t stages = static_cast<uint32_t>(p.stages);
   constexpr int kMaxStages = PairShape<HALVES>::kMaxStages;
   constexpr int kBarBytes = PairShape<HALVES>::kBarBytes;
-  // an accumulator's rows are rounded up to kUnit for the MMA, so that each CTA
-  // supplies a multiple of 8 (MN-major: of 16; a half of 8 rows more is slow to
-  // read, 58 us against 45 for 4096 x 1280 gradients)
-  constexpr int kUnit = kBMn ? 32 : 16;
+  constexpr int kUnit = pair_unit(MODE);
   // most rows per accumulator, and this CTA's bytes of one half's rows in a slot
   const int hn_max = product_pair_half(p.bn, kUnit);
-  const uint32_t half_bytes = kBMn ? (hn_max / 2 + 63) / 64 * kSubBytes : hn_max / 2 * 128;
+  const uint32_t half_bytes = pair_half_bytes(MODE, p.bn);
   // rows per accumulator of a tile: all in one if they fit, else two even halves
   auto half_rows = [&](int n_valid) {
     return HALVES == 1 || n_valid <= hn_max ? n_valid : round_up((n_valid + 1) / 2, kUnit);
@@ -96,22 +119,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + stages * kSlot + epi_bytes(p));
+  uint8_t* epi = smem + stages * slot_bytes;
+  uint8_t* received = epi + epi_bytes(p);  // of a split tile: what the other pairs send
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(received + (kSplits ? split_bytes(p.bn, p.split) : 0));
   const uint32_t full0 = smem_u32(bars);
   const uint32_t empty0 = full0 + 8 * kMaxStages;
   const uint32_t tfull0 = empty0 + 8 * kMaxStages;
   const uint32_t tempty0 = tfull0 + 16;
   const uint32_t drain = tempty0 + 16;
   const uint32_t tail0 = drain + 8;
+  const uint32_t xfull = tail0 + 8 * kMaxStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + PairShape<HALVES>::kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* tab_mem = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kBarBytes);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = blockIdx.x >> 1;
-  const int n_pairs = gridDim.x >> 1;
+  // the pairs of a cluster share one tile
+  const int split = kSplits ? p.split : 1;
+  const uint32_t in_cluster = cluster_ctarank();
+  const uint32_t rank = in_cluster & 1u, leader = in_cluster & ~1u;
+  const int pair = blockIdx.x / (2 * split);
+  const int n_pairs = gridDim.x / (2 * split);
+  const uint16_t both = static_cast<uint16_t>(3u << leader);
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < stages; ++s) {
@@ -124,6 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
       mbar_init(tempty0 + 8 * b, 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
+    mbar_init(xfull, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -142,6 +174,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   cluster_sync_all();  // both CTAs' barriers are ready before remote use
   pdl_trigger();
   tc_fence_after();
+  auto tile_of = [&](int w) {
+    Tile t = decode<MODE, kPairBM>(p, tab, w);
+    if (kSplits && split > 1) take_part(&t, static_cast<int>(in_cluster >> 1), split);
+    return t;
+  };
   const uint32_t tmem_base = *tmem_slot;
   const int total = p.f_tiles * (MODE == kProductDw ? p.groups * p.dw_blocks
                                                     : tab.block_start[p.groups]);
@@ -149,11 +186,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const uint64_t pol = l2_policy_evict_normal();
-    const uint32_t full_leader = mapa_shared(full0, 0);
+    const uint32_t full_leader = mapa_shared(full0, leader);
     uint32_t it = 0, s = 0, ph = 0;
     bool ok = true;
     for (int w = pair; w < total && ok; w += n_pairs) {
-      const Tile t = decode<MODE, kPairBM>(p, tab, w);
+      const Tile t = tile_of(w);
       const int f = t.f0 + static_cast<int>(rank) * kProductBM;
       // this CTA's first row in each half's MMA
       int j[HALVES], halves = 0;
@@ -175,8 +212,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
             mbar_arrive_expect_tx(full0 + 8 * s, 2 * box_bytes);
             mbar_arrive(full0 + 8 * s);
           }
-          const uint32_t bar = clear ? mapa_shared(tail0 + 8 * s, rank) : full_leader + 8 * s;
-          const uint32_t sa = smem_u32(smem) + s * kSlot;
+          const uint32_t bar = clear ? mapa_shared(tail0 + 8 * s, in_cluster) : full_leader + 8 * s;
+          const uint32_t sa = smem_u32(smem) + s * slot_bytes;
           const uint32_t sb = sa + kOperand;
           if (MODE == kProductForward) {
             if (p.wide_a) {
@@ -232,11 +269,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
       bool any = false, ok = true;
       // the next tile is decoded below the current one's first MMAs
       Tile next{};
-      if (pair < total) next = decode<MODE, kPairBM>(p, tab, pair);
+      if (pair < total) next = tile_of(pair);
       for (int w = pair; w < total && ok; w += n_pairs) {
         const Tile t = next;
         auto look_ahead = [&]() {
-          if (w + n_pairs < total) next = decode<MODE, kPairBM>(p, tab, w + n_pairs);
+          if (w + n_pairs < total) next = tile_of(w + n_pairs);
         };
         const int nkb = (t.depth + 63) >> 6;
         if (nkb == 0) look_ahead();
@@ -276,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
         // the MMAs of half h on that slot, `left` contraction steps remaining
         auto issue = [&](int h, uint32_t k, int left) {
           const uint32_t q = s + k;
-          const uint64_t at = static_cast<uint64_t>((q < stages ? q : q - stages) * (kSlot >> 4));
+          const uint64_t at = static_cast<uint64_t>((q < stages ? q : q - stages) * (slot_bytes >> 4));
           const uint64_t ad = ad0 + at;
           const uint64_t bd = bd0 + at + static_cast<uint64_t>(h * (kOperand >> 4));
           const uint32_t acc = left < t.depth ? 1u : 0u;
@@ -295,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
           __syncwarp();
         };
         auto release = [&]() {
-          if (elect_one()) tc_commit_pair_mc(empty0 + 8 * s, 3);  // frees the slot in both CTAs
+          if (elect_one()) tc_commit_pair_mc(empty0 + 8 * s, both);  // frees the slot in both CTAs
           __syncwarp();
           if (++s == stages) {
             s = 0;
@@ -303,7 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
           }
         };
         auto finish = [&](int h) {
-          if (elect_one()) tc_commit_pair_mc(tfull0 + 8 * ((tc + h) & 1u), 3);
+          if (elect_one()) tc_commit_pair_mc(tfull0 + 8 * ((tc + h) & 1u), both);
           __syncwarp();
         };
         if (!(ok = acquire(0))) break;
@@ -360,10 +397,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
     }
   } else if (MODE == kProductDw && warp == 2 + kEpiWarps) {
     // ------------------------------------------------------------ clearing
-    const uint32_t full_leader = mapa_shared(full0, 0);
+    const uint32_t full_leader = mapa_shared(full0, leader);
     uint32_t s = 0, phases = 0;  // the slot, and each slot's phase of its tail barrier
     for (int w = pair; w < total; w += n_pairs) {
-      const Tile t = decode<MODE, kPairBM>(p, tab, w);
+      const Tile t = tile_of(w);
       const uint32_t nkb = (t.depth + 63) >> 6;
       if (nkb == 0) continue;
       const uint32_t last = (s + nkb - 1) % stages;
@@ -373,9 +410,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
       phases ^= 1u << last;
       const int left = t.depth & 63;
       const int n16 = (((left + 15) & ~15) - left) * 8;  // 16-byte pieces per box
-      uint8_t* slot = smem + last * kSlot;
+      uint8_t* slot = smem + last * slot_bytes;
       // (boxes that this tile did not load are cleared too, harmlessly)
-      for (int i = lane; i < n16 * (kSlot / kSubBytes); i += 32) {
+      for (int i = lane; i < n16 * (slot_bytes / kSubBytes); i += 32) {
         const int box = i / n16;
         *reinterpret_cast<uint4*>(slot + box * kSubBytes + left * 128 + (i - box * n16) * 16) =
             make_uint4(0, 0, 0, 0);
@@ -388,11 +425,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;           // the TMEM lane quadrant this warp may read
     const int part = (warp - 2) >> 2;  // which of its quadrant's two warps
-    const uint32_t tempty_leader = mapa_shared(tempty0, 0);
-    uint8_t* stg = smem + stages * kSlot + (warp - 2) * (epi_bytes(p) / kEpiWarps);
+    const uint32_t tempty_leader = mapa_shared(tempty0, leader);
+    uint8_t* stg = epi + (warp - 2) * (epi_bytes(p) / kEpiWarps);
     uint32_t tc = 0;
     for (int w = pair; w < total; w += n_pairs) {
-      const Tile t = decode<MODE, kPairBM>(p, tab, w);
+      const Tile t = tile_of(w);
       const bool empty = t.depth <= 0;
       const int64_t row0 = MODE == kProductDw
                                ? static_cast<int64_t>(t.g) * p.cols + t.j0
@@ -400,16 +437,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(MODE), 1)
       bool ok = true;
       const int hn = half_rows(t.n_valid);
       const int f0 = t.f0 + static_cast<int>(rank) * kProductBM + q * 32;
+      const Split x(t.n_valid, split, static_cast<int>(in_cluster >> 1), static_cast<int>(rank), 2,
+                    smem_u32(smem), smem_u32(received), xfull);
+      if (kSplits && split > 1 && warp == 2 && lane == 0) split_expect(x);
       for (int h = 0; h * hn < t.n_valid; ++h) {
         const uint32_t buf = tc & 1u;
         if (!empty) {
           int go = 1;
           if (lane == 0)
             go = mbar_wait(tfull0 + 8 * buf, (tc >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
-          if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) break;
+          if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) {
+            if (kSplits && split > 1) split_abandon(p, x);
+            break;
+          }
           tc_fence_after();
         }
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
+        if (kSplits && split > 1) {  // the launch has a cluster per tile
+          split_send(x, taddr, 0, q, part, empty, lane);
+          if (!store_tile<MODE, T, 16, kAheadSplit, false>(
+                  p, taddr + x.first(), 0, part, 2, x.rows(x.rank), row0 + x.first(), f0, t.g, empty,
+                  stg, lane, Joined{x, q, lane, abort_flag, p.status, false}))
+            split_abandon(p, x);
+          break;
+        }
         store_tile<MODE, T, 32, kAhead, false>(p, taddr, 0, part, 2, min(hn, t.n_valid - h * hn),
                                                row0 + h * hn, f0, t.g, empty, stg, lane, Alone{});
         if (!empty) {
@@ -439,13 +490,28 @@ template <int MODE, int HALVES, typename T>
 cudaError_t launch(const ProductMaps& m, const ProductParams& p0, int grid, cudaStream_t st) {
   using S = PairShape<HALVES>;
   ProductParams p = p0;
+  const int slot = pair_slot_bytes(MODE, HALVES, p.bn);
   // (a residual's staging takes a slot's room)
-  const int fixed = 1024 + epi_bytes(p) + S::kBarBytes + group_table_bytes(p.groups);
-  p.stages = std::min(S::kMaxStages, (227 * 1024 - fixed) / S::kSlot);
-  if (p.stages <= kLead) return cudaErrorInvalidConfiguration;
-  return launch_pdl(product_pair_kernel<MODE, HALVES, T>, dim3(static_cast<unsigned>(grid)),
-                    dim3(threads_of(MODE)), static_cast<size_t>(fixed + p.stages * S::kSlot), st, m.a,
-                    m.b, p);
+  const int fixed = 1024 + epi_bytes(p) + split_bytes(p.bn, p.split) + S::kBarBytes +
+                    group_table_bytes(p.groups);
+  p.stages = std::min(S::kMaxStages, (227 * 1024 - fixed) / slot);
+  if (p.stages < (HALVES == 1 ? 2 : kLead + 1) || (p.split > 1 && (MODE == kProductDw || HALVES > 1)))
+    return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads_of(MODE));
+  cfg.dynamicSmemBytes = static_cast<size_t>(fixed + p.stages * slot);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(2 * p.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, product_pair_kernel<MODE, HALVES, T>, m.a, m.b, p);
 }
 
 template <int MODE>
@@ -487,7 +553,8 @@ cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const
   const int64_t tiles = product_tile_order(mode, kPairBM, &p);
   if (tiles <= 0) return cudaSuccess;
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
-  const int grid = static_cast<int>(std::min<int64_t>(2 * tiles, num_sms & ~1));
+  const int grid = p.split > 1 ? static_cast<int>(2 * tiles) * p.split
+                               : static_cast<int>(std::min<int64_t>(2 * tiles, num_sms & ~1));
   if (mode == kProductForward) return launch_mode<kProductForward>(bf16, m, p, grid, st);
   if (mode == kProductDx) return launch_mode<kProductDx>(bf16, m, p, grid, st);
   return launch_mode<kProductDw>(bf16, m, p, grid, st);

@@ -60,7 +60,8 @@ constexpr int kGradThreads = kPackThreads;  // 8 warps: rows of a chunk are deal
 constexpr int kGradWarps = kGradThreads / 32;
 constexpr int kVec = 8;                    // elements per 16-byte access
 // Forms of the dz kernel: 16-byte pieces; single elements, eight per row and
-// lane 32 apart; or two, for outputs of few CTAs.
+// lane 32 apart; or two, for outputs of few CTAs whatever their alignment (77
+// rows x 776 with gelu_tanh, db alone: 9.2 us in 16-byte pieces, NARROW).
 constexpr int kFormVec = 0, kFormWide = 1, kFormNarrow = 2;
 template <int FORM>
 constexpr int kLaneCols = FORM == kFormNarrow ? 2 : kVec;
@@ -234,7 +235,9 @@ cudaError_t row_grad(const RowGradParams& p0, int num_sms, cudaStream_t st) {
     const int cols = 32 * (form == kFormNarrow ? 2 : kVec);
     return units * ((p.cols + cols - 1) / cols);
   };
-  const int form = vec ? kFormVec : items(kFormWide) >= 2 * num_sms ? kFormWide : kFormNarrow;
+  const int form = items(kFormWide) < (vec ? 1 : 2) * num_sms ? kFormNarrow
+                   : vec                                     ? kFormVec
+                                                             : kFormWide;
   const dim3 grid(p.copy_ctas + static_cast<unsigned>(std::min<int64_t>(items(form), 4 * num_sms)));
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kGradThreads), tab, st, p); };
   if (p.preact != nullptr)

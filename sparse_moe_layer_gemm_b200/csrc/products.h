@@ -68,7 +68,7 @@ struct ProductParams {
   // so that one load brings both chunks of a CTA's 128 features (else one each;
   // 4096 x 4096 -> 11264 248 us against 258; dw gained nothing from it)
   bool wide_a;
-  int split;           // CTAs of a cluster sharing one tile's contraction
+  int split;           // CTAs, or pairs, of a cluster sharing one tile's contraction
   // of the tile order, filled in at launch: feature tiles, row blocks per group
   // and their rows (dw: even parts rounded up to 32), and divisions by the tiles
   // of a group (dw) or of a row block, and by those of an ordering chunk
@@ -120,6 +120,7 @@ cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const Prod
 // to 256 with one accumulator per tile, up to 512 with two of half the rows;
 // map b's box has half of an accumulator's rows (dw: 64 steps, as for one CTA).
 constexpr int kProductPairMaxBN = 512;
+constexpr int kProductPairMaxSplit = 4;
 constexpr int product_pair_half(int bn, int unit) {
   return bn <= 256 ? bn : (bn / 2 + unit - 1) / unit * unit;
 }
@@ -128,6 +129,8 @@ cudaError_t launch_product_pair(int mode, bool bf16, const ProductMaps& m, const
 
 // one-time per-device kernel attributes (dynamic shared memory limits)
 cudaError_t product_configure_device();
+// CTAs in clusters of that size that fit the device at once, one per SM
+cudaError_t product_cluster_room(int cluster, int* ctas);
 cudaError_t product_pair_configure_device();
 
 // Row kernels (product_rows.cu).

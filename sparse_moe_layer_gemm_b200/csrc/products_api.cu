@@ -27,13 +27,20 @@ size_t ws_round(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 // The kernels' status word of each device (set by a bounded wait that gave up).
 __device__ int g_product_status;
 
-// The current device's status word and SM count, looked up once per device and
+// CTAs of clusters of 1, 2, 4 and 8 that fit the device at once, one per SM.
+struct Room {
+  int ctas[4];
+  int of(int cluster) const { return ctas[cluster >= 8 ? 3 : cluster >= 4 ? 2 : cluster - 1]; }
+  int sms() const { return ctas[0]; }
+};
+
+// The current device's status word and room, looked up once per device and
 // host thread (and again if a device reset gave the device another context),
 // with the kernels' attributes set.
-int device_of(int* sms, int** status) {
+int device_of(Room* room, int** status) {
   struct Entry {
     unsigned long long ctx = 0;
-    int sms = 0;
+    Room room{};
     int* status = nullptr;
   };
   static thread_local Entry cache[kMaxDevices];
@@ -59,15 +66,16 @@ int device_of(int* sms, int** status) {
   if (e.status == nullptr || !have || id != e.ctx) {
     void* p = nullptr;
     MOE_CUDA(cudaGetSymbolAddress(&p, g_product_status));
-    MOE_CUDA(cudaDeviceGetAttribute(&e.sms, cudaDevAttrMultiProcessorCount, dev));
+    MOE_CUDA(cudaDeviceGetAttribute(&e.room.ctas[0], cudaDevAttrMultiProcessorCount, dev));
     MOE_CUDA(product_configure_device());
+    for (int i = 1; i < 4; ++i) MOE_CUDA(product_cluster_room(1 << i, &e.room.ctas[i]));
     MOE_CUDA(product_pair_configure_device());
     e.status = static_cast<int*>(p);
     if (get_ctx(&ctx) != CUDA_SUCCESS || ctx == nullptr || get_id(ctx, &id) != CUDA_SUCCESS)
       return MOE_ERR_CUDA;
     e.ctx = id;
   }
-  *sms = e.sms;
+  *room = e.room;
   *status = e.status;
   return MOE_OK;
 }
@@ -284,6 +292,11 @@ int check_ws(const void* ws, size_t have, size_t need) {
   return ws == nullptr || !aligned(ws, kWsAlign) || have < need ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
+struct Operand {
+  const void* p;
+  int64_t ld, gs;
+};
+
 // Tile, split and order of a product.
 struct Choice {
   bool pair;
@@ -297,7 +310,11 @@ struct Shape {
   int64_t feats, groups, mean, blocks64;
   bool ragged, dw, epilogue;  // epilogue: more than a bias
   int width;                  // of the output's accesses, see row_width
+  int a_lines, b_lines;       // L2 lines per 128 bytes of an operand's rows: 1 or 2
 };
+// Rows that do not start at 128 bytes take two lines per 128 bytes (132 rows
+// 4904 -> 4624: 34 us on tiles that L2's delivery bounds, 4864 -> 4608 18).
+int lines(const Operand& o) { return aligned(o.p, 128) && o.ld % 64 == 0 ? 1 : 2; }
 
 // Row blocks of bn rows over all groups; a ragged group fills half of its last
 // one on average.
@@ -306,32 +323,52 @@ int64_t row_blocks(const Shape& q, int64_t bn) {
   return (q.groups * q.mean + bn - 1) / bn + q.groups / 2;
 }
 
-// Nanoseconds of one slot of 64 contraction steps, and of what a tile's
-// epilogue leaves uncovered, as measured on one B200 with weights from L2.
-// One CTA, 128 features x bn rows: 4096 -> 1280 (64 slots) takes 15.1, 15.6,
-// 17.0, 21.2 us at bn = 16, 32, 64, 128; 1280 -> 4096 (20 slots) 7.8 to 11.2.
-// A CTA pair, 256 features: with one accumulator 23 us per wave of 64 slots at
-// 256 rows, 21 at 224, 20 at 208 and below; with two of half the rows 43 us at
-// 512 rows, 28 at 320, and 4.6 us more per tile, since its epilogue overlaps
-// the next tile less (1280 -> 4096 at 4096 rows: 33 us with one, 42 with two;
-// 4096 -> 1280, where two accumulators make one wave of what else is two: 36 us
-// and 40 forward, 33 and 39 for dx, 35 and 44 for dw).
-int one_cta_slot_ns(int bn) { return bn <= 16 ? 166 : bn <= 32 ? 173 : bn <= 64 ? 195 : 260; }
-int pair_slot_ns(int bn) {
-  if (bn <= 256) return bn >= 240 ? 360 : bn >= 224 ? 330 : 310;
-  return 440 + std::max(0, bn - 320) * 240 / 192;
+// Nanoseconds, as measured on one B200 with weights from L2 (graphs of calls in
+// a row), of one slot of 64 contraction steps.  A few CTAs alone are bound by
+// what their MMA warps issue; many by what L2 delivers, 16 bytes a picosecond.
+// One CTA, 128 features x bn rows: 16 CTAs take 132, 151, 154, 163 ns per slot at
+// bn = 16, 32, 64, 128, 128 CTAs 160 at 16 rows, 210 at 64, 258 at 128.
+int64_t l2_ns(const Shape& q, int64_t ctas, int b_rows) {
+  return ctas * (kProductBM * q.a_lines + b_rows * q.b_lines) * 128 / 16000;
+}
+int64_t one_cta_slot_ns(const Shape& q, int bn, int64_t ctas) {
+  const int alone = bn <= 16 ? 135 : bn <= 32 ? 150 : bn <= 64 ? 154 : 162;
+  return std::max<int64_t>(alone, l2_ns(q, ctas, bn));
+}
+// A CTA pair, 256 features: 262 ns per slot up to 224 rows and 280 at 256 for a
+// few pairs; on all SMs 360 at 256 rows (23 us per wave of 64 slots), 330 at
+// 224, 310 at 208 and below.  With two accumulators of half the rows 43 us per
+// wave at 512 rows, 28 at 320, and 4.6 us more per tile, since its epilogue
+// overlaps the next tile less (1280 -> 4096 at 4096 rows: 33 us with one, 42
+// with two; 4096 -> 1280, where two accumulators make one wave of what else is
+// two: 36 us and 40 forward, 33 and 39 for dx, 35 and 44 for dw).
+int64_t pair_slot_ns(const Shape& q, int bn, int64_t ctas, int num_sms) {
+  const int64_t l2 = l2_ns(q, ctas, bn / 2);
+  if (bn > 256) return std::max<int64_t>(440 + std::max(0, bn - 320) * 240 / 192, l2);
+  const int all = bn >= 240 ? 360 : bn >= 224 ? 330 : 310;
+  return std::max<int64_t>({bn >= 240 ? 280 : 265, all * ctas / num_sms, l2});
 }
 constexpr int kPairTileNs = 500, kPairTwoTileNs = 4600;
+// What a call takes beside its slots and epilogues.
+constexpr int kOneCtaNs = 3700, kPairNs = 4500;
 // Nanoseconds of a tile's epilogue, the least that a tile takes (dw of few rows
 // per group: 48 x 3588 x 744 103 us in one-CTA tiles of 128 rows, 36 x 4096 x
 // 1280 117 us in pair tiles of 256); twice that where rows are not at 16 bytes.
-int one_cta_epilogue_ns(int bn) { return 400 + 12 * bn; }
+// With the above, intercepts over the contraction's length: 4.2 us on one-CTA
+// tiles of 16 rows, 5.3 at 128, 7.8 on pair tiles at 256.
+int one_cta_epilogue_ns(int bn) { return 500 + 13 * bn; }
 int pair_epilogue_ns(int bn) { return 700 + 10 * bn; }
-// Joining a split tile: 1.6 us and 30 ns per row (one token 4096 -> 1280: 15.0
-// us unsplit, 11.4, 8.8, 7.9 in 2, 4, 8 parts; 128 tokens 20.0, 18.3, 13.7, 12.1).
-constexpr int kJoinNs = 1600, kJoinRowNs = 30;
+// Joining a split tile (intercepts over the contraction's length: 64 rows 4096
+// features 4.6 us unsplit, 5.0 in 2 parts, 6.2 in 4; 128 rows 5.3, 6.1, 7.3; one
+// tile of 64 rows 4.2, 4.6, 5.1, 5.6 in 1, 2, 4, 8; pairs at 192 and 256 rows 1.9
+// and 2.5 in 4 parts).
+int one_cta_join_ns(int split, int rows) {
+  return split == 2 ? 500 + 5 * rows : (split == 4 ? 1000 : 1300) + 8 * rows;
+}
+int pair_join_ns(int split, int rows) { return split == 2 ? 700 + 7 * rows : 1100 + 5 * rows; }
 
-Choice choose(const Shape& q, int num_sms) {
+Choice choose(const Shape& q, const Room& room) {
+  const int num_sms = room.sms();
   Choice best{false, 0, 1, 1};
   const int slow = q.width == 8 ? 1 : 2;
   int64_t best_ns = 0;
@@ -341,18 +378,21 @@ Choice choose(const Shape& q, int num_sms) {
       best_ns = ns;
     }
   };
+  auto slots = [&](int split) { return (q.blocks64 + split - 1) / split; };
   const int64_t f1 = (q.feats + kProductBM - 1) / kProductBM;
   for (int bn = 16; bn <= kProductMaxBN; bn *= 2) {
     if (bn > 16 && bn >= 2 * q.mean) break;
+    const int rows = static_cast<int>(std::min<int64_t>(bn, q.mean));
     const int64_t tiles = f1 * row_blocks(q, bn);
     for (int split = 1; split <= kProductMaxSplit; split *= 2) {
-      if (split > 1 && (tiles * split > num_sms || split > q.blocks64)) break;
+      if (split > 1 && (tiles * split > room.of(split) || split > q.blocks64)) break;
+      const int64_t ctas = std::min<int64_t>(tiles * split, num_sms);
+      const int64_t ns = slots(split) * one_cta_slot_ns(q, bn, ctas);
+      const int64_t end = slow * one_cta_epilogue_ns(bn);
       const int64_t waves = (tiles + num_sms - 1) / num_sms;
-      const int64_t slots = (q.blocks64 + split - 1) / split;
-      const int64_t ns = slots * one_cta_slot_ns(bn);
       offer(false, bn, split,
-            split > 1 ? ns + kJoinNs + kJoinRowNs * std::min<int64_t>(bn, q.mean)
-                      : waves * std::max<int64_t>(ns, slow * one_cta_epilogue_ns(bn)));
+            kOneCtaNs + (split > 1 ? ns + one_cta_join_ns(split, rows) + end
+                                   : waves * std::max(ns, end) + std::min(ns, end)));
     }
   }
   const int64_t f2 = (q.feats + 2 * kProductBM - 1) / (2 * kProductBM);
@@ -361,10 +401,20 @@ Choice choose(const Shape& q, int num_sms) {
   // gelu: 272 us with two, 254 with one; without it 251 and 242).
   const int step = q.dw ? 32 : 16;
   for (int bn = q.epilogue ? 256 : kProductPairMaxBN; bn >= 128 && q.mean > 64; bn -= step) {
+    const int rows = static_cast<int>(std::min<int64_t>(bn, q.mean));
     const int64_t tiles = f2 * row_blocks(q, bn);
     const int64_t waves = (tiles + num_sms / 2 - 1) / (num_sms / 2);
-    const int64_t ns = std::max<int64_t>(q.blocks64 * pair_slot_ns(bn), slow * pair_epilogue_ns(bn));
-    offer(true, bn, 1, waves * (ns + (bn <= 256 ? kPairTileNs : slow * kPairTwoTileNs)));
+    for (int split = 1; split <= (q.dw || bn > 256 ? 1 : kProductPairMaxSplit); split *= 2) {
+      if (split > 1 && (2 * tiles * split > room.of(2 * split) || split > q.blocks64)) break;
+      const int64_t ctas = std::min<int64_t>(2 * tiles * split, num_sms);
+      const int64_t ns = slots(split) * pair_slot_ns(q, bn, ctas, num_sms);
+      const int64_t end = slow * pair_epilogue_ns(std::min(bn, 256));
+      const int64_t tile = bn <= 256 ? kPairTileNs : slow * kPairTwoTileNs;
+      offer(true, bn, split,
+            kPairNs + (split > 1 ? ns + pair_join_ns(split, rows) + end
+                                 : waves * (std::max(ns, bn <= 256 ? end : slow * pair_epilogue_ns(bn)) +
+                                            tile) + std::min(ns, end)));
+    }
   }
   // a chunk's rows stay in L2 across its weight tiles: up to 32 MB of them
   // (4096 x 4096 -> 11264: 259 us with 8 blocks, 274 with 4; its dx, with rows
@@ -389,11 +439,6 @@ cudaError_t launch_any(const Choice& ch, int mode, bool bf16, const ProductMaps&
   return ch.pair ? launch_product_pair(mode, bf16, m, p, sms, st)
                  : launch_product(mode, bf16, m, p, sms, st);
 }
-
-struct Operand {
-  const void* p;
-  int64_t ld, gs;
-};
 
 // Turns *o into its copy at dst with 16-byte aligned rows.  With offsets the
 // weights of groups without rows are left out.
@@ -436,9 +481,9 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   if (c->rows == 0) return MOE_OK;
   const ForwardWs ws = forward_ws(c, a);
   if ((r = check_ws(workspace, ws_bytes, ws.total)) != MOE_OK) return r;
-  int sms = 0;
+  Room room{};
   int* status = nullptr;
-  if ((r = device_of(&sms, &status)) != MOE_OK) return r;
+  if ((r = device_of(&room, &status)) != MOE_OK) return r;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   const int64_t R = c->rows, K = c->in_features, N = c->out_features;
@@ -461,7 +506,7 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   const bool epilogue =
       c->activation != MOE_ACT_NONE || a->residual != nullptr || a->preact != nullptr;
   const Choice ch = choose(
-      {N, n_groups, mean, (K + 63) / 64, n_groups > 1, false, epilogue, p.width_out}, sms);
+      {N, n_groups, mean, (K + 63) / 64, n_groups > 1, false, epilogue, p.width_out, lines(w), lines(x)}, room);
   p.bn = ch.bn;
   p.box_rows = box_rows(ch, c->rows);
   p.chunk = ch.chunk;
@@ -482,7 +527,7 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 64, p.wide_a) ||
       !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, p.box_rows, false))
     return MOE_ERR_CUDA;
-  MOE_CUDA(launch_any(ch, kProductForward, bf16, m, p, sms, st));
+  MOE_CUDA(launch_any(ch, kProductForward, bf16, m, p, room.sms(), st));
   return MOE_OK;
 }
 
@@ -501,9 +546,9 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     if (a->dbias != nullptr) MOE_CUDA(cudaMemsetAsync(a->dbias, 0, static_cast<size_t>(G) * N * 2, st));
     return MOE_OK;
   }
-  int sms = 0;
+  Room room{};
   int* status = nullptr;
-  if ((r = device_of(&sms, &status)) != MOE_OK) return r;
+  if ((r = device_of(&room, &status)) != MOE_OK) return r;
   uint8_t* base = static_cast<uint8_t*>(workspace);
   Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
   Operand dz{a->dout, a->ld_dout, 0};
@@ -535,7 +580,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     q.direct = a->dbias != nullptr && !joins;
     q.chunk = row_grad_chunk(c->rows, G, c->out_features);
     q.partial = reinterpret_cast<float*>(base + ws.partial);
-    MOE_CUDA(launch_row_grad(bf16, q, sms, st));
+    MOE_CUDA(launch_row_grad(bf16, q, room.sms(), st));
     if (q.dz != nullptr) dz = {base + ws.dz, padded(N), 0};
   }
   ProductParams p{};
@@ -553,7 +598,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     int64_t n_groups, mean;
     filled(a->offsets, G, R, &n_groups, &mean);
     const Choice ch =
-        choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false, p.width_out}, sms);
+        choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false, p.width_out, lines(w), lines(dz)}, room);
     p.bn = ch.bn;
     p.box_rows = box_rows(ch, c->rows);
     p.chunk = ch.chunk;
@@ -562,7 +607,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
         !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, p.box_rows, false))
       return MOE_ERR_CUDA;
     p.order = {false};
-    MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, sms, st));
+    MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, room.sms(), st));
   }
   if (a->dw != nullptr) {
     p.feats = c->out_features;
@@ -572,7 +617,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     p.ld_out = N;
     p.width_out = row_width(a->dw, N, N);
     const int64_t steps = std::max<int64_t>(1, (R / G + 63) / 64);
-    const Choice ch = choose({N, G, K, steps, false, true, false, p.width_out}, sms);
+    const Choice ch = choose({N, G, K, steps, false, true, false, p.width_out, lines(dz), lines(x)}, room);
     p.bn = ch.bn;
     p.box_rows = box_rows(ch, c->rows);
     p.chunk = ch.chunk;
@@ -581,20 +626,20 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
         !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 64, false))
       return MOE_ERR_CUDA;
     p.order = {a->dx != nullptr};
-    MOE_CUDA(launch_any(ch, kProductDw, bf16, m, p, sms, st));
+    MOE_CUDA(launch_any(ch, kProductDw, bf16, m, p, room.sms(), st));
   }
   if (joins) {
     q.order = {products};
-    MOE_CUDA(launch_bias_grad(bf16, q, sms, st));
+    MOE_CUDA(launch_bias_grad(bf16, q, room.sms(), st));
   }
   return MOE_OK;
 }
 
 int moe_linear_get_device_error(int* device_err) {
-  int sms = 0;
+  Room room{};
   int* status = nullptr;
   if (device_err == nullptr) return MOE_ERR_INVALID_ARG;
-  const int r = device_of(&sms, &status);
+  const int r = device_of(&room, &status);
   if (r != MOE_OK) return r;
   MOE_CUDA(cudaDeviceSynchronize());
   MOE_CUDA(cudaMemcpy(device_err, status, sizeof(int), cudaMemcpyDeviceToHost));
