@@ -61,7 +61,7 @@ constexpr int kGradWarps = kGradThreads / 32;
 constexpr int kVec = 8;                    // elements per 16-byte access
 // Forms of the dz kernel: 16-byte pieces; single elements, eight per row and
 // lane 32 apart; or two, for outputs of few CTAs whatever their alignment (77
-// rows x 776 with gelu_tanh, db alone: 9.2 us in 16-byte pieces, NARROW).
+// rows x 776 with gelu_tanh, db alone: 9.2 us in 16-byte pieces, 4.8 so).
 constexpr int kFormVec = 0, kFormWide = 1, kFormNarrow = 2;
 template <int FORM>
 constexpr int kLaneCols = FORM == kFormNarrow ? 2 : kVec;
