@@ -768,6 +768,11 @@ def _need_rows(t: torch.Tensor, name: str, like: torch.Tensor, rows: int, cols: 
     return ld
 
 
+def _new_rows(like: torch.Tensor, rows: int, cols: int):
+    """A new [rows, cols] tensor of like's type and device, and its row stride."""
+    return like.new_empty(rows, cols), cols if rows > 1 else (cols + 7) // 8 * 8
+
+
 def _need_vec(t: torch.Tensor, name: str, like: torch.Tensor, shape, dtype=None):
     dtype = like.dtype if dtype is None else dtype
     if t.shape != shape or t.dtype is not dtype or t.get_device() != like.get_device() or \
@@ -828,8 +833,9 @@ def _linear(x, offsets, w, bias, residual, activation, out, preact, stream):
             return _linear(x, offsets, w, bias, residual, activation, out, preact, None)
     st = torch._C._cuda_getCurrentRawStream(x.get_device())
     if out is None:
-        out = x.new_empty((R, N))
-    ld_out = _need_rows(out, "out", x, R, N)
+        out, ld_out = _new_rows(x, R, N)
+    else:
+        ld_out = _need_rows(out, "out", x, R, N)
     args = moe_linear_args_t(x.data_ptr(), ld_x, None if offsets is None else offsets.data_ptr(),
                              w.data_ptr(), ld_w, gs, None if bias is None else bias.data_ptr(),
                              None if residual is None else residual.data_ptr(), ld_res,
@@ -890,17 +896,24 @@ def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream
         with _Elsewhere(dout, stream):
             return _linear_backward(dout, x, offsets, w, preact, activation, need, into, None)
     st = torch._C._cuda_getCurrentRawStream(dout.get_device())
-    if need[0] and dx is None:
-        dx = dout.new_empty((R, K)) if x is None else torch.empty_like(x)
-    if need[1] and dw is None:
-        dw = torch.empty_like(w) if w.is_contiguous() else dout.new_empty(w.shape)
-    if need[2] and db is None:
-        db = dout.new_empty((G, N) if G else (N,))
-    dx, dw, db = (t if n else None for t, n in zip((dx, dw, db), need))
-    ld_dx = _need_rows(dx, "dx", dout, R, K) if dx is not None else 0
-    if dw is not None:
+    ld_dx = 0
+    if not need[0]:
+        dx = None
+    elif dx is None:
+        dx, ld_dx = _new_rows(dout, R, K)
+    else:
+        ld_dx = _need_rows(dx, "dx", dout, R, K)
+    if not need[1]:
+        dw = None
+    elif dw is None:
+        dw = dout.new_empty(G, K, N) if G else dout.new_empty(K, N)
+    else:
         _need_vec(dw, "dw", dout, w.shape)
-    if db is not None:
+    if not need[2]:
+        db = None
+    elif db is None:
+        db = dout.new_empty(G, N) if G else dout.new_empty(N)
+    else:
         _need_vec(db, "db", dout, (G, N) if G else (N,))
     grads = moe_linear_grads_t(dout.data_ptr(), ld_dout, _ptr(x) if need[1] else None, ld_x,
                                _ptr(offsets), w.data_ptr() if need[0] else None, ld_w, gs,
@@ -979,8 +992,9 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, scale: Optional[torch.Tensor] =
         with _Elsewhere(gate, stream):
             return swiglu(gate, up, scale, limit=limit, offsets=offsets, out=out)
     if out is None:
-        out = gate.new_empty((R, W))
-    ldo = _need_rows(out, "out", gate, R, W)
+        out, ldo = _new_rows(gate, R, W)
+    else:
+        ldo = _need_rows(out, "out", gate, R, W)
     status = load_library().moe_swiglu(
         cfg, gate.data_ptr(), ldg, up.data_ptr(), ldu,
         None if scale is None else scale.data_ptr(),
@@ -1007,14 +1021,17 @@ def swiglu_backward(dout: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
             return swiglu_backward(dout, gate, up, scale, limit=limit, offsets=offsets,
                                    dgate=dgate, dup=dup, dscale=dscale)
     if dgate is None:
-        dgate = gate.new_empty((R, W))
+        dgate, ldg2 = _new_rows(gate, R, W)
+    else:
+        ldg2 = _need_rows(dgate, "dgate", gate, R, W)
     if dup is None:
-        dup = gate.new_empty((R, W))
-    if dscale is None and scale is not None:
-        dscale = scale.new_empty((R,))
+        dup, ldu2 = _new_rows(gate, R, W)
+    else:
+        ldu2 = _need_rows(dup, "dup", gate, R, W)
     if dscale is not None:
         _need_vec(dscale, "dscale", gate, (R,), torch.float32)
-    ldg2, ldu2 = _need_rows(dgate, "dgate", gate, R, W), _need_rows(dup, "dup", gate, R, W)
+    elif scale is not None:
+        dscale = scale.new_empty(R)
     _check(load_library().moe_swiglu_backward(
         cfg, dout.data_ptr(), ldd, gate.data_ptr(), ldg, up.data_ptr(), ldu, _ptr(scale),
         _ptr(offsets), dgate.data_ptr(), ldg2, dup.data_ptr(), ldu2, _ptr(dscale),
