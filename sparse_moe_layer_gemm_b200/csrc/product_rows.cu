@@ -43,7 +43,6 @@ __device__ __forceinline__ void pack_row(const PackParams& p, int64_t row, int l
 
 __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const PackParams p) {
   pdl_wait();
-  pdl_trigger();
   pack_row(p, static_cast<int64_t>(blockIdx.x) * (kPackThreads / 32) + (threadIdx.x >> 5),
            threadIdx.x & 31);
 }
@@ -87,7 +86,6 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
   extern __shared__ int tab_mem[];
   __shared__ alignas(16) float sums[kGradWarps][kCols];
   pdl_wait();
-  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x < p.copy_ctas) {
     pack_row(p.copies, static_cast<int64_t>(blockIdx.x) * kGradWarps + warp, lane);
