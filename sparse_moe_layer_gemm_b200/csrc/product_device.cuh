@@ -574,6 +574,11 @@ constexpr int split_chunks(int rows, int split) { return ((rows + 15) / 16 + spl
 constexpr int split_bytes(int bn, int split) {
   return split > 1 ? (split - 1) * split_chunks(bn, split) * 8192 : 0;
 }
+// What goes out: the most chunks of other ranks, which the slots have to hold.
+constexpr int split_out_bytes(int bn, int split) {
+  const int others = (split - 1) * split_chunks(bn, split), all = (bn + 15) / 16;
+  return split > 1 ? (others < all ? others : all) * 8192 : 0;
+}
 
 struct Split {
   int ranks, rank;
@@ -609,8 +614,9 @@ __device__ __forceinline__ void split_expect(const Split& x) {
   if (mine > 0) mbar_arrive_expect_tx(x.bar, (x.ranks - 1) * ((mine + 7) >> 3) * 4096);
 }
 
-// Waits, with a limit, for what the others send although a wait here gave up.
-__device__ __forceinline__ void split_abandon(const ProductParams& p, const Split& x) {
+// Waits, with a limit, for all that the others send: no CTA may end before, not
+// even one whose waits gave up or whose features all lie behind the last one.
+__device__ __forceinline__ void split_settle(const ProductParams& p, const Split& x) {
   if (x.rows(x.rank) > 0) mbar_wait(x.bar, 0, nullptr, p.status);
 }
 

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0)
           go = mbar_wait(tfull0 + 8 * buf, (tc >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, go, 0)) {
-          if (split > 1) split_abandon(p, x);
+          if (split > 1) split_settle(p, x);
           break;
         }
         tc_fence_after();
@@ -357,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // one tile per cluster in this form (the launch has a cluster per tile)
       split_send(x, taddr, second, q, part, empty, lane);
-      if (!store_tile<MODE, T, 16, kAhead, true>(
-              p, taddr + x.first(), second, part, kEpiWarps / 4, x.rows(rank), row0 + x.first(),
-              t.f0 + q * 32, t.g, empty, stg, lane, Joined{x, q, lane, abort_flag, p.status, false}))
-        split_abandon(p, x);
+      store_tile<MODE, T, 16, kAhead, true>(
+          p, taddr + x.first(), second, part, kEpiWarps / 4, x.rows(rank), row0 + x.first(),
+          t.f0 + q * 32, t.g, empty, stg, lane, Joined{x, q, lane, abort_flag, p.status, false});
+      split_settle(p, x);
       cluster_arrive();
       left = true;
       break;
@@ -447,6 +447,8 @@ cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const Prod
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
   p.stages = static_cast<int>(
       std::min<size_t>(kMaxStages, (static_cast<size_t>(227) * 1024 - fixed) / slot));
+  if (p.stages * slot < static_cast<size_t>(split_out_bytes(p.bn, p.split)))
+    return cudaErrorInvalidConfiguration;
   const size_t smem = fixed + p.stages * slot;
   const int grid =
       p.split > 1 ? static_cast<int>(tiles) * p.split : static_cast<int>(std::min<int64_t>(tiles, num_sms));

@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
           if (lane == 0)
             go = mbar_wait(tfull0 + 8 * buf, (tc >> 1) & 1u, abort_flag, p.status) ? 1 : 0;
           if (!(ok = __shfl_sync(0xffffffffu, go, 0) != 0)) {
-            if (SPLITS) split_abandon(p, x);
+            if (SPLITS) split_settle(p, x);
             break;
           }
           tc_fence_after();
@@ -458,10 +458,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
         if (SPLITS) {  // the launch has a cluster per tile
           split_send(x, taddr, 0, q, part, empty, lane);
-          if (!store_tile<MODE, T, 16, kAheadSplit, false>(
-                  p, taddr + x.first(), 0, part, 2, x.rows(x.rank), row0 + x.first(), f0, t.g, empty,
-                  stg, lane, Joined{x, q, lane, abort_flag, p.status, false}))
-            split_abandon(p, x);
+          store_tile<MODE, T, 16, kAheadSplit, false>(
+              p, taddr + x.first(), 0, part, 2, x.rows(x.rank), row0 + x.first(), f0, t.g, empty, stg,
+              lane, Joined{x, q, lane, abort_flag, p.status, false});
+          split_settle(p, x);
           break;
         }
         store_tile<MODE, T, 32, kAhead, false>(p, taddr, 0, part, 2, min(hn, t.n_valid - h * hn),
@@ -498,7 +498,9 @@ cudaError_t launch(const ProductMaps& m, const ProductParams& p0, int grid, cuda
   const int fixed = 1024 + epi_bytes(p) + split_bytes(p.bn, p.split) + S::kBarBytes +
                     group_table_bytes(p.groups);
   p.stages = std::min(S::kMaxStages, (227 * 1024 - fixed) / slot);
-  if (p.stages < (HALVES == 1 ? 2 : kLead + 1)) return cudaErrorInvalidConfiguration;
+  if (p.stages < (HALVES == 1 ? 2 : kLead + 1) ||
+      p.stages * slot < split_out_bytes(p.bn, p.split))
+    return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(threads_of(MODE));

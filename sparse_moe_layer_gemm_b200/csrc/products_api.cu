@@ -405,7 +405,10 @@ Choice choose(const Shape& q, const Room& room) {
     const int64_t tiles = f2 * row_blocks(q, bn);
     const int64_t waves = (tiles + num_sms / 2 - 1) / (num_sms / 2);
     for (int split = 1; split <= (q.dw || bn > 256 ? 1 : kProductPairMaxSplit); split *= 2) {
-      if (split > 1 && (2 * tiles * split > room.of(2 * split) || split > q.blocks64)) break;
+      // (an uneven deal of the chunks of 16 rows sends more than the slots hold)
+      if (split > 1 && (2 * tiles * split > room.of(2 * split) || split > q.blocks64 ||
+                        bn % (16 * split) != 0))
+        break;
       const int64_t ctas = std::min<int64_t>(2 * tiles * split, num_sms);
       const int64_t ns = slots(split) * pair_slot_ns(q, bn, ctas, num_sms);
       const int64_t end = slow * pair_epilogue_ns(std::min(bn, 256));

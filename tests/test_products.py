@@ -5,7 +5,7 @@ Tolerances, with u the half step of the 16-bit type (eps / 2):
   - an output is rounded once: u |value|;
   - a sum of K products on the tensor cores adds at most one truncation of
     2^-23 of the running sum (at most S = sum |a| |b|) per 16 products, and
-    one rounding of 2^-24 S per joined part (at most 8 of them) and for the
+    one rounding of 2^-24 S per joined part (at most 16 of them) and for the
     bias and the residual: (K / 16 + 10) 2^-23 S;
   - the activations have slopes up to 1.13 and are computed to a few fp32
     ulps: 2^-20 of |z| + |act(z)|;
@@ -304,6 +304,68 @@ def test_linear_large(rows, k, n, act):
     dout = normal(gen, dt, rows, n)
     grads = B.linear_backward(dout, x, w, preact=None if act == "none" else pre, activation=act)
     check_grads(*grads, dout, x, w, pre, act)
+
+
+# few tiles and a long contraction: clusters of CTAs or of CTA pairs share tiles
+SHARED = [(7, 4096, 640), (16, 8192, 128), (40, 2056, 1111), (130, 4096, 512), (250, 4096, 4096),
+          (384, 3000, 4096), (510, 4096, 1280), (700, 4104, 1288), (500, 4001, 515)]
+
+
+@gpu
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("rows,k,n", SHARED)
+def test_linear_shared_tiles(rows, k, n, act):
+    gen = torch.Generator().manual_seed(rows)
+    dt = torch.float16 if rows % 2 else torch.bfloat16
+    x, w = normal(gen, dt, rows, k), normal(gen, dt, k, n, std=k ** -0.5)
+    bias, res = normal(gen, dt, n), normal(gen, dt, rows, n)
+    pre = torch.empty(rows, n, dtype=dt, device="cuda")
+    kw = dict(residual=res, activation=act)
+    out = B.linear(x, w, bias, preact=pre, **kw)
+    check_rows(out, x, w, bias, res, act, pre)
+    plain = B.linear(x, w)
+    check_rows(plain, x, w, None, None, "none")
+    dout = normal(gen, dt, rows, n)
+    bkw = dict(preact=None if act == "none" else pre, activation=act)
+    grads = B.linear_backward(dout, x, w, **bkw)
+    check_grads(*grads, dout, x, w, pre, act)
+    for _ in range(3):  # the partials meet in one order
+        assert torch.equal(out, B.linear(x, w, bias, **kw)) and torch.equal(plain, B.linear(x, w))
+        assert all(torch.equal(a, b) for a, b in zip(grads, B.linear_backward(dout, x, w, **bkw)))
+    inplace = res.clone()
+    B.linear(x, w, bias, residual=inplace, activation=act, out=inplace)
+    assert torch.equal(inplace, out)
+    assert B.linear_device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("sizes,k,n", [([100, 0, 37], 4096, 256), ([3, 1], 4096, 520),
+                                       ([260, 130, 0, 9], 2048, 384), ([1, 0, 0], 8192, 72)])
+def test_grouped_shared_tiles(sizes, k, n):
+    """Shared tiles of ragged groups between rows that hold NaN."""
+    gen = torch.Generator().manual_seed(k + n)
+    G, first, behind = len(sizes), 3, 21
+    rows = first + sum(sizes) + behind
+    x, dout = normal(gen, torch.bfloat16, rows, k), normal(gen, torch.bfloat16, rows, n)
+    w, bias = normal(gen, torch.bfloat16, G, k, n, std=k ** -0.5), normal(gen, torch.bfloat16, G, n)
+    for t in (x, dout):
+        t[:first] = math.nan
+        t[rows - behind:] = math.inf
+    off = offsets_of(sizes, first)
+    out = torch.full((rows, n), 3.0, dtype=x.dtype, device="cuda")
+    dx = torch.full((rows, k), 3.0, dtype=x.dtype, device="cuda")
+    B.grouped_linear(x, off, w, bias, activation="silu", out=out)
+    _, dw, db = B.grouped_linear_backward(dout, x, off, w, dx=dx)
+    for t in (out, dx):
+        assert (t[:first] == 3).all() and (t[rows - behind:] == 3).all()
+    o = off.tolist()
+    for g in range(G):
+        a, b = o[g], o[g + 1]
+        if a == b:
+            assert (dw[g] == 0).all() and (db[g] == 0).all()
+            continue
+        check_rows(out[a:b], x[a:b], w[g], bias[g], None, "silu")
+        check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g], None, "none")
 
 
 @gpu
