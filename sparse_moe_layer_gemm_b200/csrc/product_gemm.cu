@@ -23,8 +23,7 @@
 // the two sums.  With one pipeline a turn of its MMA warp (wait, issue, commit)
 // bounds small tiles, whatever their rows: 173 ns per 64 steps at 16 rows, 215 at
 // 128 (16 CTAs alone), 135 and 162 with two.  Before that, 16 rows took 475 ns
-// with one-lane loops and 350 with whole-warp loops and elect.  Up to 16 rows a
-// slot holds two sub-slots of 64 steps.  With enough tiles HBM is the bound: 512
+// with one-lane loops and 350 with whole-warp loops and elect.  With enough tiles HBM is the bound: 512
 // rows over 288 groups, 4096 -> 1280, read their weights at 6.6 TB/s; with
 // weights in L2 its delivery, 16 bytes a picosecond (512 rows 4096 -> 4096 on 128
 // CTAs: 22 us).  Every wait is bounded (moe_ptx.cuh).
@@ -49,8 +48,10 @@ constexpr int kEpiWarps = 8;  // two per accumulator lane quadrant, on alternate
 constexpr int kThreads = 32 * (2 * kPipes + kEpiWarps);
 constexpr int kABytes = 2 * kSubBytes;
 constexpr int kMaxStages = 5;  // per pipeline
-// sub-slots of 64 contraction steps per slot: what leaves room for enough slots
-constexpr int subs_of(int bn) { return bn <= 16 ? 2 : 1; }
+// sub-slots of 64 contraction steps per slot: two where they leave room for
+// enough slots (32 rows 1280 -> 4096 6.8 us with two, 7.3 with one; 64 rows 4096 ->
+// 4096 in 4 parts 11.0 and 9.6)
+constexpr int subs_of(int bn) { return bn <= 32 ? 2 : 1; }
 
 constexpr int kAhead = 2;  // residual chunks on their way
 // staging of the epilogue
@@ -357,10 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // one tile per cluster in this form (the launch has a cluster per tile)
       split_send(x, taddr, second, q, part, empty, lane);
-      store_tile<MODE, T, 16, kAhead, true>(
-          p, taddr + x.first(), second, part, kEpiWarps / 4, x.rows(rank), row0 + x.first(),
-          t.f0 + q * 32, t.g, empty, stg, lane, Joined{x, q, lane, abort_flag, p.status, false});
-      split_settle(p, x);
+      // (the warp of the first features waits for all that is sent here as it joins)
+      if (!store_tile<MODE, T, 16, kAhead, true>(
+              p, taddr + x.first(), second, part, kEpiWarps / 4, x.rows(rank), row0 + x.first(),
+              t.f0 + q * 32, t.g, empty, stg, lane, Joined{x, q, lane, abort_flag, p.status, false}))
+        split_settle(p, x);
       cluster_arrive();
       left = true;
       break;

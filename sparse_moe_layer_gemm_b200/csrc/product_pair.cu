@@ -458,10 +458,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
         if (SPLITS) {  // the launch has a cluster per tile
           split_send(x, taddr, 0, q, part, empty, lane);
-          store_tile<MODE, T, 16, kAheadSplit, false>(
+          const bool joined = store_tile<MODE, T, 16, kAheadSplit, false>(
               p, taddr + x.first(), 0, part, 2, x.rows(x.rank), row0 + x.first(), f0, t.g, empty, stg,
               lane, Joined{x, q, lane, abort_flag, p.status, false});
-          split_settle(p, x);
+          if (!joined || f0 >= p.feats) split_settle(p, x);
           break;
         }
         store_tile<MODE, T, 32, kAhead, false>(p, taddr, 0, part, 2, min(hn, t.n_valid - h * hn),

@@ -326,13 +326,13 @@ int64_t row_blocks(const Shape& q, int64_t bn) {
 // Nanoseconds, as measured on one B200 with weights from L2 (graphs of calls in
 // a row), of one slot of 64 contraction steps.  A few CTAs alone are bound by
 // what their MMA warps issue; many by what L2 delivers, 16 bytes a picosecond.
-// One CTA, 128 features x bn rows: 16 CTAs take 132, 151, 154, 163 ns per slot at
+// One CTA, 128 features x bn rows: 16 CTAs take 132, 128, 154, 163 ns per slot at
 // bn = 16, 32, 64, 128, 128 CTAs 160 at 16 rows, 210 at 64, 258 at 128.
 int64_t l2_ns(const Shape& q, int64_t ctas, int b_rows) {
   return ctas * (kProductBM * q.a_lines + b_rows * q.b_lines) * 128 / 16000;
 }
 int64_t one_cta_slot_ns(const Shape& q, int bn, int64_t ctas) {
-  const int alone = bn <= 16 ? 135 : bn <= 32 ? 150 : bn <= 64 ? 154 : 162;
+  const int alone = bn <= 32 ? 132 : bn <= 64 ? 154 : 162;
   return std::max<int64_t>(alone, l2_ns(q, ctas, bn));
 }
 // A CTA pair, 256 features: 262 ns per slot up to 224 rows and 280 at 256 for a
