@@ -24,6 +24,11 @@ __device__ __forceinline__ void end_ordered(LaunchOrder o) {
 }
 
 template <typename T>
+constexpr bool is_bf16() {
+  return __is_same(T, __nv_bfloat16);
+}
+
+template <typename T>
 __device__ __forceinline__ float to_f32(T v);
 template <>
 __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -796,6 +801,10 @@ __device__ __forceinline__ bool store_chunks(const ProductParams& p, uint32_t ta
       if (ring) cp_async_wait<0>();
       return false;
     }
+    if (MODE != kProductForward && !is_bf16<T>()) {
+#pragma unroll
+      for (int i = 0; i < 16 * kB; ++i) v[i] *= p.out_scale;
+    }
 #pragma unroll
     for (int i = 0; i < 16 * kB; ++i) v[i] += bias[(i >> 1) & 3];
     auto stage = [&]() {
@@ -851,11 +860,6 @@ __device__ __forceinline__ bool store_tile(const ProductParams& p, uint32_t tadd
                                                        f0, g, zeros, stg, lane, join);
   return store_chunks<MODE, T, ROWS, false, AHEAD, TWO>(p, taddr, second, part, parts, n_valid, row0,
                                                         f0, g, zeros, stg, lane, join);
-}
-
-template <typename T>
-constexpr bool is_bf16() {
-  return __is_same(T, __nv_bfloat16);
 }
 
 }  // namespace product

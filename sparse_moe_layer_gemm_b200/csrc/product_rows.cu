@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kGradThreads, 4) row_grad_kernel(const RowGrad
 #pragma unroll
             for (int i = 0; i < E; ++i) {
               if (VEC || col + 32 * i < p.cols) acc[i] += v[i];
-              dv[k].v[i] = from_f32<T>(v[i]);
+              // (a bf16 dz is never scaled)
+              dv[k].v[i] = from_f32<T>(is_bf16<T>() ? v[i] : v[i] * p.dz_scale);
               if (!VEC && dz != nullptr && col + 32 * i < p.cols) out[32 * i] = dv[k].v[i];
             }
             if (VEC && dz != nullptr) *reinterpret_cast<Vec<T>*>(out) = dv[k];

@@ -76,6 +76,7 @@ struct ProductParams {
   // of a group (dw) or of a row block, and by those of an ordering chunk
   int f_tiles, dw_blocks, dw_rows;
   FastDiv by_group, by_chunk;
+  float out_scale;     // dx, dw in fp16: 1 / dz_scale
   void* out;
   int64_t ld_out;      // elements between output rows
   const void* bias;    // [groups, feats] or nullptr
@@ -162,6 +163,11 @@ struct RowGradParams {
   int64_t ld_preact;
   void* dz;            // nullptr: not written
   int64_t ld_dz;
+  // dz is stored times this: 1/2 in fp16, since slopes reach 1.13 and |dout| fp16's
+  // largest value (dz would be infinite where dx and dw are not), else 1.  A power
+  // of two, taken back exactly in the products' fp32 sums; it costs the steps of
+  // 2^-24 below 2^-13, which become 2^-23.
+  float dz_scale;
   const int* offsets;
   int groups, rows, cols;
   int act;

@@ -574,6 +574,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     q.ld_preact = a->ld_preact;
     q.dz = ws.make_dz || ws.copy_dout ? base + ws.dz : nullptr;
     q.ld_dz = padded(N);
+    q.dz_scale = ws.make_dz && !bf16 ? 0.5f : 1.f;
     q.offsets = a->offsets;
     q.groups = G;
     q.rows = c->rows;
@@ -591,6 +592,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
   p.groups = G;
   p.rows = c->rows;
   p.status = status;
+  p.out_scale = ws.make_dz && !bf16 ? 2.f : 1.f;
   ProductMaps m;
   if (a->dx != nullptr) {
     p.feats = c->in_features;

@@ -214,6 +214,43 @@ def test_slopes_at_zero_and_far_out():
 
 
 @gpu
+@pytest.mark.parametrize("act,at", [("silu", 2.4), ("gelu", 1.414), ("gelu_tanh", 1.414)])
+@pytest.mark.parametrize("rows,k,n", [(3, 40, 24), (130, 72, 99), (300, 2056, 264)])
+def test_fp16_gradients_of_large_values(rows, k, n, act, at):
+    """dz = dout act'(z) passes fp16's largest value (slopes reach 1.13) where dx,
+    dw and db do not."""
+    gen = torch.Generator().manual_seed(rows)
+    dt = torch.float16
+    dout = torch.full((rows, n), 65504.0, dtype=dt, device="cuda")
+    dout[:, ::2] *= -1
+    pre = torch.full((rows, n), at, dtype=dt, device="cuda")
+    x, w = normal(gen, dt, rows, k, std=2.0 ** -10), normal(gen, dt, k, n, std=2.0 ** -10)
+    assert float((dout.double() * slope64(pre.double(), act)).abs().max()) > 65504
+    dx, dw, _ = B.linear_backward(dout, x, w, preact=pre, activation=act, need_db=False)
+    check_grads(dx, dw, None, dout, x, w, pre, act)
+    off = offsets_of([rows - 2, 0, 2])
+    dx, dw, _ = B.grouped_linear_backward(dout, x, off, w.expand(3, k, n).contiguous(),
+                                          preact=pre, activation=act, need_db=False)
+    for g, (a, b) in enumerate(((0, rows - 2), (0, 0), (rows - 2, rows))):
+        if a < b:
+            check_grads(dx[a:b], dw[g], None, dout[a:b], x[a:b], w, pre[a:b], act)
+
+
+@gpu
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_fp16_gradients_of_small_values(act):
+    """Gradients around fp16's smallest: dz keeps steps of 2^-23, half of one off
+    at most, whatever many rows of it add up to."""
+    gen = torch.Generator().manual_seed(4)
+    dt, rows, k, n = torch.float16, 500, 72, 136
+    dout = normal(gen, dt, rows, n, std=3e-7)
+    pre, x = normal(gen, dt, rows, n, std=2.0), normal(gen, dt, rows, k, std=30.0)
+    w = normal(gen, dt, k, n, std=30.0)
+    grads = B.linear_backward(dout, x, w, preact=pre, activation=act)
+    check_grads(*grads, dout, x, w, pre, act)
+
+
+@gpu
 def test_offsets_past_32_bits():
     """Row strides that take the last rows more than 2^32 elements away."""
     gen = torch.Generator().manual_seed(9)
