@@ -718,15 +718,20 @@ class DenseMLP:
 
 
 # ------------------------------------------------- stand-alone products and SwiGLU
+# With stream= a call runs there, not on the current stream: the caller orders it
+# after what made its inputs; new outputs belong to that stream.
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # moe_activation_t
 _OP_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 
 
 class _Elsewhere:
     """Makes a tensor's device and the caller's stream (if given) current, so
-    that what a call allocates belongs to the stream that it runs on."""
+    that what a call allocates belongs to the stream that it runs on.  The
+    call's tensors (t and others) are recorded on a given stream: their memory
+    is not handed out again while it may still use them, even if the caller
+    drops them right after the call."""
 
-    def __init__(self, t: torch.Tensor, stream):
+    def __init__(self, t: torch.Tensor, stream, *others):
         dev = t.device
         s = torch.cuda.current_stream(dev) if stream is None else \
             stream if isinstance(stream, torch.cuda.Stream) else \
@@ -734,12 +739,16 @@ class _Elsewhere:
         if s.device != dev:
             raise ValueError(f"stream on {s.device}, tensors on {dev}")
         self._ctx = (torch.cuda.device(dev), torch.cuda.stream(s))
+        self._used = () if stream is None else [u for u in (t, *others) if u is not None]
+        self._stream = s
 
     def __enter__(self):
         for c in self._ctx:
             c.__enter__()
 
     def __exit__(self, *exc):
+        for u in self._used:
+            u.record_stream(self._stream)
         for c in reversed(self._ctx):
             c.__exit__(*exc)
 
@@ -829,7 +838,7 @@ def _linear(x, offsets, w, bias, residual, activation, out, preact, stream):
     ld_res = _need_rows(residual, "residual", x, R, N) if residual is not None else 0
     ld_pre = _need_rows(preact, "preact", x, R, N) if preact is not None else 0
     if _elsewhere(x, stream):
-        with _Elsewhere(x, stream):
+        with _Elsewhere(x, stream, offsets, w, bias, residual, out, preact):
             return _linear(x, offsets, w, bias, residual, activation, out, preact, None)
     st = torch._C._cuda_getCurrentRawStream(x.get_device())
     if out is None:
@@ -893,7 +902,7 @@ def _linear_backward(dout, x, offsets, w, preact, activation, need, into, stream
     ld_pre = _need_rows(preact, "preact", dout, R, N) if preact is not None else 0
     dx, dw, db = into
     if _elsewhere(dout, stream):
-        with _Elsewhere(dout, stream):
+        with _Elsewhere(dout, stream, x, offsets, w, preact, *into):
             return _linear_backward(dout, x, offsets, w, preact, activation, need, into, None)
     st = torch._C._cuda_getCurrentRawStream(dout.get_device())
     ld_dx = 0
@@ -989,7 +998,7 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, scale: Optional[torch.Tensor] =
     rows outside [offsets[0], offsets[-1]) are not written."""
     cfg, R, W, (ldg, ldu) = _swiglu_setup(gate, up, scale, limit, offsets)
     if _elsewhere(gate, stream):
-        with _Elsewhere(gate, stream):
+        with _Elsewhere(gate, stream, up, scale, offsets, out):
             return swiglu(gate, up, scale, limit=limit, offsets=offsets, out=out)
     if out is None:
         out, ldo = _new_rows(gate, R, W)
@@ -1017,7 +1026,7 @@ def swiglu_backward(dout: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
     if dscale is not None and scale is None:
         raise ValueError("dscale: there is no scale")
     if _elsewhere(gate, stream):
-        with _Elsewhere(gate, stream):
+        with _Elsewhere(gate, stream, dout, up, scale, offsets, dgate, dup, dscale):
             return swiglu_backward(dout, gate, up, scale, limit=limit, offsets=offsets,
                                    dgate=dgate, dup=dup, dscale=dscale)
     if dgate is None:

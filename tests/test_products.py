@@ -1107,6 +1107,74 @@ def test_swiglu_refuses(lib):
         assert bwd(**kw) == bad, kw
 
 
+def test_tensors_are_recorded_on_a_given_stream(monkeypatch):
+    """Fakes in place of the device: what a call on another stream uses is
+    recorded on it, after the call; on the current stream nothing is."""
+    import contextlib
+    done = []
+
+    class Stream:
+        device = "cuda:0"
+
+    class Tensor:
+        device = "cuda:0"
+
+        def __init__(self, name):
+            self.name = name
+
+        def record_stream(self, s):
+            done.append((self.name, s))
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: Stream())
+    s = Stream()
+    with B._Elsewhere(Tensor("x"), s, Tensor("w"), None, Tensor("out")):
+        done.append("call")
+    assert done == ["call", ("x", s), ("w", s), ("out", s)]
+    done.clear()
+    with B._Elsewhere(Tensor("x"), None, Tensor("w")):
+        pass
+    assert done == []
+
+
+@gpu
+@pytest.mark.parametrize("call", ["linear", "grouped_backward", "swiglu", "swiglu_backward"])
+def test_dropped_tensors_of_a_call_on_another_stream(call):
+    """Tensors dropped right after a call on another stream keep their memory
+    until that call is done."""
+    gen = torch.Generator().manual_seed(40)
+    rows, k = 4096, 512
+    a, b = normal(gen, torch.bfloat16, rows, k), normal(gen, torch.bfloat16, rows, k)
+    c, w = normal(gen, torch.bfloat16, rows, k), normal(gen, torch.bfloat16, k, k, std=0.05)
+    off = offsets_of([rows])
+
+    def run(a, b, c, w, off, **kw):
+        if call == "linear":
+            return (B.linear(a, w, residual=b, **kw),)
+        if call == "grouped_backward":
+            return B.grouped_linear_backward(a, b, off, w[None], preact=c, activation="silu", **kw)
+        if call == "swiglu":
+            return (B.swiglu(a, b, **kw),)
+        return B.swiglu_backward(a, b, c, **kw)[:2]
+
+    want = run(a, b, c, w, off)
+    s, busy = torch.cuda.Stream(), torch.empty(1 << 28, device="cuda")
+    copies = [t.clone() for t in (a, b, c, w, off)]
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(20):  # some milliseconds, so that the call has not begun below
+            busy.fill_(1.0)
+    got = run(*copies, stream=s)
+    del copies
+    # memory that may be the dropped tensors', overwritten on the current stream
+    spoilt = [torch.full((rows, k), math.nan, dtype=a.dtype, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    del spoilt
+
+
 def test_python_refusals_on_the_host():
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(64, 72, dtype=torch.bfloat16)
     for call in (lambda: B.linear(x, w),                               # not on a GPU
