@@ -964,10 +964,12 @@ def grouped_linear_backward(dout: torch.Tensor, x: Optional[torch.Tensor],
 
 def linear_device_error(device=None) -> int:
     """Synchronises the device, then reads and clears its products' status
-    word (0: no bounded wait gave up)."""
+    word (0: no bounded wait gave up).  Raises if it cannot be read."""
     v = ctypes.c_int()
     with torch.cuda.device(device):
-        load_library().moe_linear_get_device_error(ctypes.byref(v))
+        status = load_library().moe_linear_get_device_error(ctypes.byref(v))
+    if status not in (MOE_OK, MOE_ERR_DEVICE_TIMEOUT):
+        raise MoeError(status, "moe_linear_get_device_error")
     return v.value
 
 

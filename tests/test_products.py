@@ -1175,6 +1175,30 @@ def test_dropped_tensors_of_a_call_on_another_stream(call):
     del spoilt
 
 
+@pytest.mark.parametrize("status,word,want", [
+    (0, 0, 0), ("MOE_ERR_DEVICE_TIMEOUT", 3, 3), ("MOE_ERR_CUDA", 0, None),
+    ("MOE_ERR_UNSUPPORTED", 0, None)])
+def test_device_error_that_could_not_be_read(monkeypatch, status, word, want):
+    """A status word that could not be read is an error, not 0."""
+    import contextlib
+    code = status if status == 0 else getattr(B, status)
+
+    class Library:
+        @staticmethod
+        def moe_linear_get_device_error(p):
+            p._obj.value = word
+            return code
+
+    monkeypatch.setattr(B, "load_library", lambda: Library)
+    monkeypatch.setattr(B, "status_string", str)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    if want is None:
+        with pytest.raises(B.MoeError):
+            B.linear_device_error()
+    else:
+        assert B.linear_device_error() == want
+
+
 def test_python_refusals_on_the_host():
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(64, 72, dtype=torch.bfloat16)
     for call in (lambda: B.linear(x, w),                               # not on a GPU
