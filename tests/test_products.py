@@ -862,6 +862,29 @@ def test_swiglu_clamp_edges_and_nan():
     assert dup[0, 0] != 0 and dup[0, 1] != 0 and dup[0, 2] == 0
 
 
+@gpu
+def test_silu_far_below_zero():
+    """Where 1 + exp(-z) passes 2^126 the reciprocal is no normal number, but silu
+    is (-5e-37 at -88) and bf16 holds it."""
+    dt = torch.bfloat16
+    z = torch.tensor([[-80.0, -86.5, -87.0, -87.5, -88.0, -88.5, -1.0, 0.0]], dtype=dt, device="cuda")
+    one, eye = torch.ones_like(z), torch.eye(8, dtype=dt, device="cuda")
+    want = act64(z.double(), "silu")
+    # the exponent's rounding, 2^-18 of 2^x at |x| < 128 and log2(e)'s as much again
+    bound = (half_step(dt) + 2.0 ** -16) * want.abs()
+    close(B.swiglu(z, one), want, bound, "swiglu")
+    close(B.swiglu_backward(one, z, one)[1], want, bound, "dup")
+    x = torch.zeros(1, 8, dtype=dt, device="cuda")
+    close(B.linear(x, eye, z[0].contiguous(), activation="silu"), want, bound, "linear")
+    slope = slope64(z.double(), "silu")
+    bound = (half_step(dt) + 2.0 ** -16) * slope.abs()
+    close(B.swiglu_backward(one, z, one)[0], slope, bound, "dgate")
+    # (dz is rounded, times one in dx)
+    dx, _, db = B.linear_backward(one, None, eye, preact=z, activation="silu", need_dw=False)
+    close(dx, slope, bound, "dx")
+    close(db[None], slope, bound, "db")
+
+
 # ------------------------------------------------------------ a run of them together
 @gpu
 def test_expert_ffn_forward_matches_the_layer():
