@@ -575,6 +575,23 @@ int moe_linear(const moe_linear_config_t* cfg, const moe_linear_args_t* args, vo
 int moe_linear_backward(const moe_linear_config_t* cfg, const moe_linear_grads_t* grads,
                         void* workspace, size_t ws_bytes, void* stream);
 
+/* The tiles that a call with these arguments takes on the current device, for
+ * tests that have to reach a certain kernel.  Zeros for a product that is not
+ * computed.  Enqueues nothing. */
+typedef struct {
+  int pairs;        /* 1: CTA pairs, 256 features per tile; 0: one CTA, 128 */
+  int rows;         /* most rows of a tile (dW: rows of its output) */
+  int accumulators; /* that share a tile's rows: 1 or 2 */
+  int split;        /* CTAs or pairs that share a tile's contraction */
+  int slots;        /* of a pipeline (one CTA per tile: of each of its two) */
+  int slot_steps;   /* contraction steps of a slot */
+} moe_linear_tiles_t;
+
+int moe_linear_tiles(const moe_linear_config_t* cfg, const moe_linear_args_t* args,
+                     moe_linear_tiles_t* tiles);
+int moe_linear_backward_tiles(const moe_linear_config_t* cfg, const moe_linear_grads_t* grads,
+                              moe_linear_tiles_t* dx, moe_linear_tiles_t* dw);
+
 /* As moe_get_device_error, for the current device's status word of the
  * stand-alone products (one per device, shared by all their calls). */
 int moe_linear_get_device_error(int* device_err);

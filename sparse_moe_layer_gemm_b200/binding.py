@@ -44,7 +44,8 @@ EXPORTS = (
     "moe_check_fused_timeout", "moe_load_shard_weights", "moe_forward_host_async",
     "moe_forward_host_join", "moe_linear_config_check", "moe_linear_workspace_size",
     "moe_linear_backward_workspace_size", "moe_linear", "moe_linear_backward",
-    "moe_linear_get_device_error", "moe_swiglu", "moe_swiglu_backward",
+    "moe_linear_get_device_error", "moe_swiglu", "moe_swiglu_backward", "moe_linear_tiles",
+    "moe_linear_backward_tiles",
 )
 MOE_NUM_STAGES = 7
 STAGE_NAMES = ("router", "topk", "sort", "gather", "gate_up", "down", "combine")
@@ -122,6 +123,17 @@ class moe_linear_grads_t(ctypes.Structure):
         ("ld_dx", ctypes.c_int64),
         ("dw", ctypes.c_void_p),
         ("dbias", ctypes.c_void_p),
+    ]
+
+
+class moe_linear_tiles_t(ctypes.Structure):
+    _fields_ = [
+        ("pairs", ctypes.c_int),
+        ("rows", ctypes.c_int),
+        ("accumulators", ctypes.c_int),
+        ("split", ctypes.c_int),
+        ("slots", ctypes.c_int),
+        ("slot_steps", ctypes.c_int),
     ]
 
 
@@ -212,6 +224,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_linear.argtypes = [lc, la, vp, sz, vp]
     lib.moe_linear_backward.argtypes = [lc, lg, vp, sz, vp]
     lib.moe_linear_get_device_error.argtypes = [ctypes.POINTER(i)]
+    lt = ctypes.POINTER(moe_linear_tiles_t)
+    lib.moe_linear_tiles.argtypes = [lc, la, lt]
+    lib.moe_linear_backward_tiles.argtypes = [lc, lg, lt, lt]
     sc = ctypes.POINTER(moe_swiglu_config_t)
     lib.moe_swiglu.argtypes = [sc, vp, i64, vp, i64, vp, vp, vp, i64, vp]
     lib.moe_swiglu_backward.argtypes = [sc, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64,

@@ -437,21 +437,26 @@ cudaError_t product_cluster_room(int cluster, int* ctas) {
   return e;
 }
 
+size_t product_slots(int mode, ProductParams* p) {
+  const size_t fixed = 1024 + static_cast<size_t>(epi_bytes(*p) + split_bytes(p->bn, p->split)) +
+                       kBarBytes + static_cast<size_t>(group_table_bytes(p->groups));
+  p->subs = subs_of(p->bn);
+  const size_t slot = kPipes * p->subs * (kABytes + static_cast<size_t>(b_bytes(mode, p->bn)));
+  p->stages = static_cast<int>(
+      std::min<size_t>(kMaxStages, (static_cast<size_t>(227) * 1024 - fixed) / slot));
+  return p->stages < 1 || p->stages * slot < static_cast<size_t>(split_out_bytes(p->bn, p->split))
+             ? 0
+             : fixed + p->stages * slot;
+}
+
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p0,
                            int num_sms, cudaStream_t st) {
   ProductParams p = p0;
-  const size_t fixed = 1024 + static_cast<size_t>(epi_bytes(p) + split_bytes(p.bn, p.split)) +
-                       kBarBytes + static_cast<size_t>(group_table_bytes(p.groups));
-  p.subs = subs_of(p.bn);
-  const size_t slot = kPipes * p.subs * (kABytes + static_cast<size_t>(b_bytes(mode, p.bn)));
   const int64_t tiles = product_tile_order(mode, kProductBM, &p);
   if (tiles <= 0) return cudaSuccess;
   if (tiles > (1LL << 30)) return cudaErrorInvalidValue;
-  p.stages = static_cast<int>(
-      std::min<size_t>(kMaxStages, (static_cast<size_t>(227) * 1024 - fixed) / slot));
-  if (p.stages * slot < static_cast<size_t>(split_out_bytes(p.bn, p.split)))
-    return cudaErrorInvalidConfiguration;
-  const size_t smem = fixed + p.stages * slot;
+  const size_t smem = product_slots(mode, &p);
+  if (smem == 0) return cudaErrorInvalidConfiguration;
   const int grid =
       p.split > 1 ? static_cast<int>(tiles) * p.split : static_cast<int>(std::min<int64_t>(tiles, num_sms));
   if (bf16) {

@@ -489,22 +489,29 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
   end_ordered(p.order);
 }
 
+template <int HALVES>
+size_t slots(int mode, ProductParams* p) {
+  using S = PairShape<HALVES>;
+  const int slot = pair_slot_bytes(mode, HALVES, p->split > 1, p->bn);
+  // (a residual's staging takes a slot's room)
+  const int fixed = 1024 + epi_bytes(*p) + split_bytes(p->bn, p->split) + S::kBarBytes +
+                    group_table_bytes(p->groups);
+  p->stages = std::min(S::kMaxStages, (227 * 1024 - fixed) / slot);
+  return p->stages < (HALVES == 1 ? 2 : kLead + 1) ||
+                 p->stages * slot < split_out_bytes(p->bn, p->split)
+             ? 0
+             : static_cast<size_t>(fixed + p->stages * slot);
+}
+
 template <int MODE, int HALVES, typename T, bool SPLITS>
 cudaError_t launch(const ProductMaps& m, const ProductParams& p0, int grid, cudaStream_t st) {
-  using S = PairShape<HALVES>;
   ProductParams p = p0;
-  const int slot = pair_slot_bytes(MODE, HALVES, SPLITS, p.bn);
-  // (a residual's staging takes a slot's room)
-  const int fixed = 1024 + epi_bytes(p) + split_bytes(p.bn, p.split) + S::kBarBytes +
-                    group_table_bytes(p.groups);
-  p.stages = std::min(S::kMaxStages, (227 * 1024 - fixed) / slot);
-  if (p.stages < (HALVES == 1 ? 2 : kLead + 1) ||
-      p.stages * slot < split_out_bytes(p.bn, p.split))
-    return cudaErrorInvalidConfiguration;
+  const size_t smem = product_pair_slots(MODE, &p);
+  if (smem == 0) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(threads_of(MODE));
-  cfg.dynamicSmemBytes = static_cast<size_t>(fixed + p.stages * slot);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -557,6 +564,11 @@ cudaError_t configure() {
 }
 
 }  // namespace
+
+size_t product_pair_slots(int mode, ProductParams* p) {
+  p->subs = 1;
+  return p->bn <= kAccCols ? slots<1>(mode, p) : slots<2>(mode, p);
+}
 
 cudaError_t product_pair_configure_device() {
   const cudaError_t e = configure<__nv_bfloat16>();

@@ -118,6 +118,10 @@ struct ProductMaps {
 
 cudaError_t launch_product(int mode, bool bf16, const ProductMaps& m, const ProductParams& p,
                            int num_sms, cudaStream_t st);
+// Fills in the pipeline's slots; returns the dynamic shared memory, 0 if it does
+// not fit.
+size_t product_slots(int mode, ProductParams* p);
+size_t product_pair_slots(int mode, ProductParams* p);
 
 // The same on CTA pairs (product_pair.cu): tiles of 256 features x bn rows, up
 // to 256 with one accumulator per tile, up to 512 with two of half the rows;

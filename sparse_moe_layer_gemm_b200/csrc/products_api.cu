@@ -443,6 +443,88 @@ cudaError_t launch_any(const Choice& ch, int mode, bool bf16, const ProductMaps&
                  : launch_product(mode, bf16, m, p, sms, st);
 }
 
+// The choice for one of the products and its place in the parameters.
+void take(const Shape& q, const Room& room, ProductParams* p, Choice* ch) {
+  *ch = choose(q, room);
+  p->bn = ch->bn;
+  p->box_rows = box_rows(*ch, p->rows);
+  p->chunk = ch->chunk;
+  p->split = ch->split;
+}
+
+Choice choose_forward(const moe_linear_config_t* c, const moe_linear_args_t* a, const Operand& x,
+                      const Operand& w, const Room& room, ProductParams* p) {
+  const int64_t K = c->in_features, N = c->out_features;
+  p->offsets = a->offsets;
+  p->groups = std::max(1, c->groups);
+  p->rows = c->rows;
+  p->feats = c->out_features;
+  p->depth = c->in_features;
+  p->out = a->out;
+  p->ld_out = a->ld_out;
+  p->bias = a->bias;
+  p->residual = a->residual;
+  p->ld_residual = a->ld_residual;
+  p->preact = a->preact;
+  p->ld_preact = a->ld_preact;
+  p->act = c->activation;
+  p->width_out = row_width(a->out, a->ld_out, N);
+  p->width_residual = row_width(a->residual, a->ld_residual, N);
+  p->width_preact = row_width(a->preact, a->ld_preact, N);
+  p->wide_a = N % 64 == 0;
+  int64_t n_groups, mean;
+  filled(a->offsets, p->groups, c->rows, &n_groups, &mean);
+  const bool epilogue =
+      c->activation != MOE_ACT_NONE || a->residual != nullptr || a->preact != nullptr;
+  Choice ch;
+  take({N, n_groups, mean, (K + 63) / 64, n_groups > 1, false, epilogue, p->width_out, lines(w),
+        lines(x)}, room, p, &ch);
+  return ch;
+}
+
+Choice choose_dx(const moe_linear_config_t* c, const moe_linear_grads_t* a, const Operand& dz,
+                 const Operand& w, const Room& room, ProductParams* p) {
+  const int64_t K = c->in_features, N = c->out_features;
+  p->offsets = a->offsets;
+  p->groups = std::max(1, c->groups);
+  p->rows = c->rows;
+  p->feats = c->in_features;
+  p->depth = c->out_features;
+  p->out = a->dx;
+  p->ld_out = a->ld_dx;
+  p->width_out = row_width(a->dx, a->ld_dx, K);
+  int64_t n_groups, mean;
+  filled(a->offsets, p->groups, c->rows, &n_groups, &mean);
+  Choice ch;
+  take({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false, p->width_out, lines(w),
+        lines(dz)}, room, p, &ch);
+  return ch;
+}
+
+Choice choose_dw(const moe_linear_config_t* c, const moe_linear_grads_t* a, const Operand& dz,
+                 const Operand& x, const Room& room, ProductParams* p) {
+  const int64_t K = c->in_features, N = c->out_features;
+  p->offsets = a->offsets;
+  p->groups = std::max(1, c->groups);
+  p->rows = c->rows;
+  p->feats = c->out_features;
+  p->cols = c->in_features;
+  p->depth = 0;
+  p->out = a->dw;
+  p->ld_out = N;
+  p->width_out = row_width(a->dw, N, N);
+  const int64_t steps = std::max<int64_t>(1, (c->rows / p->groups + 63) / 64);
+  Choice ch;
+  take({N, p->groups, K, steps, false, true, false, p->width_out, lines(dz), lines(x)}, room, p, &ch);
+  return ch;
+}
+
+int report(int mode, const Choice& ch, ProductParams* p, moe_linear_tiles_t* t) {
+  if ((ch.pair ? product_pair_slots(mode, p) : product_slots(mode, p)) == 0) return MOE_ERR_CUDA;
+  *t = {ch.pair ? 1 : 0, ch.bn, ch.pair && ch.bn > 256 ? 2 : 1, ch.split, p->stages, 64 * p->subs};
+  return MOE_OK;
+}
+
 // Turns *o into its copy at dst with 16-byte aligned rows.  With offsets the
 // weights of groups without rows are left out.
 PackOperand aligned_copy(Operand* o, int64_t groups, int64_t rows, int64_t cols, void* dst,
@@ -498,35 +580,9 @@ int moe_linear(const moe_linear_config_t* c, const moe_linear_args_t* a, void* w
   if (ws.copy_w) pack.op[1] = aligned_copy(&w, G, K, N, base + ws.w, a->offsets);
   MOE_CUDA(launch_pack_rows(pack, st));
   ProductParams p{};
-  p.offsets = a->offsets;
-  p.groups = G;
-  p.rows = c->rows;
-  p.feats = c->out_features;
-  p.depth = c->in_features;
-  int64_t n_groups, mean;
-  filled(a->offsets, G, R, &n_groups, &mean);
-  p.width_out = row_width(a->out, a->ld_out, N);
-  const bool epilogue =
-      c->activation != MOE_ACT_NONE || a->residual != nullptr || a->preact != nullptr;
-  const Choice ch = choose(
-      {N, n_groups, mean, (K + 63) / 64, n_groups > 1, false, epilogue, p.width_out, lines(w), lines(x)}, room);
-  p.bn = ch.bn;
-  p.box_rows = box_rows(ch, c->rows);
-  p.chunk = ch.chunk;
-  p.split = ch.split;
-  p.out = a->out;
-  p.ld_out = a->ld_out;
-  p.bias = a->bias;
-  p.residual = a->residual;
-  p.ld_residual = a->ld_residual;
-  p.preact = a->preact;
-  p.ld_preact = a->ld_preact;
-  p.act = c->activation;
-  p.width_residual = row_width(a->residual, a->ld_residual, N);
-  p.width_preact = row_width(a->preact, a->ld_preact, N);
+  const Choice ch = choose_forward(c, a, x, w, room, &p);
   p.status = status;
   ProductMaps m;
-  p.wide_a = N % 64 == 0;
   if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, 64, p.wide_a) ||
       !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, p.box_rows, false))
     return MOE_ERR_CUDA;
@@ -588,26 +644,11 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     if (q.dz != nullptr) dz = {base + ws.dz, padded(N), 0};
   }
   ProductParams p{};
-  p.offsets = a->offsets;
-  p.groups = G;
-  p.rows = c->rows;
   p.status = status;
   p.out_scale = ws.make_dz && !bf16 ? 2.f : 1.f;
   ProductMaps m;
   if (a->dx != nullptr) {
-    p.feats = c->in_features;
-    p.depth = c->out_features;
-    p.out = a->dx;
-    p.ld_out = a->ld_dx;
-    p.width_out = row_width(a->dx, a->ld_dx, K);
-    int64_t n_groups, mean;
-    filled(a->offsets, G, R, &n_groups, &mean);
-    const Choice ch =
-        choose({K, n_groups, mean, (N + 63) / 64, n_groups > 1, false, false, p.width_out, lines(w), lines(dz)}, room);
-    p.bn = ch.bn;
-    p.box_rows = box_rows(ch, c->rows);
-    p.chunk = ch.chunk;
-    p.split = ch.split;
+    const Choice ch = choose_dx(c, a, dz, w, room, &p);
     if (!encode(&m.a, bf16, w.p, N, K, G, w.ld, w.gs, kProductBM, false) ||
         !encode(&m.b, bf16, dz.p, N, R, 1, dz.ld, 0, p.box_rows, false))
       return MOE_ERR_CUDA;
@@ -615,18 +656,7 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
     MOE_CUDA(launch_any(ch, kProductDx, bf16, m, p, room.sms(), st));
   }
   if (a->dw != nullptr) {
-    p.feats = c->out_features;
-    p.cols = c->in_features;
-    p.depth = 0;
-    p.out = a->dw;
-    p.ld_out = N;
-    p.width_out = row_width(a->dw, N, N);
-    const int64_t steps = std::max<int64_t>(1, (R / G + 63) / 64);
-    const Choice ch = choose({N, G, K, steps, false, true, false, p.width_out, lines(dz), lines(x)}, room);
-    p.bn = ch.bn;
-    p.box_rows = box_rows(ch, c->rows);
-    p.chunk = ch.chunk;
-    p.split = ch.split;
+    const Choice ch = choose_dw(c, a, dz, x, room, &p);
     if (!encode(&m.a, bf16, dz.p, N, R, 1, dz.ld, 0, 64, false) ||
         !encode(&m.b, bf16, x.p, K, R, 1, x.ld, 0, 64, false))
       return MOE_ERR_CUDA;
@@ -636,6 +666,54 @@ int moe_linear_backward(const moe_linear_config_t* c, const moe_linear_grads_t* 
   if (joins) {
     q.order = {products};
     MOE_CUDA(launch_bias_grad(bf16, q, room.sms(), st));
+  }
+  return MOE_OK;
+}
+
+int moe_linear_tiles(const moe_linear_config_t* c, const moe_linear_args_t* a,
+                     moe_linear_tiles_t* tiles) {
+  if (tiles == nullptr) return MOE_ERR_INVALID_ARG;
+  int r = check_forward(c, a);
+  if (r != MOE_OK) return r;
+  *tiles = {};
+  if (c->rows == 0) return MOE_OK;
+  Room room{};
+  int* status = nullptr;
+  if ((r = device_of(&room, &status)) != MOE_OK) return r;
+  Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
+  // (a workspace starts at 256 bytes, as its parts do)
+  const ForwardWs ws = forward_ws(c, a);
+  if (ws.copy_x) x = {nullptr, padded(c->in_features), 0};
+  if (ws.copy_w) w = {nullptr, padded(c->out_features), 0};
+  ProductParams p{};
+  const Choice ch = choose_forward(c, a, x, w, room, &p);
+  return report(kProductForward, ch, &p, tiles);
+}
+
+int moe_linear_backward_tiles(const moe_linear_config_t* c, const moe_linear_grads_t* a,
+                              moe_linear_tiles_t* dx, moe_linear_tiles_t* dw) {
+  if (dx == nullptr || dw == nullptr) return MOE_ERR_INVALID_ARG;
+  int r = check_backward(c, a);
+  if (r != MOE_OK) return r;
+  *dx = *dw = {};
+  if (c->rows == 0) return MOE_OK;
+  Room room{};
+  int* status = nullptr;
+  if ((r = device_of(&room, &status)) != MOE_OK) return r;
+  Operand x{a->x, a->ld_x, 0}, w{a->w, a->ld_w, group_stride(c, a->group_stride_w, a->ld_w)};
+  Operand dz{a->dout, a->ld_dout, 0};
+  const BackwardWs ws = backward_ws(c, a);
+  if (ws.copy_x) x = {nullptr, padded(c->in_features), 0};
+  if (ws.copy_w) w = {nullptr, padded(c->out_features), 0};
+  if (ws.make_dz || ws.copy_dout) dz = {nullptr, padded(c->out_features), 0};
+  ProductParams p{};
+  if (a->dx != nullptr) {
+    const Choice ch = choose_dx(c, a, dz, w, room, &p);
+    if ((r = report(kProductDx, ch, &p, dx)) != MOE_OK) return r;
+  }
+  if (a->dw != nullptr) {
+    const Choice ch = choose_dw(c, a, dz, x, room, &p);
+    if ((r = report(kProductDw, ch, &p, dw)) != MOE_OK) return r;
   }
   return MOE_OK;
 }

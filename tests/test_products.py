@@ -110,6 +110,30 @@ def check_grads(dx, dw, db, dout, x, w, preact, act):
               + tiny, "db")
 
 
+def tiles_of(x, w, offsets=None, residual=None, act="none", dout=None):
+    """The tiles that the product takes with a new output, and dx and dw if there
+    is a dout, as tuples (pairs, rows, accumulators, split, slots, slot_steps)."""
+    lib, (rows, k), n = B.load_library(), x.shape, w.shape[-1]
+    G = 0 if offsets is None else w.shape[0]
+    cfg = B.moe_linear_config_t(rows, k, n, G, B.MOE_BF16, B.ACTIVATIONS[act])
+    ld = lambda c: c if rows > 1 else (c + 7) // 8 * 8
+    off = None if offsets is None else offsets.data_ptr()
+    wide = w.stride(0) if G > 1 else 0
+    new, more = torch.empty(rows, n, dtype=x.dtype, device="cuda"), torch.empty_like(x)
+    got = [B.moe_linear_tiles_t() for _ in range(3)]
+    a = B.moe_linear_args_t(x.data_ptr(), ld(k), off, w.data_ptr(), n, wide, None,
+                            None if residual is None else residual.data_ptr(), ld(n),
+                            new.data_ptr(), ld(n), None, 0)
+    assert lib.moe_linear_tiles(cfg, a, got[0]) == B.MOE_OK
+    if dout is not None:
+        dw = torch.empty_like(w)
+        pre = None if act == "none" else new.data_ptr()
+        g = B.moe_linear_grads_t(dout.data_ptr(), ld(n), x.data_ptr(), ld(k), off, w.data_ptr(), n,
+                                 wide, pre, ld(n), more.data_ptr(), ld(k), dw.data_ptr(), None)
+        assert lib.moe_linear_backward_tiles(cfg, g, got[1], got[2]) == B.MOE_OK
+    return [tuple(getattr(t, f) for f, _ in t._fields_) for t in got]
+
+
 # ----------------------------------------------------------------- linear
 SHAPES = [(1, 64, 128), (1, 4096, 256), (2, 8, 8), (5, 1, 1), (16, 130, 264), (17, 64, 200),
           (33, 1000, 72), (64, 512, 1280), (77, 110, 77), (128, 256, 128), (129, 257, 129),
@@ -343,6 +367,64 @@ def test_linear_large(rows, k, n, act):
     check_grads(*grads, dout, x, w, pre, act)
 
 
+# tiles of two accumulators where nothing follows the product but a bias
+TWO = [(2600, 2600, 2600), (4000, 4104, 1288), (2700, 2312, 2601), (1100, 4096, 4096),
+       (2049, 1288, 5000)]
+
+
+@gpu
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("rows,k,n", TWO)
+def test_two_accumulators(rows, k, n, act):
+    gen = torch.Generator().manual_seed(rows + n)
+    dt = torch.float16 if rows % 4 else torch.bfloat16
+    x, w = normal(gen, dt, rows, k), normal(gen, dt, k, n, std=k ** -0.5)
+    bias, dout = normal(gen, dt, n), normal(gen, dt, rows, n)
+    pre = normal(gen, dt, rows, n) if act != "none" else None
+    assert 2 in [t[2] for t in tiles_of(x, w, act=act, dout=dout)]
+    out = B.linear(x, w, bias)
+    check_rows(out, x, w, bias, None, "none")
+    grads = B.linear_backward(dout, x, w, preact=pre, activation=act)
+    check_grads(*grads, dout, x, w, pre, act)
+    again = B.linear_backward(dout, x, w, preact=pre, activation=act)
+    assert torch.equal(out, B.linear(x, w, bias))
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    assert B.linear_device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("sizes,k,n", [([5000, 300, 70], 2600, 2600), ([3000, 0, 1, 900], 4104, 2312),
+                                       ([0, 2500, 131, 2469], 2600, 2600)])
+def test_grouped_two_accumulators(sizes, k, n):
+    """Tiles of two accumulators in ragged groups, shorter ones than a slot among
+    them; the rows around the groups hold NaN."""
+    gen = torch.Generator().manual_seed(n)
+    G, first, behind = len(sizes), 7, 40
+    rows = first + sum(sizes) + behind
+    x, dout = normal(gen, torch.bfloat16, rows, k), normal(gen, torch.bfloat16, rows, n)
+    w, bias = normal(gen, torch.bfloat16, G, k, n, std=k ** -0.5), normal(gen, torch.bfloat16, G, n)
+    for t in (x, dout):
+        t[:first] = math.nan
+        t[rows - behind:] = math.inf
+    off = offsets_of(sizes, first)
+    assert 2 in [t[2] for t in tiles_of(x, w, off, dout=dout)]
+    out = torch.full((rows, n), 3.0, dtype=x.dtype, device="cuda")
+    dx = torch.full((rows, k), 3.0, dtype=x.dtype, device="cuda")
+    B.grouped_linear(x, off, w, bias, out=out)
+    _, dw, db = B.grouped_linear_backward(dout, x, off, w, dx=dx)
+    for t in (out, dx):
+        assert (t[:first] == 3).all() and (t[rows - behind:] == 3).all()
+    o = off.tolist()
+    for g in range(G):
+        a, b = o[g], o[g + 1]
+        if a == b:
+            assert (dw[g] == 0).all() and (db[g] == 0).all()
+            continue
+        check_rows(out[a:b], x[a:b], w[g], bias[g], None, "none")
+        check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g], None, "none")
+    assert B.linear_device_error() == 0
+
+
 # few tiles and a long contraction: clusters of CTAs or of CTA pairs share tiles
 SHARED = [(7, 4096, 640), (16, 8192, 128), (40, 2056, 1111), (130, 4096, 512), (250, 4096, 4096),
           (384, 3000, 4096), (510, 4096, 1280), (700, 4104, 1288), (500, 4001, 515)]
@@ -403,6 +485,71 @@ def test_grouped_shared_tiles(sizes, k, n):
             continue
         check_rows(out[a:b], x[a:b], w[g], bias[g], None, "silu")
         check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g], None, "none")
+
+
+@gpu
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("sizes,k,n", [([8100, 0, 5, 77], 128, 128), ([8191, 1], 72, 64),
+                                       ([0, 6000, 6000], 256, 256), ([20000, 0, 11000, 70], 250, 250),
+                                       ([1, 8190], 128, 128)])
+def test_grouped_shared_weight_gradients(sizes, k, n, act):
+    """The weight gradients of long groups share their contraction in clusters:
+    groups shorter than the parts, empty ones, rows of others behind the last
+    slot; the rows around the groups hold NaN."""
+    gen = torch.Generator().manual_seed(sum(sizes))
+    G, first, behind = len(sizes), 9, 30
+    rows = first + sum(sizes) + behind
+    dt = torch.float16 if act == "none" else torch.bfloat16
+    x, dout = normal(gen, dt, rows, k), normal(gen, dt, rows, n)
+    w = normal(gen, dt, G, k, n, std=k ** -0.5)
+    pre = normal(gen, dt, rows, n) if act != "none" else None
+    for t in (x, dout):
+        t[:first] = math.nan
+        t[rows - behind:] = math.inf
+    off = offsets_of(sizes, first)
+    assert tiles_of(x, w, off, act=act, dout=dout)[2][3] > 1
+    dx = torch.full((rows, k), 3.0, dtype=dt, device="cuda")
+    kw = dict(preact=pre, activation=act)
+    _, dw, db = B.grouped_linear_backward(dout, x, off, w, dx=dx, **kw)
+    assert (dx[:first] == 3).all() and (dx[rows - behind:] == 3).all()
+    o = off.tolist()
+    for g in range(G):
+        a, b = o[g], o[g + 1]
+        if a == b:
+            assert (dw[g] == 0).all() and (db[g] == 0).all()
+            continue
+        check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g],
+                    None if pre is None else pre[a:b], act)
+    for _ in range(3):
+        again = B.grouped_linear_backward(dout, x, off, w, need_dx=False, **kw)
+        assert torch.equal(dw, again[1]) and torch.equal(db, again[2])
+    assert B.linear_device_error() == 0
+
+
+# tiles of four pairs, forward and dx; dx on four and eight CTAs
+MORE_SHARED = [(192, 8192, 3000), (190, 4096, 3000), (250, 8200, 2999), (192, 2816, 8192),
+               (190, 2560, 16384), (128, 2000, 4096), (16, 1000, 8192)]
+
+
+@gpu
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("rows,k,n", MORE_SHARED)
+def test_linear_more_shared_tiles(rows, k, n, act):
+    test_linear_shared_tiles(rows, k, n, act)
+
+
+@gpu
+def test_shared_tile_sizes_cover_every_share():
+    """What the sizes above are there for: products on clusters of 2, 4 and 8
+    CTAs and of 2 and 4 pairs, dx among them."""
+    seen = set()
+    for rows, k, n in SHARED + MORE_SHARED:
+        x, w = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((rows, k), (k, n)))
+        for what, t in zip(("forward", "dx", "dw"), tiles_of(x, w, dout=x.new_empty(rows, n))):
+            seen.add((what, t[0], t[3]))
+    shares = {s[1:] for s in seen}
+    assert {(0, 2), (0, 4), (0, 8), (1, 2), (1, 4)} <= shares
+    assert {("dx", 0, 4), ("dx", 0, 8), ("dx", 1, 2), ("dx", 1, 4)} <= seen, seen
 
 
 @gpu
@@ -1031,6 +1178,16 @@ def test_slices_of_one_tensor_are_apart(lib):
         a = _args(out=X + at)
         assert lib.moe_linear_workspace_size(ctypes.byref(c), ctypes.byref(a), ctypes.byref(n)) \
             == want
+
+
+def test_tiles_refuse_what_the_calls_refuse(lib):
+    c, t = _cfg(), B.moe_linear_tiles_t()
+    assert lib.moe_linear_tiles(c, _args(), None) == B.MOE_ERR_INVALID_ARG
+    assert lib.moe_linear_tiles(c, _args(ld_x=63), t) == B.MOE_ERR_INVALID_ARG
+    assert lib.moe_linear_backward_tiles(c, _grads(), t, None) == B.MOE_ERR_INVALID_ARG
+    assert lib.moe_linear_backward_tiles(c, _grads(dout=None), t, t) == B.MOE_ERR_INVALID_ARG
+    t.rows = 7
+    assert lib.moe_linear_tiles(_cfg(rows=0), _args(), t) == B.MOE_OK and t.rows == 0
 
 
 def test_linear_workspace(lib):
