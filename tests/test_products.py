@@ -601,6 +601,31 @@ def test_bias_gradient_alone(rows):
 
 
 @gpu
+@pytest.mark.parametrize("act", ["none", "gelu_tanh"])
+@pytest.mark.parametrize("sizes,cols", [([20000], 1024), ([20000], 1023),
+                                        ([9000, 0, 10877, 1, 129], 1024),
+                                        ([127, 16500, 128, 300], 1278)])
+def test_bias_gradient_of_many_rows(sizes, cols, act):
+    """Chunks of 128 rows: (rows / 128 + groups) x (columns / 256) >= 512."""
+    gen = torch.Generator().manual_seed(cols)
+    rows = sum(sizes) + 11
+    assert (rows // 128 + len(sizes)) * -(-cols // 256) >= 512
+    dout, x = normal(gen, torch.bfloat16, rows, cols), normal(gen, torch.bfloat16, rows, 24)
+    w = normal(gen, torch.bfloat16, len(sizes), 24, cols)
+    pre = normal(gen, torch.bfloat16, rows, cols) if act != "none" else None
+    off = offsets_of(sizes, 4)
+    dx, dw, db = B.grouped_linear_backward(dout, x, off, w, preact=pre, activation=act)
+    o = off.tolist()
+    for g in range(len(sizes)):
+        a, b = o[g], o[g + 1]
+        if a < b:
+            check_grads(dx[a:b], dw[g], db[g], dout[a:b], x[a:b], w[g],
+                        None if pre is None else pre[a:b], act)
+        else:
+            assert (db[g] == 0).all()
+
+
+@gpu
 def test_backward_calls_at_once():
     """Calls on two streams, their launches interleaved by two host threads,
     give the bits of calls one after another."""
@@ -964,6 +989,34 @@ def test_swiglu(rows, width, limit, scaled, dtype):
         close(dscale, s.grad, (2.0 ** -20 + (width / 32 + 16) * 2.0 ** -24) * sums, "dscale")
     else:
         assert dscale is None
+
+
+@gpu
+@pytest.mark.parametrize("dtype", list(SW_DT))
+@pytest.mark.parametrize("rows,width", [(1024, 256), (1500, 1280), (2051, 77), (4099, 8)])
+@pytest.mark.parametrize("limit,scaled", [(0.0, True), (1.5, True), (1.5, False)])
+def test_swiglu_many_rows(rows, width, limit, scaled, dtype):
+    """A warp per row from 1024 rows on."""
+    test_swiglu(rows, width, limit, scaled, dtype)
+
+
+@gpu
+@pytest.mark.parametrize("width", [72, 77])
+def test_swiglu_many_rows_of_no_group_and_in_place(width):
+    gen = torch.Generator().manual_seed(22)
+    gate, up, dout = (normal(gen, torch.float16, 1300, width) for _ in range(3))
+    scale, off = torch.rand(1300, generator=gen).cuda(), offsets_of([600, 0, 650], 20)
+    want, grads = B.swiglu(gate, up, scale), B.swiglu_backward(dout, gate, up, scale)
+    out, into = torch.full_like(gate, 3.0), [torch.full_like(gate, 3.0), torch.full_like(gate, 3.0),
+                                             torch.full((1300,), 3.0, device="cuda")]
+    B.swiglu(gate, up, scale, offsets=off, out=out)
+    B.swiglu_backward(dout, gate, up, scale, offsets=off, dgate=into[0], dup=into[1], dscale=into[2])
+    for t, ref in zip([out] + into, (want,) + grads):
+        assert (t[:20] == 3).all() and (t[1270:] == 3).all() and torch.equal(t[20:1270], ref[20:1270])
+    g2, u2, d2 = gate.clone(), up.clone(), dout.clone()
+    ds = B.swiglu_backward(d2, g2, u2, scale, dgate=g2, dup=d2)[2]
+    assert torch.equal(g2, grads[0]) and torch.equal(d2, grads[1]) and torch.equal(ds, grads[2])
+    assert torch.equal(B.swiglu(gate, up, scale, out=gate), want)
 
 
 @gpu
