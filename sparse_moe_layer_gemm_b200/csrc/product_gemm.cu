@@ -47,11 +47,15 @@ constexpr int kPipes = 2;     // pipelines of a CTA: a producer and an MMA warp 
 constexpr int kEpiWarps = 8;  // two per accumulator lane quadrant, on alternate chunks of rows
 constexpr int kThreads = 32 * (2 * kPipes + kEpiWarps);
 constexpr int kABytes = 2 * kSubBytes;
-constexpr int kMaxStages = 5;  // per pipeline
-// sub-slots of 64 contraction steps per slot: two where they leave room for
-// enough slots (32 rows 1280 -> 4096 6.8 us with two, 7.3 with one; 64 rows 4096 ->
-// 4096 in 4 parts 11.0 and 9.6)
-constexpr int subs_of(int bn) { return bn <= 32 ? 2 : 1; }
+constexpr int kMaxStages = 4;  // per pipeline: what 64 rows leave room for, the most of all
+// sub-slots of 64 contraction steps per slot: two up to 32 rows (32 rows 1280 ->
+// 4096 6.8 us with two, 7.3 with one; 64 rows 4096 -> 4096 in 4 parts 11.0 and 9.6)
+// where that leaves two slots, so that loads run below MMAs; else one (32 rows
+// 4096 -> 1280 in 8 parts 8.0 us with one slot of two, 7.5 with three of one; dw of
+// 8000 rows 64 x 72 10.5 and 9.3)
+constexpr int subs_of(int bn, size_t room, size_t sub) {
+  return bn <= 32 && room >= 4 * sub ? 2 : 1;
+}
 
 constexpr int kAhead = 2;  // residual chunks on their way
 // staging of the epilogue
@@ -440,10 +444,11 @@ cudaError_t product_cluster_room(int cluster, int* ctas) {
 size_t product_slots(int mode, ProductParams* p) {
   const size_t fixed = 1024 + static_cast<size_t>(epi_bytes(*p) + split_bytes(p->bn, p->split)) +
                        kBarBytes + static_cast<size_t>(group_table_bytes(p->groups));
-  p->subs = subs_of(p->bn);
-  const size_t slot = kPipes * p->subs * (kABytes + static_cast<size_t>(b_bytes(mode, p->bn)));
-  p->stages = static_cast<int>(
-      std::min<size_t>(kMaxStages, (static_cast<size_t>(227) * 1024 - fixed) / slot));
+  const size_t sub = kPipes * (kABytes + static_cast<size_t>(b_bytes(mode, p->bn)));
+  const size_t room = static_cast<size_t>(227) * 1024 - fixed;
+  p->subs = subs_of(p->bn, room, sub);
+  const size_t slot = p->subs * sub;
+  p->stages = static_cast<int>(std::min<size_t>(kMaxStages, room / slot));
   return p->stages < 1 || p->stages * slot < static_cast<size_t>(split_out_bytes(p->bn, p->split))
              ? 0
              : fixed + p->stages * slot;

@@ -553,6 +553,18 @@ def test_shared_tile_sizes_cover_every_share():
 
 
 @gpu
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,k,n", [(32, 4096, 1280), (1, 4096, 1280), (24, 4096, 1024),
+                                      (16, 8192, 128), (8000, 64, 72), (8192, 128, 128)])
+def test_two_slots_at_least(rows, k, n, residual):
+    """A pipeline loads a slot while its MMAs read another."""
+    x, w = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((rows, k), (k, n)))
+    more = x.new_empty(rows, n)
+    for t in tiles_of(x, w, residual=more if residual else None, dout=more):
+        assert t[4] >= 2, t
+
+
+@gpu
 @pytest.mark.parametrize("rows,k,n", [(2100, 1000, 2307), (1500, 1001, 2600), (2048, 520, 2314)])
 def test_linear_large_odd_rows(rows, k, n):
     """Pair tiles whose outputs, residual and pre-activation allow 2- and 4-byte
