@@ -718,9 +718,9 @@ struct Joined {
 // part + parts, ... below n_valid; row0 the tile's first output row, f0 the
 // warp's first feature.  zeros: the contraction was empty.  TWO: a second part
 // of the sum may lie `second` columns on (0: it does not).  EXTRA: with a
-// residual or the pre-activation.
+// residual or the pre-activation.  ACT: the activation may be one.
 // False if `join` gave up.
-template <int MODE, typename T, int ROWS, bool EXTRA, int AHEAD, bool TWO, typename Join>
+template <int MODE, typename T, int ROWS, bool EXTRA, bool ACT, int AHEAD, bool TWO, typename Join>
 __device__ __forceinline__ bool store_chunks(const ProductParams& p, uint32_t taddr,
                                              uint32_t second, int part, int parts, int n_valid,
                                              int64_t row0, int f0, int g, bool zeros, uint8_t* stg,
@@ -825,7 +825,7 @@ __device__ __forceinline__ bool store_chunks(const ProductParams& p, uint32_t ta
                                p.ld_preact, n, nf, p.width_preact, lane);
       __syncwarp();
     }
-    if (MODE == kProductForward) activate_all(v, p.act);
+    if (ACT) activate_all(v, p.act);
     if (EXTRA && p.residual != nullptr) {
       if (ring) cp_async_wait<AHEAD - 1>();
       __syncwarp();
@@ -853,15 +853,19 @@ __device__ __forceinline__ bool store_chunks(const ProductParams& p, uint32_t ta
   return true;
 }
 
-template <int MODE, typename T, int ROWS, int AHEAD, bool TWO, typename Join>
+// PLAIN: nothing follows the product but a bias.
+template <int MODE, typename T, int ROWS, int AHEAD, bool TWO, bool PLAIN, typename Join>
 __device__ __forceinline__ bool store_tile(const ProductParams& p, uint32_t taddr, uint32_t second,
                                            int part, int parts, int n_valid, int64_t row0, int f0,
                                            int g, bool zeros, uint8_t* stg, int lane, Join join) {
-  if (MODE == kProductForward && (p.preact != nullptr || p.residual != nullptr))
-    return store_chunks<MODE, T, 16, true, AHEAD, TWO>(p, taddr, second, part, parts, n_valid, row0,
-                                                       f0, g, zeros, stg, lane, join);
-  return store_chunks<MODE, T, ROWS, false, AHEAD, TWO>(p, taddr, second, part, parts, n_valid, row0,
-                                                        f0, g, zeros, stg, lane, join);
+  constexpr bool kMore = MODE == kProductForward && !PLAIN;
+  if constexpr (kMore) {
+    if (p.preact != nullptr || p.residual != nullptr)
+      return store_chunks<MODE, T, 16, true, true, AHEAD, TWO>(
+          p, taddr, second, part, parts, n_valid, row0, f0, g, zeros, stg, lane, join);
+  }
+  return store_chunks<MODE, T, ROWS, false, kMore, AHEAD, TWO>(
+      p, taddr, second, part, parts, n_valid, row0, f0, g, zeros, stg, lane, join);
 }
 
 }  // namespace product

@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the second pipeline's accumulator, if it had a part
       const uint32_t second = kb1 - kb0 > subs ? acc_cols : 0;
       if (split == 1) {
-        store_tile<MODE, T, 16, kAhead, true>(p, taddr, second, part, kEpiWarps / 4, t.n_valid, row0,
+        store_tile<MODE, T, 16, kAhead, true, false>(p, taddr, second, part, kEpiWarps / 4, t.n_valid, row0,
                                               t.f0 + q * 32, t.g, empty, stg, lane, Alone{});
         if (!empty) {
           tc_fence_before();
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // one tile per cluster in this form (the launch has a cluster per tile)
       split_send(x, taddr, second, q, part, empty, lane);
       // (the warp of the first features waits for all that is sent here as it joins)
-      if (!store_tile<MODE, T, 16, kAhead, true>(
+      if (!store_tile<MODE, T, 16, kAhead, true, false>(
               p, taddr + x.first(), second, part, kEpiWarps / 4, x.rows(rank), row0 + x.first(),
               t.f0 + q * 32, t.g, empty, stg, lane, Joined{x, q, lane, abort_flag, p.status, false}))
         split_settle(p, x);

@@ -458,14 +458,16 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kAccCols;
         if (SPLITS) {  // the launch has a cluster per tile
           split_send(x, taddr, 0, q, part, empty, lane);
-          const bool joined = store_tile<MODE, T, 16, kAheadSplit, false>(
+          const bool joined = store_tile<MODE, T, 16, kAheadSplit, false, false>(
               p, taddr + x.first(), 0, part, 2, x.rows(x.rank), row0 + x.first(), f0, t.g, empty, stg,
               lane, Joined{x, q, lane, abort_flag, p.status, false});
           if (!joined || f0 >= p.feats) split_settle(p, x);
           break;
         }
-        store_tile<MODE, T, 32, kAhead, false>(p, taddr, 0, part, 2, min(hn, t.n_valid - h * hn),
-                                               row0 + h * hn, f0, t.g, empty, stg, lane, Alone{});
+        // (two accumulators: choose() takes them for a bias at most)
+        store_tile<MODE, T, 32, kAhead, false, HALVES == 2>(
+            p, taddr, 0, part, 2, min(hn, t.n_valid - h * hn), row0 + h * hn, f0, t.g, empty, stg,
+            lane, Alone{});
         if (!empty) {
           tc_fence_before();
           __syncwarp();
@@ -533,8 +535,10 @@ cudaError_t launch_mode(const ProductMaps& m, const ProductParams& p, int grid, 
     }
     return cudaErrorInvalidConfiguration;
   }
-  return p.bn <= kAccCols ? launch<MODE, 1, T, false>(m, p, grid, st)
-                          : launch<MODE, 2, T, false>(m, p, grid, st);
+  if (p.bn <= kAccCols) return launch<MODE, 1, T, false>(m, p, grid, st);
+  if (p.act != MOE_ACT_NONE || p.residual != nullptr || p.preact != nullptr)
+    return cudaErrorInvalidConfiguration;
+  return launch<MODE, 2, T, false>(m, p, grid, st);
 }
 
 template <typename T>

@@ -393,6 +393,16 @@ def test_two_accumulators(rows, k, n, act):
 
 
 @gpu
+@pytest.mark.parametrize("rows,k,n", TWO + [(4096, 4096, 4096), (4096, 4096, 1280)])
+def test_one_accumulator_below_an_epilogue(rows, k, n):
+    """Tiles of two accumulators have no code for more than a bias."""
+    x, w = (torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in ((rows, k), (k, n)))
+    assert tiles_of(x, w, residual=x.new_empty(rows, n))[0][2] == 1
+    for act in ACTS[1:]:
+        assert tiles_of(x, w, act=act)[0][2] == 1
+
+
+@gpu
 @pytest.mark.parametrize("sizes,k,n", [([5000, 300, 70], 2600, 2600), ([3000, 0, 1, 900], 4104, 2312),
                                        ([0, 2500, 131, 2469], 2600, 2600)])
 def test_grouped_two_accumulators(sizes, k, n):
