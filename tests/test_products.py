@@ -1085,6 +1085,21 @@ def test_swiglu_clamp_edges_and_nan():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gelu_keeps_its_tail(dtype):
+    """gelu's relative error below zero, where 1 + erf would cancel: one rounding
+    to the type, and in fp32 2^-17: the polynomial 3.2e-7, the exponent 26 at most
+    with two roundings of 2^-24 and its constant's 2^-25 (26 * 2.5 * 2^-24 ln 2 =
+    2.7e-6), reciprocal, exponential and the polynomial's steps 2^-22 each."""
+    dt = DT[dtype]
+    z = -torch.linspace(2.0 ** -6, 6.0, 64 * 64).reshape(64, 64).to(dt).cuda()
+    out = B.linear(z, torch.eye(64, dtype=dt, device="cuda"), activation="gelu")
+    want = act64(z.double(), "gelu")
+    u, tiny = half_step(dt), torch.finfo(dt).tiny
+    close(out, want, (u * 1.01 + 2.0 ** -17) * want.abs() + tiny * u * 2, "gelu")
+
+
+@gpu
 def test_silu_far_below_zero():
     """Where 1 + exp(-z) passes 2^126 the reciprocal is no normal number, but silu
     is (-5e-37 at -88) and bf16 holds it."""
