@@ -32,10 +32,12 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // serialization is launched as the previous kernel of the stream retires its
 // CTAs, and runs its prologue (barriers, TMEM, tensor-map prefetch) while that
 // kernel's tail finishes; pdl_wait blocks until the previous kernel has
-// completed and its memory operations are visible.  (No kernel triggers its
-// dependents early: measured, an early trigger made the small kernels'
-// successors occupy SMs while they still ran.)  A no-op for a kernel launched
-// without the attribute.
+// completed and its memory operations are visible.  (The layer's kernels do not
+// trigger their dependents early: measured, an early trigger made the small
+// kernels' successors occupy SMs while they still ran.  The stand-alone
+// products, the bias gradient and SwiGLU do, see LaunchOrder in products.h; so
+// every kernel that may follow one in a stream waits here before it touches a
+// tensor.)  A no-op for a kernel launched without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------------------------------------------------------- mbarrier

@@ -47,9 +47,15 @@ inline FastDiv fast_div(uint32_t d) {
 //
 // The kernels of one backward call run one after another, but some do not need
 // the one before: dw runs beside dx, the bias gradient beside both.  Such a
-// kernel (late_wait) starts when its predecessor does, so that what came before
-// the predecessor is complete, and waits for it only before it ends, so that
-// what follows it in the stream follows both.
+// kernel (late_wait) does not wait for what it reads: the row pass's dz, copies
+// and partial sums.  It relies on the call's first product, which precedes it in
+// the stream and lets it start only after all of its own CTAs have waited for
+// the row pass to complete with its memory visible (pdl_wait before
+// pdl_trigger); a kernel of another host thread's call that comes between them
+// in the stream either waits itself or was let start by one that did.  So a
+// call's first product is never late_wait.  Such a kernel waits for its
+// predecessor only before it ends, so that what follows it in the stream follows
+// both.
 struct LaunchOrder {
   bool late_wait;
 };
