@@ -77,12 +77,13 @@ __device__ __forceinline__ float exp2_fast(float v) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 / (1 + exp(-z)); an exponential of infinity (z < -88.7) gives 0.  A quarter
+// 4 / (1 + exp(-z)); an exponential of infinity (z < -88.7) gives 0.  A quarter
 // of the sum is inverted, since rcp gives 0 for what passes 2^126 (z < -87.3)
 // and silu and its slope are normal numbers there.
-__device__ __forceinline__ float sigmoid(float z) {
-  return 0.25f * reciprocal(fmaf(0.25f, exp2_fast(-kLog2e * z), 0.25f));
+__device__ __forceinline__ float sigmoid_times_4(float z) {
+  return reciprocal(fmaf(0.25f, exp2_fast(-kLog2e * z), 0.25f));
 }
+__device__ __forceinline__ float sigmoid(float z) { return 0.25f * sigmoid_times_4(z); }
 
 // Phi(z), and exp(-z^2 / 2)
 __device__ __forceinline__ float normal_cdf(float z, float* e) {

@@ -39,11 +39,11 @@ struct alignas(sizeof(T) * V) Pack {
   T v[V];
 };
 
-// fp32 rows take the exact division and exponential.
+// 4 sigmoid(x); fp32 rows take the exact division and exponential.
 template <typename T>
-__device__ __forceinline__ float sigmoid_of(float x) { return sigmoid(x); }
+__device__ __forceinline__ float sigmoid4_of(float x) { return sigmoid_times_4(x); }
 template <>
-__device__ __forceinline__ float sigmoid_of<float>(float x) { return 1.0f / (1.0f + expf(-x)); }
+__device__ __forceinline__ float sigmoid4_of<float>(float x) { return 4.0f / (1.0f + expf(-x)); }
 
 // NaN passes the clamps, as it passes the plain formula.
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 6) swiglu_kernel(const 
               a = min_nan(a, L);
               b = max_nan(min_nan(b, L), -L);
             }
-            o.v[i] = from_f32<T>(s * b * (a * sigmoid_of<T>(a)));
+            o.v[i] = from_f32<T>(s * b * (0.25f * a * sigmoid4_of<T>(a)));
           }
           *reinterpret_cast<Pack<T, V>*>(out + c0 + k * kStep) = o;
         }
@@ -154,12 +154,12 @@ __global__ void __launch_bounds__(kThreads, V == 1 ? 3 : 6) swiglu_backward_kern
               a = min_nan(gf, L);
               b = max_nan(min_nan(uf, L), -L);
             }
-            const float sg = sigmoid_of<T>(a);
-            const float silu = a * sg;
-            const float ds = df * s, db = df * b;
-            acc = fmaf(db, silu, acc);
-            float dgv = ds * b * sg * fmaf(a, 1.0f - sg, 1.0f);
-            float duv = ds * silu;
+            const float sg = 0.25f * sigmoid4_of<T>(a);
+            const float dsg = df * sg;
+            const float dsilu = dsg * a;
+            acc = fmaf(dsilu, b, acc);
+            float dgv = dsg * s * b * fmaf(a, 1.0f - sg, 1.0f);
+            float duv = dsilu * s;
             if (CLAMP) {
               dgv = gf > L ? 0.f : dgv;
               duv = fabsf(uf) > L ? 0.f : duv;
