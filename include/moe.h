@@ -478,13 +478,14 @@ void moe_dense_destroy(moe_dense_t* layer);
  * weights cost nothing.
  *
  * Arithmetic: 16-bit operands, products and sums in fp32 on the tensor cores
- * (each 16 products added drop at most 2^-23 of the sum of magnitudes: it shows
- * in dW of millions of rows), bias, activation and residual in fp32, one rounding to the output type.  dz
- * is rounded to the operand type where it enters the products (not where
- * dbias sums it): one rounding more in dx and dW, by half a step of |dz|, and
- * in fp16 by 2^-24 at most below 2^-13 (its range is that of 2 x 65504, so dz
- * past 65504 stays finite); dbias is summed in fp32.  Every sum has a fixed order: the
- * same call gives the same bits.
+ * (each 16 products added drop at most 2^-23 of the sum of magnitudes: it
+ * shows in dW of millions of rows), bias, activation and residual in fp32,
+ * one rounding to the output type.  dz is rounded to the operand type where
+ * it enters the products (not where dbias sums it): one rounding more in dx
+ * and dW, by half a step of |dz|, and in fp16 by 2^-24 at most below 2^-13
+ * (its range is that of 2 x 65504, so dz past 65504 stays finite); dbias is
+ * summed in fp32.  Every sum has a fixed order: the same call gives the same
+ * bits.
  *
  * offsets [G + 1] (device, int32) as moe_routing_t's: non-decreasing, within
  * [0, rows].  Empty groups are allowed: their dW and dbias are zero.  Rows
